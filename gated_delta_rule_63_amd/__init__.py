@@ -16,7 +16,8 @@ import torch
 
 from ._lib import KDA_BF16, KDA_F32, KERNELS, Desc, KDAError, Layout, lib, status_string  # noqa: F401
 
-__all__ = ["fwd", "gdn_fwd", "fwd_noalloc", "noalloc_max_workspace", "fwd_workspace_size", "kernel_workspace_size", "decode_step", "fwd_staged", "Staged", "KDAError", "status_string", "version"]
+__all__ = ["fwd", "gdn_fwd", "fwd_noalloc", "noalloc_max_workspace", "fwd_workspace_size", "kernel_workspace_size", "decode_step", "fwd_staged", "Staged", "KDAError", "status_string", "version",
+           "bwd", "gdn_bwd", "bwd_workspace_size"]
 
 D = 128
 
@@ -285,3 +286,6 @@ def fwd_staged(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_fin
     if rc != 0:
         raise KDAError(rc, "kda_fwd_staged")
     return o, hT, st
+
+
+from ._ops import bwd, bwd_workspace_size, gdn_bwd  # noqa: E402

@@ -19,7 +19,8 @@ EXPORTS = ["kda_status_string", "kda_version", "kda_fwd_check", "kda_fwd", "kda_
            "kda_fwd_noalloc_max_workspace",
            "kda_decode_step", "kda_staged_layout",
            "kda_staged_workspace_size", "kda_stage_chunk_map", "kda_stage_gate_scan", "kda_stage_intra",
-           "kda_stage_recurrence", "kda_stage_output", "kda_fwd_staged"]
+           "kda_stage_recurrence", "kda_stage_output", "kda_fwd_staged",
+           "kda_bwd", "kda_gdn_bwd", "kda_bwd_workspace_size"]
 
 
 class Desc(ctypes.Structure):
@@ -85,6 +86,12 @@ def lib():
             fn.restype = ctypes.c_int
         L.kda_fwd_staged.argtypes = [P] * 9 + [D, P]
         L.kda_fwd_staged.restype = ctypes.c_int
+        for name in ("kda_bwd", "kda_gdn_bwd"):
+            fn = getattr(L, name)
+            fn.argtypes = [P] * 15 + [D, P]
+            fn.restype = ctypes.c_int
+        L.kda_bwd_workspace_size.argtypes = [D]
+        L.kda_bwd_workspace_size.restype = ctypes.c_size_t
         _lib = L
     return _lib
 

@@ -1,0 +1,740 @@
+// kda_bwd.hip -- the gradient of the chunked gated delta rule (KDA and, with a
+// scalar gate, Gated DeltaNet) for gfx950.
+//
+// Chunks of 32 tokens, G the in-chunk cumulative gate, all decays as
+// differences of G (never above 1 once combined):
+//   kr = k e^G, qr = q e^G, ki = k e^-G, kc = k e^(G_last - G)
+//   B_ts = kr_t . ki_s (s < t),  M_ts = qr_t . ki_s (s <= t),  b = beta
+//   X = -B (I + Diag(b) B)^-1       so that (I + B Diag(b))^-1 = I + X Diag(b)
+//   e = (I + X b)(v - kr S) = U - W S,  W = kr + X b kr,  U = v + X b v
+//   S' = e^G_last S + kc^T (b e),   o = qr S + M (b e)
+// and backwards, from do and the gradient dS' of the leaving state:
+//   dD = M^T do + kc dS',  rho = dD + X^T (b dD),  r = b rho
+//   dv = r,  dbeta = e . rho,  dM_ts = b_s do_t . e_s,  dB_ts = -b_t b_s rho_t . e_s
+//   dS = e^G_last dS' + qr^T do - W^T (b dD)
+//   dq = e^G (do S^T) + sum_s dM_ts k_s e^(G_t - G_s)
+//   dk = row + col,  row = -e^G (r S^T) + sum_s dB_ts k_s e^(G_t - G_s)
+//   col_s = sum_t (dM_ts q_t + dB_ts k_t) e^(G_t - G_s) + carry_s,
+//   carry_s = e^(G_last - G_s) (b_s e_s dS'^T)
+//   dG = q dq + k (row - col),  dg_t = sum_(u >= t) dG_u + sum_s k_s carry_s
+//        + rowsum(e^G_last S dS')
+// The form with X divides by no beta, so beta = 0 is an ordinary value.
+//
+// Four kernels. Only the two state walks are sequential, and both split over
+// the columns of V, which the recurrence never mixes:
+//   1 intra   per (chunk, head): X, W, U, M^T do, kc, qr
+//   2 states  per (sequence, head, V-block), forwards: S, e
+//   3 dstates per (sequence, head, V-block), backwards: dS, dD
+//   4 grads   per (chunk, head): everything else
+// All products run on the fp32 matrix instruction (16x16x4): gradients of fp32
+// leaves (g, beta, the states) come out with fp32 accuracy, and dg is a sum of
+// differences that cancel, where 16-bit operands would leave an error of 1e-3.
+//
+// Gates inside a chunk: two sub-blocks of 16 tokens, each with its own
+// cumulative sum L and its value m after 8 tokens; E1 = e^(L - m) and
+// 1 / E1 stay within e^+-40 for g >= -5. A product within a sub-block pairs
+// E1 with 1 / E1; from sub-block 0 to 1 the same factors are scaled by
+// cs = e^(m_1 + G_0 - m_0) per channel.
+#include "kda_bwd.h"
+#include "kda_device.h"
+
+namespace kda {
+namespace bwd {
+
+constexpr int C = kBwdChunk;
+constexpr int LD = 132;      // LDS row of 128 channels, 16-byte aligned rows
+constexpr int LM = 36;       // LDS row of 32 tokens
+
+__device__ __forceinline__ f32x4 splat(float x) { return f32x4{x, x, x, x}; }
+__device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+__device__ __forceinline__ void st4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+
+// acc += A B over 16 reduction indices: lane l holds A[l % 16][4 (l / 16) + j]
+// and B[4 (l / 16) + j][l % 16] in component j.
+__device__ __forceinline__ f32x4 mma(const f32x4& a, const f32x4& b, f32x4 acc) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = mfma16x4(a[j], b[j], acc);
+    return acc;
+}
+
+struct Chunk {
+    int n, nv;               // sequence, valid tokens (<= 0: no chunk)
+    long long tok;           // first token, counted over the batch
+};
+
+// Offsets are clamped to [0, T], so that no offset leads outside the tensors.
+__device__ __forceinline__ void seq_range(const BwdArgs& a, int n, int& t0, int& t1) {
+    t0 = min(max(a.cu[n], 0), a.T);
+    t1 = min(max(a.cu[n + 1], t0), a.T);
+}
+
+__device__ __forceinline__ Chunk find_chunk(const BwdArgs& a, int slot) {
+    Chunk r;
+    if (!a.cu) {
+        const int nc = (a.T + C - 1) / C;
+        r.n = slot / nc;
+        const int t0 = (slot - r.n * nc) * C;
+        r.nv = min(C, a.T - t0);
+        r.tok = (long long)r.n * a.T + t0;
+        return r;
+    }
+    int lo = 0, hi = a.N;    // the last n with floor(cu[n] / 32) + n <= slot
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (min(max(a.cu[mid], 0), a.T) / C + mid <= slot) lo = mid;
+        else hi = mid;
+    }
+    r.n = lo;
+    r.nv = 0;
+    r.tok = 0;
+    if (a.N > 0) {
+        int t0, t1;
+        seq_range(a, lo, t0, t1);
+        const int c = slot - (t0 / C + lo);
+        if (c >= 0) {
+            r.tok = t0 + (long long)c * C;
+            r.nv = (int)min((long long)C, t1 - r.tok);
+        }
+    }
+    return r;
+}
+
+// The gates of 16 tokens of one channel: this lane's half of the chunk.
+struct Gates {
+    float L[16];             // cumulative within the sub-block
+    float m, G0, G1, m0, m1; // its value after 8 tokens; the sub-blocks' totals and midpoints
+};
+
+template <bool F32>
+__device__ __forceinline__ void load_gates(Gates& s, const BwdArgs& a, const Chunk& ck, int h, int c, int half) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int t = 16 * half + i;
+        const long long th = (ck.tok + t) * a.H + h;
+        s.L[i] = t < ck.nv ? (a.scalar_gate ? a.g[th] : a.g[th * D + c]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s.L[i] += s.L[i - 1];
+    s.m = s.L[7];
+    const float other = __shfl_xor(s.L[15], 32), mo = __shfl_xor(s.m, 32);
+    s.G0 = half ? other : s.L[15];
+    s.G1 = half ? s.L[15] : other;
+    s.m0 = half ? mo : s.m;
+    s.m1 = half ? s.m : mo;
+}
+
+// ------------------------------------------------------------------ 1 intra
+template <bool F32>
+__global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
+    const long long ch = blockIdx.x;
+    const int slot = (int)(ch / a.H), h = (int)(ch % a.H);
+    const Chunk ck = find_chunk(a, slot);
+    if (ck.nv <= 0) return;
+    __shared__ __align__(16) float Kd[C * LD], KQ[2 * C * LD];
+    float *const Ki = KQ, *const Qd = KQ + C * LD;
+    __shared__ __align__(16) float Bs[C * LM], Ms[C * LM], Xs[C * LM];
+    __shared__ __align__(16) float cs[D], sc[2][D], bs[C];
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    if (tid < C) {
+        const float b = tid < ck.nv ? a.beta[(ck.tok + tid) * a.H + h] : 0.f;
+        bs[tid] = b;
+        a.b[ch * C + tid] = b;
+    }
+    {
+        // wave w owns channels 32 w .. 32 w + 31, one lane per channel and half chunk
+        const int c = 32 * w + (l & 31), half = l >> 5;
+        Gates s;
+        load_gates<F32>(s, a, ck, h, c, half);
+        const float up = expf(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
+        const float dn = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
+        sc[half][c] = up;
+        if (half == 0) {
+            cs[c] = expf(s.m1 + s.G0 - s.m0);
+            a.decay[ch * D + c] = expf(s.G0 + s.G1);
+        }
+        f32x4 kc[4], qr[4];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = 16 * half + i;
+            const long long at = ((ck.tok + t) * a.H + h) * D + c;
+            const float kk = t < ck.nv ? ld_in<F32>(a.k, at) : 0.f;
+            const float qq = t < ck.nv ? ld_in<F32>(a.q, at) : 0.f;
+            const float E1 = expf(s.L[i] - s.m), E2 = expf(s.m - s.L[i]);
+            Kd[t * LD + c] = kk * E1;
+            Ki[t * LD + c] = kk * E2;
+            Qd[t * LD + c] = qq * E1;
+            kc[i >> 2][i & 3] = kk * E2 * dn;
+            qr[i >> 2][i & 3] = qq * E1 * up;
+        }
+        const long long o = (ch * D + c) * C + 16 * half;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            st4(a.KcT + o + 4 * i, kc[i]);
+            st4(a.QrT + o + 4 * i, qr[i]);
+        }
+    }
+    __syncthreads();
+    // B and M, each wave over its own 32 channels: tiles (0,0), (1,1), (1,0)
+    f32x4 pb[3], pm[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) pb[i] = pm[i] = splat(0.f);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+        const int c = 32 * w + 16 * kb + g4;
+        const f32x4 kd0 = ld4(Kd + r16 * LD + c), kd1 = ld4(Kd + (16 + r16) * LD + c);
+        const f32x4 qd0 = ld4(Qd + r16 * LD + c), qd1 = ld4(Qd + (16 + r16) * LD + c);
+        const f32x4 ki0 = ld4(Ki + r16 * LD + c), ki1 = ld4(Ki + (16 + r16) * LD + c);
+        const f32x4 x = ld4(cs + c);
+        pb[0] = mma(kd0, ki0, pb[0]);
+        pb[1] = mma(kd1, ki1, pb[1]);
+        pb[2] = mma(kd1 * x, ki0, pb[2]);
+        pm[0] = mma(qd0, ki0, pm[0]);
+        pm[1] = mma(qd1, ki1, pm[1]);
+        pm[2] = mma(qd1 * x, ki0, pm[2]);
+    }
+    __syncthreads();         // the partial tiles take the place of Ki and Qd
+    float* const P = KQ;     // [wave][6][64][4]: 24 of the 33 KiB
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        st4(P + ((w * 6 + i) * 64 + l) * 4, pb[i]);
+        st4(P + ((w * 6 + 3 + i) * 64 + l) * 4, pm[i]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        float x = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) x += P[(u * 6 + i) * 256 + tid];
+        const int tile = i % 3, lane = tid >> 2;
+        const int row = 4 * (lane >> 4) + (tid & 3), col = lane & 15;
+        const int t = row + (tile ? 16 : 0), s = col + (tile == 1 ? 16 : 0);
+        if (i < 3) Bs[t * LM + s] = t > s ? x : 0.f;
+        else Ms[t * LM + s] = t >= s ? x : 0.f;
+    }
+    __syncthreads();
+    if (w == 0) {
+        // X of the two diagonal blocks by substitution, one lane per column:
+        // X_ts = -B_ts - sum_(s < u < t) B_tu b_u X_us
+        const int blk = (l >> 4) & 1, o = 16 * blk;
+        float y[16];
+#pragma unroll
+        for (int t = 0; t < 16; ++t) {
+            float x = -Bs[(o + t) * LM + o + r16];
+#pragma unroll
+            for (int u = 0; u < t; ++u) x -= Bs[(o + t) * LM + o + u] * y[u];
+            x = t > r16 ? x : 0.f;
+            y[t] = bs[o + t] * x;
+            if (l < 32) {
+                Xs[(o + t) * LM + o + r16] = x;
+                if (blk) Xs[t * LM + 16 + r16] = 0.f;
+            }
+        }
+    }
+    __syncthreads();
+    if (w == 0) {
+        // X_10 = -(I + X_11 b_1) B_10 (I + b_0 X_00)
+        f32x4 y, x00;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[j] = Bs[(16 + g4 + j) * LM + r16];
+            x00[j] = Xs[(g4 + j) * LM + r16];
+        }
+        y = mma(ld4(Bs + (16 + r16) * LM + g4) * ld4(bs + g4), x00, y);
+        const f32x4 x10 = mma(ld4(Xs + (16 + r16) * LM + 16 + g4) * ld4(bs + 16 + g4), y, y);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) Xs[(16 + g4 + j) * LM + r16] = -x10[j];
+    }
+    __syncthreads();
+    {
+        const int i = 4 * tid;
+        st4(a.X + ch * (C * C) + i, ld4(Xs + (i >> 5) * LM + (i & 31)));
+    }
+    // W, U, M^T do: each wave its own 32 columns
+    const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
+    const f32x4 x00 = ld4(Xs + r16 * LM + g4) * b0, x10 = ld4(Xs + (16 + r16) * LM + g4) * b0,
+                x11 = ld4(Xs + (16 + r16) * LM + 16 + g4) * b1;
+    f32x4 m00, m10, m11;     // transposed
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        m00[j] = Ms[(g4 + j) * LM + r16];
+        m10[j] = Ms[(16 + g4 + j) * LM + r16];
+        m11[j] = Ms[(16 + g4 + j) * LM + 16 + r16];
+    }
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+        const int col = 32 * w + 16 * ct + r16;
+        f32x4 f0, f1, v0, v1, d0, d1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t0 = g4 + j, t1 = 16 + t0;
+            const long long at = ((ck.tok + t0) * a.H + h) * D + col, at1 = at + (long long)16 * a.H * D;
+            v0[j] = t0 < ck.nv ? ld_in<F32>(a.v, at) : 0.f;
+            v1[j] = t1 < ck.nv ? ld_in<F32>(a.v, at1) : 0.f;
+            d0[j] = t0 < ck.nv ? a.d_o[at] : 0.f;
+            d1[j] = t1 < ck.nv ? a.d_o[at1] : 0.f;
+            f0[j] = Kd[t0 * LD + col] * sc[0][col];
+            f1[j] = Kd[t1 * LD + col] * sc[1][col];
+        }
+        const long long o = (ch * D + col) * C + g4;
+        st4(a.WT + o, mma(x00, f0, f0));
+        st4(a.WT + o + 16, mma(x11, f1, mma(x10, f0, f1)));
+        st4(a.eT + o, mma(x00, v0, v0));
+        st4(a.eT + o + 16, mma(x11, v1, mma(x10, v0, v1)));
+        st4(a.dDT + o, mma(m10, d1, mma(m00, d0, splat(0.f))));
+        st4(a.dDT + o + 16, mma(m11, d1, splat(0.f)));
+    }
+}
+
+// ----------------------------------------------------- 2 states, 3 dstates
+// One workgroup per (sequence, head, 16 NV columns of V). Wave w holds rows
+// 32 w .. 32 w + 31 of the state as accumulators (row = channel k, column =
+// v); as such they are also the right operand of the product with W (or kc),
+// of which each wave forms the part of its own channels. The parts meet in
+// LDS, and every wave sums them into the operand of the state's update: one
+// barrier a chunk. A chain's V-blocks run on one XCD, whose L2 serves W, kc
+// and qr to all of them.
+struct Walk {
+    int n, h, v0, first, nc;
+    long long tok;
+    bool on;
+};
+
+template <int NV>
+__device__ __forceinline__ Walk find_walk(const BwdArgs& a) {
+    constexpr int nb = D / (16 * NV);
+    Walk r;
+    const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int chain = (i / nb) * 8 + xcd;
+    r.on = chain < a.N * a.H;
+    r.v0 = (i % nb) * 16 * NV;
+    r.n = r.on ? chain / a.H : 0;
+    r.h = chain - r.n * a.H;
+    int t0 = 0, t1 = a.T;
+    if (r.on && a.cu) seq_range(a, r.n, t0, t1);
+    r.nc = (t1 - t0 + C - 1) / C;
+    r.first = a.cu ? t0 / C + r.n : r.n * r.nc;
+    r.tok = a.cu ? t0 : (long long)r.n * a.T;
+    return r;
+}
+
+template <int NV>
+__global__ __launch_bounds__(256) void kda_bwd_states(BwdArgs a) {
+    const Walk wk = find_walk<NV>(a);
+    if (!wk.on) return;
+    __shared__ __align__(16) float P[2][4][2 * NV][64][4];
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    f32x4 S[2][NV];
+    const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                S[kt][nv][j] = a.h0 ? a.h0[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
+    for (int c = 0; c < wk.nc; ++c) {
+        const long long ch = (long long)(wk.first + c) * a.H + wk.h;
+        f32x4 W[2][2], Kc[2][2], dec[2], b[2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            const int k0 = 32 * w + 16 * kt;
+            dec[kt] = ld4(a.decay + ch * D + k0 + g4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) W[i][kt][j] = a.WT[(ch * D + k0 + g4 + j) * C + 16 * i + r16];
+                Kc[i][kt] = ld4(a.KcT + (ch * D + k0 + r16) * C + 16 * i + g4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b[i] = ld4(a.b + ch * C + 16 * i + g4);
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+                st4(a.S + ch * (D * D) + (wk.v0 + 16 * nv + r16) * D + 32 * w + 16 * kt + g4, S[kt][nv]);
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            f32x4 p = mma(W[i][1], S[1][nv], mma(W[i][0], S[0][nv], splat(0.f)));
+            if ((tile & 3) == w) p -= ld4(a.eT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4);
+            st4(P[c & 1][w][tile][l], p);
+        }
+        __syncthreads();
+        f32x4 e[2][NV];
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            const f32x4 x = -(ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) +
+                              ld4(P[c & 1][2][tile][l]) + ld4(P[c & 1][3][tile][l]));
+            if ((tile & 3) == w) st4(a.eT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4, x);
+            e[i][nv] = x * b[i];
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+                S[kt][nv] = mma(Kc[1][kt], e[1][nv], mma(Kc[0][kt], e[0][nv], S[kt][nv] * dec[kt]));
+    }
+}
+
+template <int NV>
+__global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
+    const Walk wk = find_walk<NV>(a);
+    if (!wk.on) return;
+    __shared__ __align__(16) float P[2][4][2 * NV][64][4];
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    f32x4 S[2][NV];
+    const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
+    int T1 = a.T;            // the sequence's length
+    if (a.cu) {
+        int t0;
+        seq_range(a, wk.n, t0, T1);
+        T1 -= t0;
+    }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                S[kt][nv][j] = a.dhT ? a.dhT[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
+    for (int c = wk.nc - 1; c >= 0; --c) {
+        const long long ch = (long long)(wk.first + c) * a.H + wk.h;
+        f32x4 W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], d_o[2][NV];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            const int k0 = 32 * w + 16 * kt;
+            dec[kt] = ld4(a.decay + ch * D + k0 + g4);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) Kc[i][kt][j] = a.KcT[(ch * D + k0 + g4 + j) * C + 16 * i + r16];
+                W[i][kt] = ld4(a.WT + (ch * D + k0 + r16) * C + 16 * i + g4);
+                Qr[i][kt] = ld4(a.QrT + (ch * D + k0 + r16) * C + 16 * i + g4);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            b[i] = ld4(a.b + ch * C + 16 * i + g4);
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int t = c * C + 16 * i + g4 + j;
+                    d_o[i][nv][j] = t < T1 ? a.d_o[((wk.tok + t) * a.H + wk.h) * D + wk.v0 + 16 * nv + r16] : 0.f;
+                }
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+                st4(a.dS + ch * (D * D) + (wk.v0 + 16 * nv + r16) * D + 32 * w + 16 * kt + g4, S[kt][nv]);
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            f32x4 p = mma(Kc[i][1], S[1][nv], mma(Kc[i][0], S[0][nv], splat(0.f)));
+            if ((tile & 3) == w) p += ld4(a.dDT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4);
+            st4(P[c & 1][w][tile][l], p);
+        }
+        __syncthreads();
+        f32x4 dd[2][NV];
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            const f32x4 x = ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) + ld4(P[c & 1][2][tile][l]) +
+                            ld4(P[c & 1][3][tile][l]);
+            if ((tile & 3) == w) st4(a.dDT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4, x);
+            dd[i][nv] = -(x * b[i]);
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv) {
+                f32x4 x = S[kt][nv] * dec[kt];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x = mma(W[i][kt], dd[i][nv], mma(Qr[i][kt], d_o[i][nv], x));
+                S[kt][nv] = x;
+            }
+    }
+    if (a.dh0)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    a.dh0[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] = S[kt][nv][j];
+}
+
+// ------------------------------------------------------------------ 4 grads
+template <bool F32>
+__device__ __forceinline__ void st_out(void* p, long long i, float x) {
+    if constexpr (F32) static_cast<float*>(p)[i] = x;
+    else static_cast<__bf16*>(p)[i] = (__bf16)x;   // the gradient of a bf16 tensor: rounded once, here
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
+    const long long ch = blockIdx.x;
+    const int slot = (int)(ch / a.H), h = (int)(ch % a.H);
+    const Chunk ck = find_chunk(a, slot);
+    if (ck.nv <= 0) return;
+    // first do, rho, e as [token][v]; then E1, k, q as [token][k]
+    __shared__ __align__(16) float R0[C * LD], R1[C * LD], R2[C * LD];
+    __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM];
+    __shared__ __align__(16) float up[2][D], dn[2][D], cs[D], dec[D], bs[C], part[4][C];
+    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    if (tid < C) bs[tid] = a.b[ch * C + tid];
+    st4(Xs + (tid >> 3) * LM + 4 * (tid & 7), ld4(a.X + ch * (C * C) + 4 * tid));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int t = (tid >> 5) + 8 * i, c = 4 * (tid & 31);
+        f32x4 x = splat(0.f);
+        const long long at = ((ck.tok + t) * a.H + h) * D + c;
+        if (t < ck.nv) x = ld4(a.d_o + at);
+        st4(R0 + t * LD + c, x);
+    }
+    __syncthreads();
+    const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
+    {
+        f32x4 x00, x10, x11; // transposed
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            x00[j] = Xs[(g4 + j) * LM + r16];
+            x10[j] = Xs[(16 + g4 + j) * LM + r16];
+            x11[j] = Xs[(16 + g4 + j) * LM + 16 + r16];
+        }
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            const int col = 32 * w + 16 * ct + r16;
+            const long long o = (ch * D + col) * C + g4;
+            const f32x4 d0 = ld4(a.dDT + o), d1 = ld4(a.dDT + o + 16);
+            const f32x4 e0 = ld4(a.eT + o), e1 = ld4(a.eT + o + 16);
+            const f32x4 p0 = mma(x10, d1 * b1, mma(x00, d0 * b0, d0)), p1 = mma(x11, d1 * b1, d1);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t0 = g4 + j, t1 = 16 + t0;
+                R1[t0 * LD + col] = p0[j];
+                R1[t1 * LD + col] = p1[j];
+                R2[t0 * LD + col] = e0[j];
+                R2[t1 * LD + col] = e1[j];
+                const long long at = ((ck.tok + t0) * a.H + h) * D + col;
+                if (t0 < ck.nv) st_out<F32>(a.dv, at, b0[j] * p0[j]);
+                if (t1 < ck.nv) st_out<F32>(a.dv, at + (long long)16 * a.H * D, b1[j] * p1[j]);
+            }
+        }
+    }
+    __syncthreads();
+    // dM, dB and dbeta from do e^T and rho e^T: tiles (0,0), (1,1), (1,0) of each
+    for (int i = w; i < 6; i += 4) {
+        const int tile = i % 3, ro = tile ? 16 : 0, co = tile == 1 ? 16 : 0;
+        const float* A = i < 3 ? R0 : R1;
+        f32x4 x = splat(0.f);
+#pragma unroll
+        for (int vb = 0; vb < 8; ++vb)
+            x = mma(ld4(A + (ro + r16) * LD + 16 * vb + g4), ld4(R2 + (co + r16) * LD + 16 * vb + g4), x);
+        const int s = co + r16;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int t = ro + g4 + j;
+            if (i < 3) {
+                dMs[t * LM + s] = t >= s ? bs[s] * x[j] : 0.f;
+            } else {
+                dBs[t * LM + s] = t > s ? -bs[t] * bs[s] * x[j] : 0.f;
+                if (t == s && t < ck.nv) a.dbeta[(ck.tok + t) * a.H + h] = x[j];
+            }
+        }
+    }
+    // products with the states: each wave its own 32 channels
+    f32x4 qS[2][2], rS[2][2], eS[2][2];
+    float sd[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) qS[i][kt] = rS[i][kt] = eS[i][kt] = splat(0.f);
+    const float* Sp = a.S + ch * (D * D) + g4 * D + 32 * w + r16;
+    const float* dSp = a.dS + ch * (D * D) + g4 * D + 32 * w + r16;
+#pragma unroll 2
+    for (int vb = 0; vb < 8; ++vb) {
+        f32x4 s[2], ds[2];
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                s[kt][j] = Sp[(16 * vb + j) * D + 16 * kt];
+                ds[kt][j] = dSp[(16 * vb + j) * D + 16 * kt];
+            }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sd[kt] += s[kt][j] * ds[kt][j];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int o = (16 * i + r16) * LD + 16 * vb + g4;
+            const f32x4 x = ld4(R0 + o), y = ld4(R1 + o), z = ld4(R2 + o);
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt) {
+                qS[i][kt] = mma(x, s[kt], qS[i][kt]);
+                rS[i][kt] = mma(y, s[kt], rS[i][kt]);
+                eS[i][kt] = mma(z, ds[kt], eS[i][kt]);
+            }
+        }
+    }
+    __syncthreads();
+    {
+        const int c = 32 * w + (l & 31), half = l >> 5;
+        Gates s;
+        load_gates<F32>(s, a, ck, h, c, half);
+        up[half][c] = expf(s.m + (half ? s.G0 : 0.f));
+        dn[half][c] = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
+        if (half == 0) {
+            cs[c] = expf(s.m1 + s.G0 - s.m0);
+            dec[c] = expf(s.G0 + s.G1);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int t = 16 * half + i;
+            const long long at = ((ck.tok + t) * a.H + h) * D + c;
+            R0[t * LD + c] = expf(s.L[i] - s.m);
+            R1[t * LD + c] = t < ck.nv ? ld_in<F32>(a.k, at) : 0.f;
+            R2[t * LD + c] = t < ck.nv ? ld_in<F32>(a.q, at) : 0.f;
+        }
+    }
+    __syncthreads();
+    const f32x4 M00 = ld4(dMs + r16 * LM + g4), M10 = ld4(dMs + (16 + r16) * LM + g4),
+                M11 = ld4(dMs + (16 + r16) * LM + 16 + g4);
+    const f32x4 N00 = ld4(dBs + r16 * LM + g4), N10 = ld4(dBs + (16 + r16) * LM + g4),
+                N11 = ld4(dBs + (16 + r16) * LM + 16 + g4);
+    f32x4 M00t, M10t, M11t, N00t, N10t, N11t;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        M00t[j] = dMs[(g4 + j) * LM + r16];
+        M10t[j] = dMs[(16 + g4 + j) * LM + r16];
+        M11t[j] = dMs[(16 + g4 + j) * LM + 16 + r16];
+        N00t[j] = dBs[(g4 + j) * LM + r16];
+        N10t[j] = dBs[(16 + g4 + j) * LM + r16];
+        N11t[j] = dBs[(16 + g4 + j) * LM + 16 + r16];
+    }
+    f32x4 dgs[2] = {splat(0.f), splat(0.f)};   // scalar gate: this lane's channels summed
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct) {
+        const int col = 32 * w + 16 * ct + r16;
+        f32x4 E1[2], E2[2], kk[2], qq[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int o = (16 * i + g4 + j) * LD + col;
+                E1[i][j] = R0[o];
+                E2[i][j] = 1.f / R0[o];
+                kk[i][j] = R1[o];
+                qq[i][j] = R2[o];
+            }
+        const f32x4 ki0 = kk[0] * E2[0], ki1 = kk[1] * E2[1], kd0 = kk[0] * E1[0], kd1 = kk[1] * E1[1],
+                    qd0 = qq[0] * E1[0], qd1 = qq[1] * E1[1];
+        const f32x4 z = splat(0.f), x = splat(cs[col]);
+        f32x4 dq[2], row[2], cl[2];
+        dq[0] = mma(M00, ki0, z);
+        dq[1] = mma(M11, ki1, mma(M10, ki0, z) * x);
+        row[0] = mma(N00, ki0, z);
+        row[1] = mma(N11, ki1, mma(N10, ki0, z) * x);
+        cl[0] = mma(N00t, kd0, mma(M00t, qd0, mma(N10t, kd1, mma(M10t, qd1, z)) * x));
+        cl[1] = mma(N11t, kd1, mma(M11t, qd1, z));
+        f32x4 dG[2];
+        float end = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const f32x4 bb = i ? b1 : b0, u = splat(up[i][col]);
+            const f32x4 q_ = E1[i] * (dq[i] + u * qS[i][ct]);
+            const f32x4 r_ = E1[i] * (row[i] - u * (bb * rS[i][ct]));
+            const f32x4 cy = E2[i] * splat(dn[i][col]) * (bb * eS[i][ct]);
+            const f32x4 c_ = E2[i] * cl[i] + cy;
+            dG[i] = qq[i] * q_ + kk[i] * (r_ - c_);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                end += kk[i][j] * cy[j];
+                const int t = 16 * i + g4 + j;
+                const long long at = ((ck.tok + t) * a.H + h) * D + col;
+                if (t < ck.nv) {
+                    st_out<F32>(a.dq, at, q_[j]);
+                    st_out<F32>(a.dk, at, r_[j] + c_[j]);
+                }
+            }
+        }
+        end += dec[col] * sd[ct];
+        end += __shfl_xor(end, 16);
+        end += __shfl_xor(end, 32);
+        // dg: sum over the tokens from t on
+        float tot[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            dG[i][2] += dG[i][3];
+            dG[i][1] += dG[i][2];
+            dG[i][0] += dG[i][1];
+            const float x0 = dG[i][0];
+            float later = 0.f;
+#pragma unroll
+            for (int u = 1; u < 4; ++u) {
+                const float y = __shfl(x0, (l + 16 * u) & 63);
+                later += (l >> 4) + u < 4 ? y : 0.f;
+            }
+            tot[i] = __shfl(x0 + later, r16);
+            dG[i] += splat(later + end);
+        }
+        dG[0] += splat(tot[1]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (a.scalar_gate) {
+                dgs[i] += dG[i];
+                continue;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 16 * i + g4 + j;
+                if (t < ck.nv) a.dg[((ck.tok + t) * a.H + h) * D + col] = dG[i][j];
+            }
+        }
+    }
+    if (a.scalar_gate) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float x = dgs[i][j];
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
+                if (r16 == 0) part[w][16 * i + g4 + j] = x;
+            }
+        __syncthreads();
+        if (tid < ck.nv) a.dg[(ck.tok + tid) * a.H + h] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+    }
+}
+
+}  // namespace bwd
+
+long long bwd_slots(int B, int T, int N, bool varlen) {
+    return varlen ? (long long)T / kBwdChunk + N : (long long)B * (((long long)T + kBwdChunk - 1) / kBwdChunk);
+}
+
+template <bool F32, int NV>
+static hipError_t run_bwd(const BwdArgs& a, hipStream_t s) {
+    const long long work = (long long)a.nslots * a.H;
+    const int nb = D / (16 * NV);
+    const unsigned walks = (unsigned)(((long long)a.N * a.H + 7) / 8 * 8 * nb);
+    if (walks == 0) return hipSuccess;
+    if (work > 0) {
+        hipLaunchKernelGGL(bwd::kda_bwd_intra<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
+        hipLaunchKernelGGL(bwd::kda_bwd_states<NV>, dim3(walks), dim3(256), 0, s, a);
+    }
+    hipLaunchKernelGGL(bwd::kda_bwd_dstates<NV>, dim3(walks), dim3(256), 0, s, a);
+    if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_grads<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_bwd(const BwdArgs& a, int cus, hipStream_t s) {
+    (void)cus;
+    return a.f32 ? run_bwd<true, 2>(a, s) : run_bwd<false, 2>(a, s);
+}
+
+}  // namespace kda

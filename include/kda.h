@@ -323,6 +323,42 @@ kda_status_t kda_fwd_staged(const void* q, const void* k, const void* v, const f
                             const float* beta, const int32_t* cu_seqlens, const float* h0,
                             void* o, float* hT, const kda_desc_t* desc, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Gradient of kda_fwd (training). Given d_o, the gradient of a loss with
+ * respect to o, and dhT, the gradient with respect to the final state (NULL:
+ * zero), it writes the gradients with respect to every input:
+ *     dq, dk, dv  [B, T, H, 128] in_dtype
+ *     dg          [B, T, H, 128] fp32
+ *     dbeta       [B, T, H]      fp32
+ *     dh0         [N, H, 128, 128] fp32 (NULL: not written)
+ * q, k, v, g, beta, cu_seqlens, h0 are the forward's own inputs (states inside
+ * the sequences are recomputed, nothing is kept from the forward); d_o is
+ * [B, T, H, 128] fp32, 16-byte aligned (KDA_ERR_UNSUPPORTED otherwise). Rows of tokens outside
+ * [cu[0], cu[N]) are left as they were. A zero-length sequence has dh0 = dhT.
+ * Needs desc->workspace of kda_bwd_workspace_size(desc) bytes, 16-byte aligned
+ * (KDA_ERR_WORKSPACE when missing or smaller); nothing is allocated, so the call
+ * may be captured. A workspace is used by one call at a time.
+ * Products run on fp32 matrix instructions and every sum is fp32: dg, dbeta and
+ * dh0 are accurate to about 1e-6 of their RMS, dq, dk, dv to their type's
+ * rounding, for g in [-5, 0], beta in [0, 1] and L2-normalised keys. Results do
+ * not depend on the order of execution (no atomics).
+ * No output may overlap an input, except dh0 == dhT. Other errors as kda_fwd. */
+kda_status_t kda_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                     const int32_t* cu_seqlens, const float* h0, const float* d_o, const float* dhT,
+                     void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dh0,
+                     const kda_desc_t* desc, void* stream);
+
+/* The same for kda_gdn_fwd: g and dg are [B, T, H]. */
+kda_status_t kda_gdn_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
+                         const int32_t* cu_seqlens, const float* h0, const float* d_o, const float* dhT,
+                         void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dh0,
+                         const kda_desc_t* desc, void* stream);
+
+/* Bytes of device workspace kda_bwd and kda_gdn_bwd need: 217,728 per head and
+ * chunk of 32 tokens (a sequence's last chunk may be shorter). 0 for an
+ * invalid descriptor. */
+size_t kda_bwd_workspace_size(const kda_desc_t* desc);
+
 #ifdef __cplusplus
 }
 #endif
