@@ -17,7 +17,8 @@ import torch
 from ._lib import KDA_BF16, KDA_F32, KERNELS, Desc, KDAError, Layout, lib, status_string  # noqa: F401
 
 __all__ = ["fwd", "gdn_fwd", "fwd_noalloc", "noalloc_max_workspace", "fwd_workspace_size", "kernel_workspace_size", "decode_step", "fwd_staged", "Staged", "KDAError", "status_string", "version",
-           "bwd", "gdn_bwd", "bwd_workspace_size"]
+           "bwd", "gdn_bwd", "bwd_workspace_size", "recurrent", "gdn_recurrent", "block_in", "gdn_block_in",
+           "block_in_bwd", "gdn_block_in_bwd", "block_out", "block_out_bwd"]
 
 D = 128
 
@@ -288,4 +289,5 @@ def fwd_staged(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_fin
     return o, hT, st
 
 
-from ._ops import bwd, bwd_workspace_size, gdn_bwd  # noqa: E402
+from ._ops import (block_in, block_in_bwd, block_out, block_out_bwd, bwd, bwd_workspace_size,  # noqa: E402
+                   gdn_block_in, gdn_block_in_bwd, gdn_bwd, gdn_recurrent, recurrent)

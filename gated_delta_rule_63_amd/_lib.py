@@ -8,6 +8,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkda.so")
 
 KDA_BF16, KDA_F32 = 0, 1
+# kda_activation_t
+ACTIVATIONS = {"sigmoid": 0, "silu": 1}
 # kda_kernel_t
 KERNELS = {"auto": 0, "pipe": 1, "serial": 2, "chunk16": 3, "two_pass": 4}
 STATUS = {0: "KDA_OK", -1: "KDA_ERR_NULL", -2: "KDA_ERR_SHAPE", -3: "KDA_ERR_UNSUPPORTED",
@@ -20,7 +22,10 @@ EXPORTS = ["kda_status_string", "kda_version", "kda_fwd_check", "kda_fwd", "kda_
            "kda_decode_step", "kda_staged_layout",
            "kda_staged_workspace_size", "kda_stage_chunk_map", "kda_stage_gate_scan", "kda_stage_intra",
            "kda_stage_recurrence", "kda_stage_output", "kda_fwd_staged",
-           "kda_bwd", "kda_gdn_bwd", "kda_bwd_workspace_size"]
+           "kda_bwd", "kda_gdn_bwd", "kda_bwd_workspace_size", "kda_recurrent", "kda_gdn_recurrent",
+           "kda_block_in", "kda_gdn_block_in", "kda_block_in_bwd", "kda_gdn_block_in_bwd",
+           "kda_block_in_bwd_workspace_size", "kda_block_out", "kda_block_out_bwd",
+           "kda_block_out_bwd_workspace_size"]
 
 
 class Desc(ctypes.Structure):
@@ -90,8 +95,21 @@ def lib():
             fn = getattr(L, name)
             fn.argtypes = [P] * 15 + [D, P]
             fn.restype = ctypes.c_int
-        L.kda_bwd_workspace_size.argtypes = [D]
-        L.kda_bwd_workspace_size.restype = ctypes.c_size_t
+        I, R = ctypes.c_int32, ctypes.c_float
+        for name in ("recurrent", "block_in", "block_in_bwd"):
+            types = {"recurrent": [P] * 9 + [I, I, P], "block_in": [P] * 6 + [R, R] + [P] * 4,
+                     "block_in_bwd": [P] * 6 + [R, R] + [P] * 10}[name]
+            for fn in (getattr(L, "kda_" + name), getattr(L, "kda_gdn_" + name)):
+                fn.argtypes = types + [D, P]
+                fn.restype = ctypes.c_int
+        L.kda_block_out.argtypes = [P, P, P, R, I, P, D, P]
+        L.kda_block_out.restype = ctypes.c_int
+        L.kda_block_out_bwd.argtypes = [P, P, P, R, I, P, P, P, P, D, P]
+        L.kda_block_out_bwd.restype = ctypes.c_int
+        for name in ("kda_bwd", "kda_block_in_bwd", "kda_block_out_bwd"):
+            fn = getattr(L, name + "_workspace_size")
+            fn.argtypes = [D]
+            fn.restype = ctypes.c_size_t
         _lib = L
     return _lib
 

@@ -10,7 +10,7 @@ from typing import Optional, Tuple
 import torch
 
 from . import D, _check_inputs, _check_out, _check_state, _desc, _ptr
-from ._lib import KDAError, lib
+from ._lib import ACTIVATIONS, KDA_BF16, KDA_F32, Desc, KDAError, lib
 
 _Tensor = Optional[torch.Tensor]
 
@@ -84,3 +84,190 @@ def _bwd(entry, q, k, v, g, beta, do, cu_seqlens, initial_state, d_final_state, 
         _call(entry, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(initial_state), _ptr(do),
               _ptr(d_final_state), *map(_ptr, outs), _ptr(dh0), ctypes.byref(d), s)
     return (*outs, dh0)
+
+
+# ------------------------------------------------- token by token over a state pool
+
+def recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+              pool: torch.Tensor, slots: _Tensor = None, out_slots: _Tensor = None, cu_seqlens: _Tensor = None,
+              out: _Tensor = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """The rule token by token for a few tokens per sequence, on states in a pool
+    ([P, H, 128, 128], fp32 or bf16), which is updated in place. q, k, v, g [B, T, H, 128],
+    beta [B, T, H], cu_seqlens as for fwd(). slots: int32 [N], the slot that sequence n
+    starts from (None: slot n); a value outside [0, P) is an empty place of the batch,
+    whose rows of the output are left as they were (unset without `out`). out_slots:
+    int32, one per token ([B, T]), where the state after that token goes (outside
+    [0, P): not kept); None: the last state goes back to the sequence's slot. A slot
+    that is written may not be used by another sequence of the call. Returns o, fp32
+    [B, T, H, 128]."""
+    return _recurrent("kda_recurrent", q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, stream)
+
+
+def gdn_recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
+                  pool: torch.Tensor, slots: _Tensor = None, out_slots: _Tensor = None, cu_seqlens: _Tensor = None,
+                  out: _Tensor = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """recurrent() with one gate per (token, head): g [B, T, H]."""
+    return _recurrent("kda_gdn_recurrent", q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, stream)
+
+
+def _check_recurrent(q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, scalar_gate, _device=True):
+    _check_inputs(q, k, v, g, beta, cu_seqlens, scalar_gate=scalar_gate, _device=_device)
+    d = _desc(q, cu_seqlens)
+    if (pool.dim() != 4 or tuple(pool.shape[1:]) != (q.shape[2], D, D) or not pool.is_contiguous()
+            or pool.dtype not in (torch.float32, torch.bfloat16) or pool.device != q.device):
+        raise ValueError(f"pool must be a contiguous float32 or bfloat16 [P, {q.shape[2]}, 128, 128] tensor on q's device")
+    if slots is None and pool.shape[0] < d.num_seqs:
+        raise ValueError("pool has fewer slots than there are sequences")
+    for name, t, n in (("slots", slots, d.num_seqs), ("out_slots", out_slots, q.shape[0] * q.shape[1])):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != q.device):
+            raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on q's device")
+    if out is not None:
+        _check_out("out", out, q.shape, q.device)
+    return d
+
+
+def _recurrent(entry, q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, stream):
+    d = _check_recurrent(q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, entry == "kda_gdn_recurrent")
+    with _on(q.device, stream) as s:
+        o = out if out is not None else torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        _call(entry, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(slots), _ptr(out_slots),
+              _ptr(pool), pool.shape[0], KDA_BF16 if pool.dtype == torch.bfloat16 else KDA_F32, _ptr(o),
+              ctypes.byref(d), s)
+    return o
+
+
+# ------------------------------------------------------------------ before the rule
+
+def block_in(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+             dt_bias: _Tensor = None, lower_bound: Optional[float] = None, eps: float = 1e-6,
+             stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
+    """The inputs of fwd() from raw projections: q / sqrt(|q|^2 + eps), k alike, the
+    gate g from f, and beta = sigmoid(b). With x = f + dt_bias,
+    g = -exp(A_log) softplus(x), or with a lower bound (< 0) lower_bound *
+    sigmoid(exp(A_log) x). q, k, f [B, T, H, 128] and b [B, T, H] share a dtype (bf16
+    or fp32); A_log [H], dt_bias [H, 128] fp32. Returns (q, k, g, beta)."""
+    return _block_in("kda_block_in", q, k, f, b, A_log, dt_bias, lower_bound, eps, stream)
+
+
+def gdn_block_in(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+                 dt_bias: _Tensor = None, lower_bound: Optional[float] = None, eps: float = 1e-6,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
+    """block_in() for gdn_fwd(): f [B, T, H], dt_bias [H], g [B, T, H]."""
+    return _block_in("kda_gdn_block_in", q, k, f, b, A_log, dt_bias, lower_bound, eps, stream)
+
+
+def _rows(name, t, shape, dtype, like, _device=True):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device \
+            or (_device and not t.is_cuda):
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} device tensor on the first argument's device")
+
+
+def _rows_desc(x):
+    B, T, H, K = x.shape
+    return Desc(B, T, H, K, K, B, {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}.get(x.dtype, -1), KDA_F32, None, 0)
+
+
+def _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar_gate, _device=True):
+    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("q must be a bfloat16 or float32 [B, T, H, 128] tensor")
+    gate = q.shape[:3] if scalar_gate else q.shape
+    for name, t, shape in (("q", q, q.shape), ("k", k, q.shape), ("f", f, gate), ("b", b, q.shape[:3])):
+        _rows(name, t, shape, q.dtype, q, _device)
+    _rows("A_log", A_log, q.shape[2:3], torch.float32, q, _device)
+    if dt_bias is not None:
+        _rows("dt_bias", dt_bias, gate[2:], torch.float32, q, _device)
+    if lower_bound is not None and not lower_bound < 0:
+        raise ValueError("lower_bound must be negative (None: no bound)")
+
+
+def _block_in(entry, q, k, f, b, A_log, dt_bias, lower_bound, eps, stream):
+    scalar = entry == "kda_gdn_block_in"
+    _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar)
+    with _on(q.device, stream) as s:
+        outs = [torch.empty_like(q), torch.empty_like(k), torch.empty(f.shape, dtype=torch.float32, device=q.device),
+                torch.empty(b.shape, dtype=torch.float32, device=q.device)]
+        _call(entry, _ptr(q), _ptr(k), _ptr(f), _ptr(b), _ptr(A_log), _ptr(dt_bias), lower_bound or 0.0, eps,
+              *map(_ptr, outs), ctypes.byref(_rows_desc(q)), s)
+    return tuple(outs)
+
+
+def block_in_bwd(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+                 dq: torch.Tensor, dk: torch.Tensor, dg: torch.Tensor, dbeta: torch.Tensor, dt_bias: _Tensor = None,
+                 lower_bound: Optional[float] = None, eps: float = 1e-6,
+                 stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
+    """Gradient of block_in(): its inputs, and the gradients with respect to its outputs
+    (as bwd() returns them). Returns (dq, dk, df, db, dA_log, ddt_bias), the first four
+    in q's dtype, the sums over tokens fp32 (ddt_bias None without dt_bias)."""
+    return _block_in_bwd("kda_block_in_bwd", q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps, stream)
+
+
+def gdn_block_in_bwd(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
+                     dq: torch.Tensor, dk: torch.Tensor, dg: torch.Tensor, dbeta: torch.Tensor,
+                     dt_bias: _Tensor = None, lower_bound: Optional[float] = None, eps: float = 1e-6,
+                     stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
+    """Gradient of gdn_block_in()."""
+    return _block_in_bwd("kda_gdn_block_in_bwd", q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps,
+                         stream)
+
+
+def _check_block_in_bwd(q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, scalar_gate, _device=True):
+    _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar_gate, _device)
+    for name, t, like, dtype in (("dq", dq, q, q.dtype), ("dk", dk, q, q.dtype), ("dg", dg, f, torch.float32),
+                                 ("dbeta", dbeta, b, torch.float32)):
+        _rows(name, t, like.shape, dtype, q, _device)
+
+
+def _block_in_bwd(entry, q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps, stream):
+    scalar = entry == "kda_gdn_block_in_bwd"
+    _check_block_in_bwd(q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, scalar)
+    d = _rows_desc(q)
+    with _on(q.device, stream) as s:
+        ws = torch.empty(int(lib().kda_block_in_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8, device=q.device)
+        d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
+        outs = [torch.empty_like(x) for x in (q, k, f, b, A_log)]
+        dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
+        _call(entry, _ptr(q), _ptr(k), _ptr(f), _ptr(b), _ptr(A_log), _ptr(dt_bias), lower_bound or 0.0, eps, _ptr(dq),
+              _ptr(dk), _ptr(dg), _ptr(dbeta), *map(_ptr, outs), _ptr(dbias), ctypes.byref(d), s)
+    return (*outs, dbias)
+
+
+# ------------------------------------------------------------------- after the rule
+
+def block_out(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, activation: str = "sigmoid", eps: float = 1e-5,
+              stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gated RMS norm of fwd()'s output: o / sqrt(mean(o^2) + eps) * weight * act(z), over
+    the 128 channels of each (token, head). o fp32, z bf16 or fp32 [B, T, H, 128], weight
+    fp32 [128]; activation "sigmoid" or "silu" (z sigmoid(z)). Returns y in z's dtype."""
+    _check_block_out(o, z, weight, activation)
+    with _on(z.device, stream) as s:
+        y = torch.empty_like(z)
+        _call("kda_block_out", _ptr(o), _ptr(z), _ptr(weight), eps, ACTIVATIONS[activation], _ptr(y),
+              ctypes.byref(_rows_desc(z)), s)
+    return y
+
+
+def _check_block_out(o, z, weight, activation, dy=None, _device=True):
+    if z.dim() != 4 or z.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("z must be a bfloat16 or float32 [B, T, H, 128] tensor")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    _rows("z", z, z.shape, z.dtype, z, _device)
+    _rows("o", o, z.shape, torch.float32, z, _device)
+    _rows("weight", weight, (D,), torch.float32, z, _device)
+    if dy is not None:
+        _rows("dy", dy, z.shape, z.dtype, z, _device)
+
+
+def block_out_bwd(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
+                  activation: str = "sigmoid", eps: float = 1e-5,
+                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
+    """Gradient of block_out(). Returns (do fp32, dz in z's dtype, dweight fp32)."""
+    _check_block_out(o, z, weight, activation, dy)
+    d = _rows_desc(z)
+    with _on(z.device, stream) as s:
+        ws = torch.empty(int(lib().kda_block_out_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8, device=z.device)
+        d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
+        do, dz, dw = torch.empty_like(o), torch.empty_like(z), torch.empty_like(weight)
+        _call("kda_block_out_bwd", _ptr(o), _ptr(z), _ptr(weight), eps, ACTIVATIONS[activation], _ptr(dy), _ptr(do),
+              _ptr(dz), _ptr(dw), ctypes.byref(d), s)
+    return do, dz, dw

@@ -359,6 +359,108 @@ kda_status_t kda_gdn_bwd(const void* q, const void* k, const void* v, const floa
  * invalid descriptor. */
 size_t kda_bwd_workspace_size(const kda_desc_t* desc);
 
+/* ---------------------------------------------------------------------------
+ * The rule token by token over a pool of states (serving): one token or a few
+ * per sequence, with states kept in slots of a pool.
+ *     q, k, v, g, beta, cu_seqlens, o as for kda_fwd (N sequences, rows of T
+ *                tokens or packed)
+ *     pool       [num_slots, H, 128, 128], the states as S[k][v], pool_dtype
+ *                KDA_F32 or KDA_BF16
+ *     slots      int32 [N], device: the slot that sequence n starts from. NULL:
+ *                slot n. A value outside [0, num_slots) marks an empty place of
+ *                the batch: its o rows and the pool are left as they were.
+ *     out_slots  int32, one per token (cu_seqlens: [T], else [N, T]), device:
+ *                the slot that receives the state after that token; outside
+ *                [0, num_slots): it is not kept. NULL: the state after the last
+ *                token goes back to the sequence's own slot.
+ * With out_slots a batch of drafted tokens can be verified and any prefix of
+ * them accepted afterwards: the states are all there, and the start state stays
+ * unless one of the slots is its own.
+ * Within a call, a slot that is written may not be read or written for another
+ * sequence, nor for two tokens of one (its contents would be undefined; no
+ * access leaves the pool). A zero-length sequence changes nothing. The state is
+ * fp32 within the call; a bf16 pool is rounded when a state is written.
+ * q, k, v, pool, o and, per channel, g must be 16-byte aligned
+ * (KDA_ERR_UNSUPPORTED). num_slots < N without slots, or more than 2^23
+ * (sequence, head) pairs, is KDA_ERR_SHAPE; other errors as kda_fwd.
+ * desc->workspace is ignored. Time grows with the tokens of a sequence: for
+ * whole prompts use kda_fwd. */
+kda_status_t kda_recurrent(const void* q, const void* k, const void* v, const float* g,
+                           const float* beta, const int32_t* cu_seqlens, const int32_t* slots,
+                           const int32_t* out_slots, void* pool, int32_t num_slots, int32_t pool_dtype,
+                           float* o, const kda_desc_t* desc, void* stream);
+
+/* The same with one gate per (token, head): g [B, T, H]. */
+kda_status_t kda_gdn_recurrent(const void* q, const void* k, const void* v, const float* g,
+                               const float* beta, const int32_t* cu_seqlens, const int32_t* slots,
+                               const int32_t* out_slots, void* pool, int32_t num_slots, int32_t pool_dtype,
+                               float* o, const kda_desc_t* desc, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What comes right before the rule, in one pass: L2 norms of the queries and
+ * keys, the decay gate and beta. The pages name the gate's parameters A_log,
+ * dt_bias and lower_bound but not its formula (donniechu.com page, section "Số
+ * liệu kỹ thuật"); this library's reading is
+ *     q_out = q / sqrt(|q|^2 + eps),  k_out alike,  beta = sigmoid(b)
+ *     x = f + dt_bias,  g = -exp(A_log) softplus(x)          lower_bound == 0
+ *                       g = lower_bound sigmoid(exp(A_log) x)   lower_bound < 0
+ * so that a lower bound of -5 keeps g in the domain of kda_fwd.
+ *     q, k, q_out, k_out [B, T, H, 128] in_dtype
+ *     f        [B, T, H, 128] in_dtype (kda_gdn_block_in: [B, T, H])
+ *     b        [B, T, H] in_dtype
+ *     A_log    [H] fp32;  dt_bias [H, 128] (kda_gdn_block_in: [H]) fp32, NULL: zero
+ *     g        [B, T, H, 128] fp32 (kda_gdn_block_in: [B, T, H]);  beta [B, T, H] fp32
+ * desc: shapes and in_dtype; num_seqs is not used beyond kda_fwd's checks. A
+ * positive or non-finite lower_bound, a negative or non-finite eps, or a pointer
+ * to rows of 128 channels that is not 16-byte aligned is KDA_ERR_UNSUPPORTED;
+ * more than 2^29 (token, head) rows is KDA_ERR_SHAPE. q_out == q and k_out == k
+ * are allowed. With eps == 0 a zero row gives NaN. */
+kda_status_t kda_block_in(const void* q, const void* k, const void* f, const void* b, const float* A_log,
+                          const float* dt_bias, float lower_bound, float eps, void* q_out, void* k_out,
+                          float* g, float* beta, const kda_desc_t* desc, void* stream);
+kda_status_t kda_gdn_block_in(const void* q, const void* k, const void* f, const void* b,
+                              const float* A_log, const float* dt_bias, float lower_bound, float eps,
+                              void* q_out, void* k_out, float* g, float* beta, const kda_desc_t* desc,
+                              void* stream);
+
+/* Its gradient. q .. eps are the forward's inputs; dq_out, dk_out (in_dtype),
+ * dg and dbeta (fp32) the gradients with respect to its outputs; dq, dk, df, db
+ * (in_dtype), dA_log [H] and ddt_bias (fp32, like dt_bias; NULL: not written)
+ * the results. No output may overlap an input. Needs desc->workspace of
+ * kda_block_in_bwd_workspace_size(desc) bytes (KDA_ERR_WORKSPACE), used by one
+ * call at a time; sums over tokens are fp32 in a fixed order. T = 0 gives zero
+ * sums. */
+kda_status_t kda_block_in_bwd(const void* q, const void* k, const void* f, const void* b, const float* A_log,
+                              const float* dt_bias, float lower_bound, float eps, const void* dq_out,
+                              const void* dk_out, const float* dg, const float* dbeta, void* dq, void* dk,
+                              void* df, void* db, float* dA_log, float* ddt_bias, const kda_desc_t* desc,
+                              void* stream);
+kda_status_t kda_gdn_block_in_bwd(const void* q, const void* k, const void* f, const void* b,
+                                  const float* A_log, const float* dt_bias, float lower_bound, float eps,
+                                  const void* dq_out, const void* dk_out, const float* dg, const float* dbeta,
+                                  void* dq, void* dk, void* df, void* db, float* dA_log, float* ddt_bias,
+                                  const kda_desc_t* desc, void* stream);
+size_t kda_block_in_bwd_workspace_size(const kda_desc_t* desc);   /* enough for both gates */
+
+/* ---------------------------------------------------------------------------
+ * What comes right after the rule: RMS norm over each (token, head)'s 128
+ * channels, weight and output gate,
+ *     y = o / sqrt(mean(o^2) + eps) * weight * act(z)
+ *     o [B, T, H, 128] fp32 (kda_fwd's output);  z, y [B, T, H, 128] in_dtype
+ *     weight [128] fp32;  activation a kda_activation_t: sigmoid(z) or z sigmoid(z)
+ * and its gradient: d_o (fp32), dz (in_dtype) and dweight (fp32) from dy
+ * (in_dtype), with desc->workspace of kda_block_out_bwd_workspace_size(desc)
+ * bytes (KDA_ERR_WORKSPACE). Errors as kda_block_in; every pointer to rows of 128
+ * channels, weight included, is 16-byte aligned. d_o may take o's place, dz that of z or dy. */
+typedef enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_activation_t;
+
+kda_status_t kda_block_out(const float* o, const void* z, const float* weight, float eps, int32_t activation,
+                           void* y, const kda_desc_t* desc, void* stream);
+kda_status_t kda_block_out_bwd(const float* o, const void* z, const float* weight, float eps,
+                               int32_t activation, const void* dy, float* d_o, void* dz, float* dweight,
+                               const kda_desc_t* desc, void* stream);
+size_t kda_block_out_bwd_workspace_size(const kda_desc_t* desc);
+
 #ifdef __cplusplus
 }
 #endif

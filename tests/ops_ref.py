@@ -60,7 +60,7 @@ def rule_bwd(q, k, v, g, beta, do, bounds, h0=None, dhT=None):
 
 def within(got, ref, what, half_step=0.0, scale=None, tol=1e-4):
     """|got - ref| <= half_step |ref| + tol * scale. half_step: the rounding to the
-    output's type (bf16 2^-8, fp32 0). scale: RMS of the reference by default. tol:
+    output's type (bf16 2^-8, fp32 0), or an array that bounds the rounding itself. scale: RMS of the reference by default. tol:
     1e-4, the library's bar for fp32 arithmetic: sums of up to 128 products of
     rounding 2^-24 (rms 2^-24 sqrt(128) = 7e-7), chained about ten times (2e-6),
     exponents up to 40 with rounding 40 * 2^-24 = 2.4e-6, at 6 sigma over the
@@ -69,6 +69,7 @@ def within(got, ref, what, half_step=0.0, scale=None, tol=1e-4):
     assert got.shape == ref.shape, (what, got.shape, ref.shape)
     assert np.all(np.isfinite(got)), f"{what}: not finite"
     scale = max(W.rms(ref) if scale is None else scale, 1e-30)
-    off = float(np.max(np.abs(got - ref) - half_step * np.abs(ref), initial=0.0)) / scale
+    allowed = half_step if isinstance(half_step, np.ndarray) else half_step * np.abs(ref)
+    off = float(np.max(np.abs(got - ref) - allowed, initial=0.0)) / scale
     print(f"{what}: {off:.2e} of {scale:.2e}", flush=True)
     assert off <= tol, f"{what}: off by {off:.2e} of {scale:.2e} (bar {tol:.0e})"
