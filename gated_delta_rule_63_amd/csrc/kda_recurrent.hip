@@ -10,108 +10,97 @@
 // bytes are the bound (64 KiB in fp32, 32 KiB in bf16, against 1.3 KB of
 // inputs a token); the products are 7 * 128^2 operations a token on the VALU.
 //
-// The columns of S never mix, so a wave owns 4 CG of them over all 128 rows
-// and needs no other wave: no LDS and no barrier, which would cost a small
-// batch its latency. Lane (rg, cg) holds ROWS consecutive rows of four
-// columns; the column sums run over the 64 / CG row groups by lane exchange.
-// CG = 8 gives 128-byte row pieces and 4 waves a head; CG = 4 gives 64-byte
-// pieces and 8 waves a head, for batches too small to occupy the chip.
+// The columns of S never mix, so a wave owns 8 NC of them over all 128 rows
+// and needs no other wave: no barrier, which would cost a small batch its
+// latency. Lane (rg, cg) holds rows rg, rg + 8, ... of NC neighbouring columns;
+// the column sums run over the eight row groups by lane exchange. A token's k,
+// q and e^g pass through the wave's own LDS, so that they are converted once
+// a wave. NC = 4 gives 128-byte row pieces and 4 waves a head; NC = 2 gives
+// 64-byte pieces and 8 waves a head, for batches too small to occupy the chip.
+//
+// Every product and sum of the state's update is rounded by itself, and P^T k
+// is summed in eight interleaved parts of 16 rows (even parts, then odd ones):
+// the bits of the formula evaluated operation by operation. A fused or
+// reordered form would be as accurate, but a bf16 pool turns a difference in
+// the last bit into a whole bf16 step whenever it falls on a rounding boundary.
 #include "kda_device.h"
 #include "kda_recurrent.h"
 
 namespace kda {
 namespace recurrent {
 
-template <bool BF16>
-__device__ __forceinline__ f32x4 ld_state(const void* p, long long i) {
+template <int NC>
+struct alignas(4 * NC) Cols {
+    float x[NC];
+};
+
+template <bool BF16, int NC>
+__device__ __forceinline__ Cols<NC> ld_cols(const void* p, long long i) {
     if constexpr (BF16) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-        return f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u)};
+        typedef uint32_t words __attribute__((ext_vector_type(NC / 2)));
+        Cols<NC> r;
+        const words u = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) {
+            r.x[2 * j] = __uint_as_float(u[j] << 16);
+            r.x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+        }
+        return r;
     } else {
-        return *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i);
+        return *reinterpret_cast<const Cols<NC>*>(static_cast<const float*>(p) + i);
     }
 }
 // A bf16 pool's states are rounded to nearest when they are written, once per
 // call and not per token.
-template <bool BF16>
-__device__ __forceinline__ void st_state(void* p, long long i, const f32x4& x) {
+template <bool BF16, int NC>
+__device__ __forceinline__ void st_cols(void* p, long long i, const Cols<NC>& r) {
     if constexpr (BF16) {
-        bf16x2 lo = {(__bf16)x[0], (__bf16)x[1]}, hi = {(__bf16)x[2], (__bf16)x[3]};
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i) =
-            make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+        typedef uint32_t words __attribute__((ext_vector_type(NC / 2)));
+        words u;
+#pragma unroll
+        for (int j = 0; j < NC / 2; ++j) {
+            const bf16x2 h = {(__bf16)r.x[2 * j], (__bf16)r.x[2 * j + 1]};
+            u[j] = __builtin_bit_cast(uint32_t, h);
+        }
+        *reinterpret_cast<words*>(static_cast<uint16_t*>(p) + i) = u;
     } else {
-        *reinterpret_cast<f32x4*>(static_cast<float*>(p) + i) = x;
+        *reinterpret_cast<Cols<NC>*>(static_cast<float*>(p) + i) = r;
     }
 }
 
-// N consecutive inputs from element i on, i a multiple of N.
-template <bool F32, int N>
-__device__ __forceinline__ void ld_row(float (&x)[N], const void* p, long long i) {
-    if constexpr (F32) {
-#pragma unroll
-        for (int j = 0; j < N; j += 4) {
-            const f32x4 u = *reinterpret_cast<const f32x4*>(static_cast<const float*>(p) + i + j);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) x[j + m] = u[m];
-        }
-    } else if constexpr (N == 4) {
-        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-        x[0] = __uint_as_float(u.x << 16);
-        x[1] = __uint_as_float(u.x & 0xffff0000u);
-        x[2] = __uint_as_float(u.y << 16);
-        x[3] = __uint_as_float(u.y & 0xffff0000u);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; j += 8) {
-            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i + j);
-            const uint32_t s[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                x[j + 2 * m] = __uint_as_float(s[m] << 16);
-                x[j + 2 * m + 1] = __uint_as_float(s[m] & 0xffff0000u);
-            }
-        }
-    }
-}
-
-template <int CG>
-__device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-    for (int o = CG; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
-}
-
-// One token's inputs as a lane needs them.
-template <int ROWS>
+// One token's inputs: channels 2 l and 2 l + 1 of k, q, g in lane l, this
+// lane's columns of v.
+template <int NC>
 struct Token {
-    float k[ROWS], q[ROWS], d[ROWS], v[4], beta;
+    Cols<2> k, q, g;
+    Cols<NC> v;
+    float beta;
 };
 
-template <bool F32, int ROWS>
-__device__ __forceinline__ void ld_token(Token<ROWS>& x, const RecurrentArgs& a, long long tok, int h, int r0, int c0) {
+template <bool F32, int NC>
+__device__ __forceinline__ void ld_token(Token<NC>& x, const RecurrentArgs& a, long long tok, int h, int l, int c0) {
     const long long th = tok * a.H + h;
-    ld_row<F32>(x.k, a.k, th * D + r0);
-    ld_row<F32>(x.q, a.q, th * D + r0);
-    ld_row<F32>(x.v, a.v, th * D + c0);
+    x.k = ld_cols<!F32, 2>(a.k, th * D + 2 * l);
+    x.q = ld_cols<!F32, 2>(a.q, th * D + 2 * l);
+    x.v = ld_cols<!F32, NC>(a.v, th * D + c0);
+    if (a.scalar_gate) x.g.x[0] = a.g[th];
+    else x.g = ld_cols<false, 2>(a.g, th * D + 2 * l);
     x.beta = a.beta[th];
-    if (a.scalar_gate) {
-        x.d[0] = a.g[th];
-    } else {
-        ld_row<true>(x.d, a.g, th * D + r0);
-    }
 }
 
-template <bool F32, bool BF16, int CG>
+constexpr int RS = 20;      // LDS row of a row group's 16 rows: 16-byte aligned, banks spread
+
+template <bool F32, bool BF16, int NC>
 __global__ __launch_bounds__(256) void kda_recurrent_kernel(RecurrentArgs a) {
-    constexpr int ROWS = D * CG / 64, WV = D / (4 * CG);   // rows a lane, waves a head
+    constexpr int WV = D / (8 * NC);                       // waves a head
+    __shared__ __align__(16) float sh[4][3][8 * RS];
     const long long wave = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
     const long long nh = wave / WV;
     if (nh >= (long long)a.N * a.H) return;
     const int n = (int)(nh / a.H), h = (int)(nh % a.H);
     const int slot = a.slots ? a.slots[n] : n;
     if (slot < 0 || slot >= a.num_slots) return;           // an empty place of the batch
-    const int l = threadIdx.x & 63, r0 = (l / CG) * ROWS, c0 = (int)(wave % WV) * 4 * CG + 4 * (l % CG);
+    const int l = threadIdx.x & 63, rg = l >> 3, c0 = (int)(wave % WV) * 8 * NC + NC * (l & 7);
     long long tok = (long long)n * a.T;
     int len = a.T;
     if (a.cu) {
@@ -120,41 +109,83 @@ __global__ __launch_bounds__(256) void kda_recurrent_kernel(RecurrentArgs a) {
         tok = t0;
     }
     if (len <= 0) return;
-    Token<ROWS> x;
-    ld_token<F32>(x, a, tok, h, r0, c0);
-    f32x4 s[ROWS];
-    const long long from = ((long long)slot * a.H + h) * (D * D) + r0 * D + c0;
+    Token<NC> x;
+    ld_token<F32, NC>(x, a, tok, h, l, c0);
+    Cols<NC> s[16];
+    const long long from = ((long long)slot * a.H + h) * (D * D) + rg * D + c0;
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) s[r] = ld_state<BF16>(a.pool, from + r * D);
+    for (int m = 0; m < 16; ++m) s[m] = ld_cols<BF16, NC>(a.pool, from + m * 8 * D);
+    float (*const w)[8 * RS] = sh[threadIdx.x >> 6];
+    const int at0 = ((2 * l) & 7) * RS + (l >> 2), at1 = at0 + RS;   // channel c at (c % 8) RS + c / 8
     for (int t = 0; t < len; ++t, ++tok) {
-        float d = a.scalar_gate ? expf(x.d[0]) : 0.f;
-        f32x4 ak = {0.f, 0.f, 0.f, 0.f}, aq = ak;
-        float kq = 0.f;
+        __builtin_amdgcn_wave_barrier();                   // the reads below stay behind these writes
+        w[0][at0] = x.k.x[0];
+        w[0][at1] = x.k.x[1];
+        w[1][at0] = x.q.x[0];
+        w[1][at1] = x.q.x[1];
+        const float d0 = expf(x.g.x[0]);
+        w[2][at0] = d0;
+        w[2][at1] = a.scalar_gate ? d0 : expf(x.g.x[1]);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        float ak[NC], aq[NC], kq = 0.f;
 #pragma unroll
-        for (int r = 0; r < ROWS; ++r) {
-            s[r] *= a.scalar_gate ? d : expf(x.d[r]);
-            ak += s[r] * x.k[r];
-            aq += s[r] * x.q[r];
-            kq += x.k[r] * x.q[r];
+        for (int j = 0; j < NC; ++j) ak[j] = aq[j] = 0.f;
+        float kk[16];
+#pragma unroll
+        for (int m4 = 0; m4 < 4; ++m4) {
+            const f32x4 k4 = *reinterpret_cast<const f32x4*>(&w[0][rg * RS + 4 * m4]);
+            const f32x4 q4 = *reinterpret_cast<const f32x4*>(&w[1][rg * RS + 4 * m4]);
+            const f32x4 d4 = *reinterpret_cast<const f32x4*>(&w[2][rg * RS + 4 * m4]);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int m = 4 * m4 + u;
+                kk[m] = k4[u];
+                kq += k4[u] * q4[u];
+#pragma unroll
+                for (int j = 0; j < NC; ++j) {
+                    const float p = s[m].x[j] * d4[u];
+                    s[m].x[j] = p;
+                    const float pk = p * k4[u];
+                    ak[j] += pk;
+                    aq[j] += p * q4[u];
+                }
+            }
         }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            ak[j] = row_sum<CG>(ak[j]);
-            aq[j] = row_sum<CG>(aq[j]);
-        }
-        kq = row_sum<CG>(kq);
-        f32x4 be;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) be[j] = x.beta * (x.v[j] - ak[j]);
-#pragma unroll
-        for (int r = 0; r < ROWS; ++r) s[r] += be * x.k[r];
-        if (l < CG) *reinterpret_cast<f32x4*>(a.o + (tok * a.H + h) * D + c0) = aq + be * kq;
+        const float v_beta = x.beta;
+        const Cols<NC> v = x.v;
+        const long long th = tok * a.H + h;
         const int to = a.out_slots ? a.out_slots[tok] : t + 1 == len ? slot : -1;
-        if (t + 1 < len) ld_token<F32>(x, a, tok + 1, h, r0, c0);
-        if (to >= 0 && to < a.num_slots) {
-            const long long into = ((long long)to * a.H + h) * (D * D) + r0 * D + c0;
+        if (t + 1 < len) ld_token<F32, NC>(x, a, tok + 1, h, l, c0);
+        kq += __shfl_xor(kq, 8);
+        kq += __shfl_xor(kq, 16);
+        kq += __shfl_xor(kq, 32);
+        Cols<NC> be, o;
 #pragma unroll
-            for (int r = 0; r < ROWS; ++r) st_state<BF16>(a.pool, into + r * D, s[r]);
+        for (int j = 0; j < NC; ++j) {
+            float e = __shfl(ak[j], l & 15);               // parts 0 and 1, then 2 and 3, ...
+#pragma unroll
+            for (int r = 1; r < 4; ++r) e += __shfl(ak[j], (l & 15) + 16 * r);
+            e += __shfl_xor(e, 8);
+            be.x[j] = v_beta * (v.x[j] - e);
+            aq[j] += __shfl_xor(aq[j], 8);
+            aq[j] += __shfl_xor(aq[j], 16);
+            aq[j] += __shfl_xor(aq[j], 32);
+            o.x[j] = aq[j] + be.x[j] * kq;
+        }
+#pragma unroll
+        for (int m = 0; m < 16; ++m)
+#pragma unroll
+            for (int j = 0; j < NC; ++j) {
+                const float ke = kk[m] * be.x[j];
+                s[m].x[j] += ke;
+            }
+        if (rg == 0) *reinterpret_cast<Cols<NC>*>(a.o + th * D + c0) = o;
+        if (to >= 0 && to < a.num_slots) {
+            const long long into = ((long long)to * a.H + h) * (D * D) + rg * D + c0;
+#pragma unroll
+            for (int m = 0; m < 16; ++m) st_cols<BF16, NC>(a.pool, into + m * 8 * D, s[m]);
         }
     }
 }
@@ -163,8 +194,8 @@ template <bool F32, bool BF16>
 hipError_t run(const RecurrentArgs& a, int cus, hipStream_t stream) {
     const long long nh = (long long)a.N * a.H;
     // four waves a head leave compute units without a workgroup: eight
-    if (nh < cus) hipLaunchKernelGGL((kda_recurrent_kernel<F32, BF16, 4>), dim3((unsigned)(2 * nh)), dim3(256), 0, stream, a);
-    else hipLaunchKernelGGL((kda_recurrent_kernel<F32, BF16, 8>), dim3((unsigned)nh), dim3(256), 0, stream, a);
+    if (nh < cus) hipLaunchKernelGGL((kda_recurrent_kernel<F32, BF16, 2>), dim3((unsigned)(2 * nh)), dim3(256), 0, stream, a);
+    else hipLaunchKernelGGL((kda_recurrent_kernel<F32, BF16, 4>), dim3((unsigned)nh), dim3(256), 0, stream, a);
     return hipGetLastError();
 }
 
