@@ -15,16 +15,37 @@ from ._lib import ACTIVATIONS, KDA_BF16, KDA_F32, Desc, KDAError, lib
 _Tensor = Optional[torch.Tensor]
 
 
-@contextlib.contextmanager
+class _Here:
+    """The call's stream where its device and stream are current already."""
+
+    def __init__(self, raw):
+        self.raw = raw
+
+    def __enter__(self):
+        return self.raw
+
+    def __exit__(self, *_):
+        pass
+
+
 def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     """Makes `device` and the call's stream current, so that launches and
-    allocations go there; yields the stream as the C ABI takes it."""
+    allocations go there; yields the stream as the C ABI takes it. (Entering torch's
+    contexts costs more than a small kernel: where they would change nothing they are
+    left out.)"""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return _Here(torch.cuda.current_stream(device.index).cuda_stream)
+    return _there(device, stream)
+
+
+@contextlib.contextmanager
+def _there(device, stream):
     with torch.cuda.device(device):
         s = stream or torch.cuda.current_stream(device)
         if s.device != device:
             raise ValueError("stream must belong to the tensors' device")
         with torch.cuda.stream(s):
-            yield ctypes.c_void_p(s.cuda_stream)
+            yield s.cuda_stream
 
 
 def _call(entry: str, *args) -> None:

@@ -118,13 +118,13 @@ __device__ __forceinline__ void gate_bwd(float x, float a, float bound, float& d
 constexpr int kRows = 16;          // rows of a workgroup at a time
 constexpr int kSteps = 4;          // rows of a lane group of the forward kernels
 
-template <bool F32, bool SCALAR>
+template <bool F32, bool SCALAR, int STEPS>
 __global__ __launch_bounds__(256) void kda_block_in_kernel(BlockInArgs a) {
     const int gi = threadIdx.x >> 4, i = threadIdx.x & 15;
-    const long long first = (long long)blockIdx.x * (kRows * kSteps), rows = a.tokens * a.H;
+    const long long first = (long long)blockIdx.x * (kRows * STEPS), rows = a.tokens * a.H;
     const unsigned h0 = (unsigned)(first % a.H);
 #pragma unroll
-    for (int step = 0; step < kSteps; ++step) {
+    for (int step = 0; step < STEPS; ++step) {
         const int at = step * kRows + gi;
         const long long row = first + at;
         if (row >= rows) return;
@@ -248,12 +248,14 @@ __global__ __launch_bounds__(256) void kda_block_in_bwd_kernel(BlockInArgs a) {
 __device__ __forceinline__ float column_sum(const float* part, long long P, long long n, long long col, bool on) {
     __shared__ float s[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-    float acc = 0.f;
+    float a[8] = {};   // eight loads in flight: the latency of one after the other was the whole time
     if (on)
-        for (long long p = y; p < P; p += 32) acc += part[p * n + col];
-    s[y][x] = acc;
+        for (long long p = y; p < P; p += 8 * 32)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) a[i] += p + 32 * i < P ? part[(p + 32 * i) * n + col] : 0.f;
+    s[y][x] = ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
     __syncthreads();
-    acc = 0.f;
+    float acc = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) acc += s[i][x];
     return acc;
@@ -271,13 +273,13 @@ __global__ __launch_bounds__(1024) void kda_block_in_sum(BlockInArgs a, long lon
 }
 
 // ----------------------------------------------------------------------- after
-template <bool F32>
+template <bool F32, int STEPS>
 __global__ __launch_bounds__(256) void kda_block_out_kernel(BlockOutArgs a) {
     const int gi = threadIdx.x >> 4, i = threadIdx.x & 15;
     const f32x8 w = ld8(a.weight + 8 * i);
 #pragma unroll
-    for (int step = 0; step < kSteps; ++step) {
-        const long long row = ((long long)blockIdx.x * kSteps + step) * kRows + gi;
+    for (int step = 0; step < STEPS; ++step) {
+        const long long row = ((long long)blockIdx.x * STEPS + step) * kRows + gi;
         if (row >= a.rows) return;
         const long long at = row * D + 8 * i;
         const f32x8 o = ld8(a.o + at), z = ld8<F32>(a.z, at);
@@ -334,7 +336,15 @@ __global__ __launch_bounds__(1024) void kda_block_out_sum(BlockOutArgs a, int P)
     if (threadIdx.x < 32) a.dweight[col] = x;
 }
 
-unsigned blocks(long long rows) { return (unsigned)((rows + kRows * kSteps - 1) / (kRows * kSteps)); }
+// Four rows of a lane group one after the other hide the cost of a workgroup's
+// start; too few rows to give every compute unit a workgroup take one each.
+template <typename K1, typename K4, typename A>
+hipError_t forward(K1 one, K4 four, long long rows, const A& a, hipStream_t s) {
+    const bool few = rows < (long long)kRows * kSteps * 256;
+    const long long per = few ? kRows : kRows * kSteps;
+    hipLaunchKernelGGL(few ? one : four, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
 
 }  // namespace block
 
@@ -350,18 +360,16 @@ int block_out_partials(long long rows) {
 
 #define KDA_BLOCK_LAUNCH(kernel, grid, threads, ...) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, s, __VA_ARGS__)
 
-hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s) {
+template <bool F32, bool SCALAR>
+static hipError_t run_block_in(const BlockInArgs& a, hipStream_t s) {
     using namespace block;
+    return forward(kda_block_in_kernel<F32, SCALAR, 1>, kda_block_in_kernel<F32, SCALAR, kSteps>, a.tokens * a.H, a, s);
+}
+
+hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s) {
     if (a.tokens == 0) return hipSuccess;
-    const unsigned n = blocks(a.tokens * a.H);
-    if (a.f32) {
-        if (a.scalar_gate) KDA_BLOCK_LAUNCH((kda_block_in_kernel<true, true>), n, 256, a);
-        else KDA_BLOCK_LAUNCH((kda_block_in_kernel<true, false>), n, 256, a);
-    } else {
-        if (a.scalar_gate) KDA_BLOCK_LAUNCH((kda_block_in_kernel<false, true>), n, 256, a);
-        else KDA_BLOCK_LAUNCH((kda_block_in_kernel<false, false>), n, 256, a);
-    }
-    return hipGetLastError();
+    if (a.f32) return a.scalar_gate ? run_block_in<true, true>(a, s) : run_block_in<true, false>(a, s);
+    return a.scalar_gate ? run_block_in<false, true>(a, s) : run_block_in<false, false>(a, s);
 }
 
 hipError_t launch_block_in_bwd(const BlockInArgs& a, hipStream_t s) {
@@ -387,9 +395,8 @@ hipError_t launch_block_in_bwd(const BlockInArgs& a, hipStream_t s) {
 hipError_t launch_block_out(const BlockOutArgs& a, hipStream_t s) {
     using namespace block;
     if (a.rows == 0) return hipSuccess;
-    if (a.f32) KDA_BLOCK_LAUNCH(kda_block_out_kernel<true>, blocks(a.rows), 256, a);
-    else KDA_BLOCK_LAUNCH(kda_block_out_kernel<false>, blocks(a.rows), 256, a);
-    return hipGetLastError();
+    if (a.f32) return forward(kda_block_out_kernel<true, 1>, kda_block_out_kernel<true, kSteps>, a.rows, a, s);
+    return forward(kda_block_out_kernel<false, 1>, kda_block_out_kernel<false, kSteps>, a.rows, a, s);
 }
 
 hipError_t launch_block_out_bwd(const BlockOutArgs& a, hipStream_t s) {

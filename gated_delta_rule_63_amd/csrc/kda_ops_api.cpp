@@ -3,7 +3,7 @@
 // validation on the host, then kernel launches.
 #include "../../include/kda.h"
 
-#include <algorithm>
+#include <atomic>
 #include <math.h>
 #include <stdint.h>
 
@@ -32,10 +32,14 @@ kda_status_t check_desc(const kda_desc_t* d) {
 
 kda_status_t status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
 
+// Compute units of the current device, read once per device.
 int compute_units() {
+    static std::atomic<int> cache[64];
     int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess) return 256;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 256;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
+    if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
+    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 
