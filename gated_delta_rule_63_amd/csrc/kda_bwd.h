@@ -11,7 +11,9 @@ constexpr int kBwdChunk = 32;
 
 // Layouts: q, k, v, g, d_o and their gradients as in include/kda.h. A chunk of
 // a (sequence, head) has the index ch = slot * H + h; the workspace arrays
-// below are fp32 and indexed by it. "T" in a name: [channel][32 tokens].
+// below are fp32 and indexed by it. Matrices are kept as 16 x 16 tiles of 1 KiB,
+// row after row, so that a wave's fragment is one contiguous piece; "T" in a
+// name: [channel][token], tiles in the order (channel tile, token tile).
 struct BwdArgs {
     const void* q;
     const void* k;
@@ -31,13 +33,13 @@ struct BwdArgs {
     float* X;            // [32][32]
     float* b;            // [32] beta, zero behind the last token
     float* decay;        // [128] exp(sum of g over the chunk)
-    float* WT;           // [128][32]
-    float* eT;           // [128][32] first U, then e
-    float* dDT;          // [128][32] first M^T do, then dDelta
-    float* KcT;          // [128][32]
-    float* QrT;          // [128][32]
-    float* S;            // [v][k] state entering the chunk
-    float* dS;           // [v][k] gradient of the state leaving it
+    float* WT;           // 128 x 32
+    float* eT;           // 128 x 32, first U, then e
+    float* dDT;          // 128 x 32, first M^T do, then dDelta
+    float* KcT;          // 128 x 32
+    float* QrT;          // 128 x 32
+    float* S;            // 128 x 128, [v][k], tiles (v tile, k tile): state entering the chunk
+    float* dS;           // the same: gradient of the state leaving it
     int B, T, H, N, nslots;
     bool scalar_gate, f32;
 };

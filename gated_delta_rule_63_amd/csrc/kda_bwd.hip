@@ -49,12 +49,32 @@ __device__ __forceinline__ f32x4 splat(float x) { return f32x4{x, x, x, x}; }
 __device__ __forceinline__ f32x4 ld4(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
 __device__ __forceinline__ void st4(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
 
+// A workgroup barrier for what passes through LDS: loads and stores of device
+// memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // acc += A B over 16 reduction indices: lane l holds A[l % 16][4 (l / 16) + j]
 // and B[4 (l / 16) + j][l % 16] in component j.
 __device__ __forceinline__ f32x4 mma(const f32x4& a, const f32x4& b, f32x4 acc) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc = mfma16x4(a[j], b[j], acc);
     return acc;
+}
+
+// Tiles: (channel tile ct, token tile i) of a 128 x 32 matrix, (v tile, k tile)
+// of a state. Lane l's fragment of a tile: row l % 16, columns 4 (l / 16) ..
+__device__ __forceinline__ long long tile32(long long ch, int ct, int i) { return ch * (D * C) + (2 * ct + i) * 256; }
+__device__ __forceinline__ long long tileS(long long ch, int vt, int kt) { return ch * (D * D) + (8 * vt + kt) * 256; }
+// ... and its transposed fragment: column l % 16, rows 4 (l / 16) ..
+__device__ __forceinline__ f32x4 ld4t(const float* p, int r16, int g4) {
+    f32x4 x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = p[(g4 + j) * 16 + r16];
+    return x;
 }
 
 struct Chunk {
@@ -105,16 +125,28 @@ struct Gates {
     float m, G0, G1, m0, m1; // its value after 8 tokens; the sub-blocks' totals and midpoints
 };
 
+// The raw inputs of this lane's channel and half chunk, loaded ahead of use.
+struct Raw {
+    float g[16], k[16], q[16];
+};
+
 template <bool F32>
-__device__ __forceinline__ void load_gates(Gates& s, const BwdArgs& a, const Chunk& ck, int h, int c, int half) {
+__device__ __forceinline__ void load_raw(Raw& r, const BwdArgs& a, const Chunk& ck, int h, int c, int half) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int t = 16 * half + i;
         const long long th = (ck.tok + t) * a.H + h;
-        s.L[i] = t < ck.nv ? (a.scalar_gate ? a.g[th] : a.g[th * D + c]) : 0.f;
+        const bool on = t < ck.nv;
+        r.g[i] = on ? (a.scalar_gate ? a.g[th] : a.g[th * D + c]) : 0.f;
+        r.k[i] = on ? ld_in<F32>(a.k, th * D + c) : 0.f;
+        r.q[i] = on ? ld_in<F32>(a.q, th * D + c) : 0.f;
     }
+}
+
+__device__ __forceinline__ void scan_gates(Gates& s, const Raw& r, int half) {
+    s.L[0] = r.g[0];
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s.L[i] += s.L[i - 1];
+    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + r.g[i];
     s.m = s.L[7];
     const float other = __shfl_xor(s.L[15], 32), mo = __shfl_xor(s.m, 32);
     s.G0 = half ? other : s.L[15];
@@ -126,25 +158,40 @@ __device__ __forceinline__ void load_gates(Gates& s, const BwdArgs& a, const Chu
 // ------------------------------------------------------------------ 1 intra
 template <bool F32>
 __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
-    const long long ch = blockIdx.x;
-    const int slot = (int)(ch / a.H), h = (int)(ch % a.H);
+    const int slot = (int)(blockIdx.x / (unsigned)a.H), h = (int)(blockIdx.x % (unsigned)a.H);
     const Chunk ck = find_chunk(a, slot);
     if (ck.nv <= 0) return;
+    const long long ch = (long long)h * a.nslots + slot;
     __shared__ __align__(16) float Kd[C * LD], KQ[2 * C * LD];
     float *const Ki = KQ, *const Qd = KQ + C * LD;
     __shared__ __align__(16) float Bs[C * LM], Ms[C * LM], Xs[C * LM];
-    __shared__ __align__(16) float cs[D], sc[2][D], bs[C];
+    __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    // everything from memory at once: the latency of one fetch, not of three.
+    // Wave w owns channels 32 w .. 32 w + 31, one lane per channel and half chunk.
+    const int c = 32 * w + (l & 31), half = l >> 5;
+    Raw raw;
+    load_raw<F32>(raw, a, ck, h, c, half);
+    f32x4 v[2][2], d_o[2][2];   // [column tile][token tile]
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = 16 * i + g4 + j;
+                const long long at = ((ck.tok + t) * a.H + h) * D + 32 * w + 16 * ct + r16;
+                v[ct][i][j] = t < ck.nv ? ld_in<F32>(a.v, at) : 0.f;
+                d_o[ct][i][j] = t < ck.nv ? a.d_o[at] : 0.f;
+            }
     if (tid < C) {
         const float b = tid < ck.nv ? a.beta[(ck.tok + tid) * a.H + h] : 0.f;
         bs[tid] = b;
         a.b[ch * C + tid] = b;
     }
     {
-        // wave w owns channels 32 w .. 32 w + 31, one lane per channel and half chunk
-        const int c = 32 * w + (l & 31), half = l >> 5;
         Gates s;
-        load_gates<F32>(s, a, ck, h, c, half);
+        scan_gates(s, raw, half);
         const float up = expf(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
         const float dn = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
         sc[half][c] = up;
@@ -152,28 +199,33 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
             cs[c] = expf(s.m1 + s.G0 - s.m0);
             a.decay[ch * D + c] = expf(s.G0 + s.G1);
         }
-        f32x4 kc[4], qr[4];
+        sc2[half][c] = dn;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = 16 * half + i;
-            const long long at = ((ck.tok + t) * a.H + h) * D + c;
-            const float kk = t < ck.nv ? ld_in<F32>(a.k, at) : 0.f;
-            const float qq = t < ck.nv ? ld_in<F32>(a.q, at) : 0.f;
+            const float kk = raw.k[i], qq = raw.q[i];
             const float E1 = expf(s.L[i] - s.m), E2 = expf(s.m - s.L[i]);
             Kd[t * LD + c] = kk * E1;
             Ki[t * LD + c] = kk * E2;
             Qd[t * LD + c] = qq * E1;
-            kc[i >> 2][i & 3] = kk * E2 * dn;
-            qr[i >> 2][i & 3] = qq * E1 * up;
-        }
-        const long long o = (ch * D + c) * C + 16 * half;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            st4(a.KcT + o + 4 * i, kc[i]);
-            st4(a.QrT + o + 4 * i, qr[i]);
         }
     }
-    __syncthreads();
+    lds_barrier();
+    const int fr = 16 * r16 + g4;   // this lane's place in a tile
+#pragma unroll
+    for (int ct = 0; ct < 2; ++ct)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int col = 32 * w + 16 * ct + r16;
+            f32x4 kc, qr;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                kc[j] = Ki[(16 * i + g4 + j) * LD + col] * sc2[i][col];
+                qr[j] = Qd[(16 * i + g4 + j) * LD + col] * sc[i][col];
+            }
+            st4(a.KcT + tile32(ch, 2 * w + ct, i) + fr, kc);
+            st4(a.QrT + tile32(ch, 2 * w + ct, i) + fr, qr);
+        }
     // B and M, each wave over its own 32 channels: tiles (0,0), (1,1), (1,0)
     f32x4 pb[3], pm[3];
 #pragma unroll
@@ -192,14 +244,14 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         pm[1] = mma(qd1, ki1, pm[1]);
         pm[2] = mma(qd1 * x, ki0, pm[2]);
     }
-    __syncthreads();         // the partial tiles take the place of Ki and Qd
+    lds_barrier();         // the partial tiles take the place of Ki and Qd
     float* const P = KQ;     // [wave][6][64][4]: 24 of the 33 KiB
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         st4(P + ((w * 6 + i) * 64 + l) * 4, pb[i]);
         st4(P + ((w * 6 + 3 + i) * 64 + l) * 4, pm[i]);
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int i = 0; i < 6; ++i) {
         float x = 0.f;
@@ -211,7 +263,7 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         if (i < 3) Bs[t * LM + s] = t > s ? x : 0.f;
         else Ms[t * LM + s] = t >= s ? x : 0.f;
     }
-    __syncthreads();
+    lds_barrier();
     if (w == 0) {
         // X of the two diagonal blocks by substitution, one lane per column:
         // X_ts = -B_ts - sum_(s < u < t) B_tu b_u X_us
@@ -230,7 +282,7 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
             }
         }
     }
-    __syncthreads();
+    lds_barrier();
     if (w == 0) {
         // X_10 = -(I + X_11 b_1) B_10 (I + b_0 X_00)
         f32x4 y, x00;
@@ -244,7 +296,7 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) Xs[(16 + g4 + j) * LM + r16] = -x10[j];
     }
-    __syncthreads();
+    lds_barrier();
     {
         const int i = 4 * tid;
         st4(a.X + ch * (C * C) + i, ld4(Xs + (i >> 5) * LM + (i & 31)));
@@ -263,25 +315,21 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
         const int col = 32 * w + 16 * ct + r16;
-        f32x4 f0, f1, v0, v1, d0, d1;
+        const f32x4 v0 = v[ct][0], v1 = v[ct][1], d0 = d_o[ct][0], d1 = d_o[ct][1];
+        f32x4 f0, f1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t0 = g4 + j, t1 = 16 + t0;
-            const long long at = ((ck.tok + t0) * a.H + h) * D + col, at1 = at + (long long)16 * a.H * D;
-            v0[j] = t0 < ck.nv ? ld_in<F32>(a.v, at) : 0.f;
-            v1[j] = t1 < ck.nv ? ld_in<F32>(a.v, at1) : 0.f;
-            d0[j] = t0 < ck.nv ? a.d_o[at] : 0.f;
-            d1[j] = t1 < ck.nv ? a.d_o[at1] : 0.f;
             f0[j] = Kd[t0 * LD + col] * sc[0][col];
             f1[j] = Kd[t1 * LD + col] * sc[1][col];
         }
-        const long long o = (ch * D + col) * C + g4;
+        const long long o = tile32(ch, 2 * w + ct, 0) + fr;
         st4(a.WT + o, mma(x00, f0, f0));
-        st4(a.WT + o + 16, mma(x11, f1, mma(x10, f0, f1)));
+        st4(a.WT + o + 256, mma(x11, f1, mma(x10, f0, f1)));
         st4(a.eT + o, mma(x00, v0, v0));
-        st4(a.eT + o + 16, mma(x11, v1, mma(x10, v0, v1)));
+        st4(a.eT + o + 256, mma(x11, v1, mma(x10, v0, v1)));
         st4(a.dDT + o, mma(m10, d1, mma(m00, d0, splat(0.f))));
-        st4(a.dDT + o + 16, mma(m11, d1, splat(0.f)));
+        st4(a.dDT + o + 256, mma(m11, d1, splat(0.f)));
     }
 }
 
@@ -317,12 +365,42 @@ __device__ __forceinline__ Walk find_walk(const BwdArgs& a) {
     return r;
 }
 
+// A chunk's operands for the walk forwards, fetched a chunk ahead: a step is
+// shorter than a fetch from memory.
+template <int NV>
+struct Fwd {
+    f32x4 W[2][2], Kc[2][2], dec[2], b[2], U[(2 * NV + 3) / 4];
+};
+
+template <int NV>
+__device__ __forceinline__ void fetch(Fwd<NV>& x, const BwdArgs& a, long long ch, int w, int r16, int g4, int v0) {
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x.W[i][kt] = ld4t(a.WT + tile32(ch, 2 * w + kt, i), r16, g4);
+    }
+#pragma unroll
+    for (int tile = 0; tile < 2 * NV; ++tile)
+        if ((tile & 3) == w)
+            x.U[tile / 4] = ld4(a.eT + tile32(ch, v0 / 16 + tile % NV, tile / NV) + 16 * r16 + g4);
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x.Kc[i][kt] = ld4(a.KcT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
+        x.dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) x.b[i] = ld4(a.b + ch * C + 16 * i + g4);
+}
+
 template <int NV>
 __global__ __launch_bounds__(256) void kda_bwd_states(BwdArgs a) {
     const Walk wk = find_walk<NV>(a);
-    if (!wk.on) return;
+    if (!wk.on || wk.nc == 0) return;
     __shared__ __align__(16) float P[2][4][2 * NV][64][4];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
+    Fwd<NV> next;
+    fetch<NV>(next, a, (long long)wk.h * a.nslots + wk.first, w, r16, g4, wk.v0);
     f32x4 S[2][NV];
     const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
 #pragma unroll
@@ -333,48 +411,75 @@ __global__ __launch_bounds__(256) void kda_bwd_states(BwdArgs a) {
             for (int j = 0; j < 4; ++j)
                 S[kt][nv][j] = a.h0 ? a.h0[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
     for (int c = 0; c < wk.nc; ++c) {
-        const long long ch = (long long)(wk.first + c) * a.H + wk.h;
-        f32x4 W[2][2], Kc[2][2], dec[2], b[2];
+        const long long ch = (long long)wk.h * a.nslots + wk.first + c;
+        const Fwd<NV> x = next;
+        if (c + 1 < wk.nc) fetch<NV>(next, a, ch + 1, w, r16, g4, wk.v0);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            const int k0 = 32 * w + 16 * kt;
-            dec[kt] = ld4(a.decay + ch * D + k0 + g4);
+        for (int nv = 0; nv < NV; ++nv)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) W[i][kt][j] = a.WT[(ch * D + k0 + g4 + j) * C + 16 * i + r16];
-                Kc[i][kt] = ld4(a.KcT + (ch * D + k0 + r16) * C + 16 * i + g4);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) b[i] = ld4(a.b + ch * C + 16 * i + g4);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int nv = 0; nv < NV; ++nv)
-                st4(a.S + ch * (D * D) + (wk.v0 + 16 * nv + r16) * D + 32 * w + 16 * kt + g4, S[kt][nv]);
+            for (int kt = 0; kt < 2; ++kt)
+                st4(a.S + tileS(ch, wk.v0 / 16 + nv, 2 * w + kt) + 16 * r16 + g4, S[kt][nv]);
 #pragma unroll
         for (int tile = 0; tile < 2 * NV; ++tile) {
             const int i = tile / NV, nv = tile % NV;
-            f32x4 p = mma(W[i][1], S[1][nv], mma(W[i][0], S[0][nv], splat(0.f)));
-            if ((tile & 3) == w) p -= ld4(a.eT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4);
+            f32x4 p = mma(x.W[i][1], S[1][nv], mma(x.W[i][0], S[0][nv], splat(0.f)));
+            if ((tile & 3) == w) p -= x.U[tile / 4];
             st4(P[c & 1][w][tile][l], p);
         }
-        __syncthreads();
+        lds_barrier();
         f32x4 e[2][NV];
 #pragma unroll
         for (int tile = 0; tile < 2 * NV; ++tile) {
             const int i = tile / NV, nv = tile % NV;
-            const f32x4 x = -(ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) +
+            const f32x4 y = -(ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) +
                               ld4(P[c & 1][2][tile][l]) + ld4(P[c & 1][3][tile][l]));
-            if ((tile & 3) == w) st4(a.eT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4, x);
-            e[i][nv] = x * b[i];
+            if ((tile & 3) == w) st4(a.eT + tile32(ch, wk.v0 / 16 + nv, i) + 16 * r16 + g4, y);
+            e[i][nv] = y * x.b[i];
         }
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int nv = 0; nv < NV; ++nv)
-                S[kt][nv] = mma(Kc[1][kt], e[1][nv], mma(Kc[0][kt], e[0][nv], S[kt][nv] * dec[kt]));
+                S[kt][nv] = mma(x.Kc[1][kt], e[1][nv], mma(x.Kc[0][kt], e[0][nv], S[kt][nv] * x.dec[kt]));
+    }
+}
+
+template <int NV>
+struct Bwd {
+    f32x4 W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], d_o[2][NV], dD[(2 * NV + 3) / 4];
+};
+
+template <int NV>
+__device__ __forceinline__ void fetch(Bwd<NV>& x, const BwdArgs& a, const Walk& wk, int c, int T1, int w, int r16, int g4) {
+    const long long ch = (long long)wk.h * a.nslots + wk.first + c;
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x.Kc[i][kt] = ld4t(a.KcT + tile32(ch, 2 * w + kt, i), r16, g4);
+    }
+#pragma unroll
+    for (int tile = 0; tile < 2 * NV; ++tile)
+        if ((tile & 3) == w)
+            x.dD[tile / 4] = ld4(a.dDT + tile32(ch, wk.v0 / 16 + tile % NV, tile / NV) + 16 * r16 + g4);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        x.b[i] = ld4(a.b + ch * C + 16 * i + g4);
+#pragma unroll
+        for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int t = c * C + 16 * i + g4 + j;
+                x.d_o[i][nv][j] = t < T1 ? a.d_o[((wk.tok + t) * a.H + wk.h) * D + wk.v0 + 16 * nv + r16] : 0.f;
+            }
+    }
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+        x.dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            x.W[i][kt] = ld4(a.WT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
+            x.Qr[i][kt] = ld4(a.QrT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
+        }
     }
 }
 
@@ -392,6 +497,8 @@ __global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
         seq_range(a, wk.n, t0, T1);
         T1 -= t0;
     }
+    Bwd<NV> next;
+    if (wk.nc > 0) fetch<NV>(next, a, wk, wk.nc - 1, T1, w, r16, g4);
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -400,62 +507,42 @@ __global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
             for (int j = 0; j < 4; ++j)
                 S[kt][nv][j] = a.dhT ? a.dhT[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
     for (int c = wk.nc - 1; c >= 0; --c) {
-        const long long ch = (long long)(wk.first + c) * a.H + wk.h;
-        f32x4 W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], d_o[2][NV];
+        const long long ch = (long long)wk.h * a.nslots + wk.first + c;
+        const Bwd<NV> x = next;
+        if (c > 0) fetch<NV>(next, a, wk, c - 1, T1, w, r16, g4);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            const int k0 = 32 * w + 16 * kt;
-            dec[kt] = ld4(a.decay + ch * D + k0 + g4);
+        for (int nv = 0; nv < NV; ++nv)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int kt = 0; kt < 2; ++kt)
+                st4(a.dS + tileS(ch, wk.v0 / 16 + nv, 2 * w + kt) + 16 * r16 + g4, S[kt][nv]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) Kc[i][kt][j] = a.KcT[(ch * D + k0 + g4 + j) * C + 16 * i + r16];
-                W[i][kt] = ld4(a.WT + (ch * D + k0 + r16) * C + 16 * i + g4);
-                Qr[i][kt] = ld4(a.QrT + (ch * D + k0 + r16) * C + 16 * i + g4);
-            }
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            f32x4 p = mma(x.Kc[i][1], S[1][nv], mma(x.Kc[i][0], S[0][nv], splat(0.f)));
+            if ((tile & 3) == w) p += x.dD[tile / 4];
+            st4(P[c & 1][w][tile][l], p);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            b[i] = ld4(a.b + ch * C + 16 * i + g4);
-#pragma unroll
-            for (int nv = 0; nv < NV; ++nv)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int t = c * C + 16 * i + g4 + j;
-                    d_o[i][nv][j] = t < T1 ? a.d_o[((wk.tok + t) * a.H + wk.h) * D + wk.v0 + 16 * nv + r16] : 0.f;
-                }
-        }
+        // the part of the update that does not wait for dD
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
             for (int nv = 0; nv < NV; ++nv)
-                st4(a.dS + ch * (D * D) + (wk.v0 + 16 * nv + r16) * D + 32 * w + 16 * kt + g4, S[kt][nv]);
-#pragma unroll
-        for (int tile = 0; tile < 2 * NV; ++tile) {
-            const int i = tile / NV, nv = tile % NV;
-            f32x4 p = mma(Kc[i][1], S[1][nv], mma(Kc[i][0], S[0][nv], splat(0.f)));
-            if ((tile & 3) == w) p += ld4(a.dDT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4);
-            st4(P[c & 1][w][tile][l], p);
-        }
-        __syncthreads();
+                S[kt][nv] = mma(x.Qr[1][kt], x.d_o[1][nv], mma(x.Qr[0][kt], x.d_o[0][nv], S[kt][nv] * x.dec[kt]));
+        lds_barrier();
         f32x4 dd[2][NV];
 #pragma unroll
         for (int tile = 0; tile < 2 * NV; ++tile) {
             const int i = tile / NV, nv = tile % NV;
-            const f32x4 x = ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) + ld4(P[c & 1][2][tile][l]) +
+            const f32x4 y = ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) + ld4(P[c & 1][2][tile][l]) +
                             ld4(P[c & 1][3][tile][l]);
-            if ((tile & 3) == w) st4(a.dDT + (ch * D + wk.v0 + 16 * nv + r16) * C + 16 * i + g4, x);
-            dd[i][nv] = -(x * b[i]);
+            if ((tile & 3) == w) st4(a.dDT + tile32(ch, wk.v0 / 16 + nv, i) + 16 * r16 + g4, y);
+            dd[i][nv] = -(y * x.b[i]);
         }
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-            for (int nv = 0; nv < NV; ++nv) {
-                f32x4 x = S[kt][nv] * dec[kt];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) x = mma(W[i][kt], dd[i][nv], mma(Qr[i][kt], d_o[i][nv], x));
-                S[kt][nv] = x;
-            }
+            for (int nv = 0; nv < NV; ++nv)
+                S[kt][nv] = mma(x.W[1][kt], dd[1][nv], mma(x.W[0][kt], dd[0][nv], S[kt][nv]));
     }
     if (a.dh0)
 #pragma unroll
@@ -475,11 +562,11 @@ __device__ __forceinline__ void st_out(void* p, long long i, float x) {
 }
 
 template <bool F32>
-__global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
-    const long long ch = blockIdx.x;
-    const int slot = (int)(ch / a.H), h = (int)(ch % a.H);
+__global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
+    const int slot = (int)(blockIdx.x / (unsigned)a.H), h = (int)(blockIdx.x % (unsigned)a.H);
     const Chunk ck = find_chunk(a, slot);
     if (ck.nv <= 0) return;
+    const long long ch = (long long)h * a.nslots + slot;
     // first do, rho, e as [token][v]; then E1, k, q as [token][k]
     __shared__ __align__(16) float R0[C * LD], R1[C * LD], R2[C * LD];
     __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM];
@@ -495,7 +582,7 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
         if (t < ck.nv) x = ld4(a.d_o + at);
         st4(R0 + t * LD + c, x);
     }
-    __syncthreads();
+    lds_barrier();
     const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
     {
         f32x4 x00, x10, x11; // transposed
@@ -508,9 +595,9 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
             const int col = 32 * w + 16 * ct + r16;
-            const long long o = (ch * D + col) * C + g4;
-            const f32x4 d0 = ld4(a.dDT + o), d1 = ld4(a.dDT + o + 16);
-            const f32x4 e0 = ld4(a.eT + o), e1 = ld4(a.eT + o + 16);
+            const long long o = tile32(ch, 2 * w + ct, 0) + 16 * r16 + g4;
+            const f32x4 d0 = ld4(a.dDT + o), d1 = ld4(a.dDT + o + 256);
+            const f32x4 e0 = ld4(a.eT + o), e1 = ld4(a.eT + o + 256);
             const f32x4 p0 = mma(x10, d1 * b1, mma(x00, d0 * b0, d0)), p1 = mma(x11, d1 * b1, d1);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -525,7 +612,7 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
             }
         }
     }
-    __syncthreads();
+    lds_barrier();
     // dM, dB and dbeta from do e^T and rho e^T: tiles (0,0), (1,1), (1,0) of each
     for (int i = w; i < 6; i += 4) {
         const int tile = i % 3, ro = tile ? 16 : 0, co = tile == 1 ? 16 : 0;
@@ -553,18 +640,26 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt) qS[i][kt] = rS[i][kt] = eS[i][kt] = splat(0.f);
-    const float* Sp = a.S + ch * (D * D) + g4 * D + 32 * w + r16;
-    const float* dSp = a.dS + ch * (D * D) + g4 * D + 32 * w + r16;
-#pragma unroll 2
+    const float* Sp = a.S + tileS(ch, 0, 2 * w);
+    const float* dSp = a.dS + tileS(ch, 0, 2 * w);
+    f32x4 sn[2], dsn[2];     // 16 columns of v ahead
+    const auto load_states = [&](int vb) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+            sn[kt] = ld4t(Sp + (8 * vb + kt) * 256, r16, g4);
+            dsn[kt] = ld4t(dSp + (8 * vb + kt) * 256, r16, g4);
+        }
+    };
+    load_states(0);
+#pragma unroll
     for (int vb = 0; vb < 8; ++vb) {
         f32x4 s[2], ds[2];
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[kt][j] = Sp[(16 * vb + j) * D + 16 * kt];
-                ds[kt][j] = dSp[(16 * vb + j) * D + 16 * kt];
-            }
+        for (int kt = 0; kt < 2; ++kt) {
+            s[kt] = sn[kt];
+            ds[kt] = dsn[kt];
+        }
+        if (vb < 7) load_states(vb + 1);
 #pragma unroll
         for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -581,11 +676,13 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
             }
         }
     }
-    __syncthreads();
+    lds_barrier();
     {
         const int c = 32 * w + (l & 31), half = l >> 5;
+        Raw raw;
+        load_raw<F32>(raw, a, ck, h, c, half);
         Gates s;
-        load_gates<F32>(s, a, ck, h, c, half);
+        scan_gates(s, raw, half);
         up[half][c] = expf(s.m + (half ? s.G0 : 0.f));
         dn[half][c] = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
         if (half == 0) {
@@ -595,13 +692,12 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int t = 16 * half + i;
-            const long long at = ((ck.tok + t) * a.H + h) * D + c;
             R0[t * LD + c] = expf(s.L[i] - s.m);
-            R1[t * LD + c] = t < ck.nv ? ld_in<F32>(a.k, at) : 0.f;
-            R2[t * LD + c] = t < ck.nv ? ld_in<F32>(a.q, at) : 0.f;
+            R1[t * LD + c] = raw.k[i];
+            R2[t * LD + c] = raw.q[i];
         }
     }
-    __syncthreads();
+    lds_barrier();
     const f32x4 M00 = ld4(dMs + r16 * LM + g4), M10 = ld4(dMs + (16 + r16) * LM + g4),
                 M11 = ld4(dMs + (16 + r16) * LM + 16 + g4);
     const f32x4 N00 = ld4(dBs + r16 * LM + g4), N10 = ld4(dBs + (16 + r16) * LM + g4),
@@ -706,7 +802,7 @@ __global__ __launch_bounds__(256) void kda_bwd_grads(BwdArgs a) {
                 for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
                 if (r16 == 0) part[w][16 * i + g4 + j] = x;
             }
-        __syncthreads();
+        lds_barrier();
         if (tid < ck.nv) a.dg[(ck.tok + tid) * a.H + h] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
     }
 }
@@ -734,7 +830,7 @@ static hipError_t run_bwd(const BwdArgs& a, hipStream_t s) {
 
 hipError_t launch_bwd(const BwdArgs& a, int cus, hipStream_t s) {
     (void)cus;
-    return a.f32 ? run_bwd<true, 2>(a, s) : run_bwd<false, 2>(a, s);
+    return a.f32 ? run_bwd<true, 1>(a, s) : run_bwd<false, 1>(a, s);
 }
 
 }  // namespace kda
