@@ -125,28 +125,80 @@ struct Gates {
     float m, G0, G1, m0, m1; // its value after 8 tokens; the sub-blocks' totals and midpoints
 };
 
-// The raw inputs of this lane's channel and half chunk, loaded ahead of use.
-struct Raw {
-    float g[16], k[16], q[16];
+// Rows of a [tokens, H, 128] tensor, one chunk of them: 16 bytes a lane and
+// whole rows a few lanes, held in registers until LDS is ready for them.
+// (Loads of one channel a lane touch every line several times from several
+// waves; with them alone a kernel took twice as long.)
+template <bool F32>
+struct Rows {
+    uint4 x[F32 ? 4 : 2];
 };
 
 template <bool F32>
-__device__ __forceinline__ void load_raw(Raw& r, const BwdArgs& a, const Chunk& ck, int h, int c, int half) {
+__device__ __forceinline__ void load_rows(Rows<F32>& r, const void* p, const BwdArgs& a, const Chunk& ck, int h, int tid) {
+    constexpr int per = F32 ? 32 : 16, bytes = F32 ? 4 : 2;   // pieces a row
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int t = 16 * half + i;
-        const long long th = (ck.tok + t) * a.H + h;
-        const bool on = t < ck.nv;
-        r.g[i] = on ? (a.scalar_gate ? a.g[th] : a.g[th * D + c]) : 0.f;
-        r.k[i] = on ? ld_in<F32>(a.k, th * D + c) : 0.f;
-        r.q[i] = on ? ld_in<F32>(a.q, th * D + c) : 0.f;
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
+        r.x[i] = make_uint4(0, 0, 0, 0);
+        if (t < ck.nv)
+            r.x[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
+                                                     (((ck.tok + t) * a.H + h) * D) * bytes + 16 * c);
     }
 }
 
-__device__ __forceinline__ void scan_gates(Gates& s, const Raw& r, int half) {
-    s.L[0] = r.g[0];
+template <bool F32>
+__device__ __forceinline__ void put_rows(const Rows<F32>& r, float* to, int tid) {
+    constexpr int per = F32 ? 32 : 16;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + r.g[i];
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
+        const uint4 u = r.x[i];
+        if constexpr (F32) {
+            *reinterpret_cast<uint4*>(to + t * LD + 4 * c) = u;
+        } else {
+            st4(to + t * LD + 8 * c, f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                           __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u)});
+            st4(to + t * LD + 8 * c + 4, f32x4{__uint_as_float(u.z << 16), __uint_as_float(u.z & 0xffff0000u),
+                                               __uint_as_float(u.w << 16), __uint_as_float(u.w & 0xffff0000u)});
+        }
+    }
+}
+
+// The way back: rows of LDS, each scaled by its token's `by` (nullptr: 1). The
+// gradient of a bf16 tensor is rounded once, here.
+template <bool F32>
+__device__ __forceinline__ void store_rows(void* p, const float* from, const float* by, const BwdArgs& a,
+                                           const Chunk& ck, int h, int tid) {
+    constexpr int per = F32 ? 32 : 16, bytes = F32 ? 4 : 2;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
+        if (t >= ck.nv) continue;
+        const float f = by ? by[t] : 1.f;
+        char* const to = static_cast<char*>(p) + (((ck.tok + t) * a.H + h) * D) * bytes + 16 * c;
+        if constexpr (F32) {
+            *reinterpret_cast<f32x4*>(to) = ld4(from + t * LD + 4 * c) * f;
+        } else {
+            const f32x4 x = ld4(from + t * LD + 8 * c) * f, y = ld4(from + t * LD + 8 * c + 4) * f;
+            const bf16x2 u[4] = {{(__bf16)x[0], (__bf16)x[1]}, {(__bf16)x[2], (__bf16)x[3]},
+                                 {(__bf16)y[0], (__bf16)y[1]}, {(__bf16)y[2], (__bf16)y[3]}};
+            *reinterpret_cast<uint4*>(to) = __builtin_bit_cast(uint4, u);
+        }
+    }
+}
+
+// The gates of this lane's channel and half chunk: G holds them as rows, gs
+// one per token (scalar gate).
+__device__ __forceinline__ void read_gates(float (&g)[16], const BwdArgs& a, const float* G, const float* gs, int c, int half) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) g[i] = a.scalar_gate ? gs[16 * half + i] : G[(16 * half + i) * LD + c];
+}
+
+__device__ __forceinline__ void scan_gates(Gates& s, const float (&g)[16], int half) {
+    s.L[0] = g[0];
+#pragma unroll
+    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + g[i];
     s.m = s.L[7];
     const float other = __shfl_xor(s.L[15], 32), mo = __shfl_xor(s.m, 32);
     s.G0 = half ? other : s.L[15];
@@ -165,49 +217,49 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     __shared__ __align__(16) float Kd[C * LD], KQ[2 * C * LD];
     float *const Ki = KQ, *const Qd = KQ + C * LD;
     __shared__ __align__(16) float Bs[C * LM], Ms[C * LM], Xs[C * LM];
-    __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C];
+    __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C], gs[C];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
-    // everything from memory at once: the latency of one fetch, not of three.
-    // Wave w owns channels 32 w .. 32 w + 31, one lane per channel and half chunk.
-    const int c = 32 * w + (l & 31), half = l >> 5;
-    Raw raw;
-    load_raw<F32>(raw, a, ck, h, c, half);
-    f32x4 v[2][2], d_o[2][2];   // [column tile][token tile]
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 16 * i + g4 + j;
-                const long long at = ((ck.tok + t) * a.H + h) * D + 32 * w + 16 * ct + r16;
-                v[ct][i][j] = t < ck.nv ? ld_in<F32>(a.v, at) : 0.f;
-                d_o[ct][i][j] = t < ck.nv ? a.d_o[at] : 0.f;
-            }
+    // everything from memory at once: the latency of one fetch, not of three
+    Rows<F32> rk, rq, rv;
+    Rows<true> rg, rd;
+    load_rows<F32>(rk, a.k, a, ck, h, tid);
+    load_rows<F32>(rq, a.q, a, ck, h, tid);
+    if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
+    load_rows<F32>(rv, a.v, a, ck, h, tid);
+    load_rows<true>(rd, a.d_o, a, ck, h, tid);
     if (tid < C) {
         const float b = tid < ck.nv ? a.beta[(ck.tok + tid) * a.H + h] : 0.f;
         bs[tid] = b;
         a.b[ch * C + tid] = b;
+        if (a.scalar_gate) gs[tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
     }
+    put_rows<F32>(rk, Kd, tid);
+    put_rows<F32>(rq, Qd, tid);
+    if (!a.scalar_gate) put_rows<true>(rg, Ki, tid);
+    lds_barrier();
     {
+        // wave w owns channels 32 w .. 32 w + 31, one lane per channel and half
+        // chunk; it turns k, q and g into Kd, Qd and Ki in place
+        const int c = 32 * w + (l & 31), half = l >> 5;
+        float g[16];
+        read_gates(g, a, Ki, gs, c, half);
         Gates s;
-        scan_gates(s, raw, half);
+        scan_gates(s, g, half);
         const float up = expf(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
         const float dn = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
         sc[half][c] = up;
+        sc2[half][c] = dn;
         if (half == 0) {
             cs[c] = expf(s.m1 + s.G0 - s.m0);
             a.decay[ch * D + c] = expf(s.G0 + s.G1);
         }
-        sc2[half][c] = dn;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int t = 16 * half + i;
-            const float kk = raw.k[i], qq = raw.q[i];
-            const float E1 = expf(s.L[i] - s.m), E2 = expf(s.m - s.L[i]);
-            Kd[t * LD + c] = kk * E1;
-            Ki[t * LD + c] = kk * E2;
-            Qd[t * LD + c] = qq * E1;
+            const int o = (16 * half + i) * LD + c;
+            const float kk = Kd[o], E1 = expf(s.L[i] - s.m), E2 = expf(s.m - s.L[i]);
+            Kd[o] = kk * E1;
+            Ki[o] = kk * E2;
+            Qd[o] *= E1;
         }
     }
     lds_barrier();
@@ -264,6 +316,9 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         else Ms[t * LM + s] = t >= s ? x : 0.f;
     }
     lds_barrier();
+    float *const Vs = KQ, *const Ds = KQ + C * LD;   // the parts have been summed: v and do take their place
+    put_rows<F32>(rv, Vs, tid);
+    put_rows<true>(rd, Ds, tid);
     if (w == 0) {
         // X of the two diagonal blocks by substitution, one lane per column:
         // X_ts = -B_ts - sum_(s < u < t) B_tu b_u X_us
@@ -315,11 +370,14 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
         const int col = 32 * w + 16 * ct + r16;
-        const f32x4 v0 = v[ct][0], v1 = v[ct][1], d0 = d_o[ct][0], d1 = d_o[ct][1];
-        f32x4 f0, f1;
+        f32x4 f0, f1, v0, v1, d0, d1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const int t0 = g4 + j, t1 = 16 + t0;
+            v0[j] = Vs[t0 * LD + col];
+            v1[j] = Vs[t1 * LD + col];
+            d0[j] = Ds[t0 * LD + col];
+            d1[j] = Ds[t1 * LD + col];
             f0[j] = Kd[t0 * LD + col] * sc[0][col];
             f1[j] = Kd[t1 * LD + col] * sc[1][col];
         }
@@ -556,12 +614,6 @@ __global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
 
 // ------------------------------------------------------------------ 4 grads
 template <bool F32>
-__device__ __forceinline__ void st_out(void* p, long long i, float x) {
-    if constexpr (F32) static_cast<float*>(p)[i] = x;
-    else static_cast<__bf16*>(p)[i] = (__bf16)x;   // the gradient of a bf16 tensor: rounded once, here
-}
-
-template <bool F32>
 __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     const int slot = (int)(blockIdx.x / (unsigned)a.H), h = (int)(blockIdx.x % (unsigned)a.H);
     const Chunk ck = find_chunk(a, slot);
@@ -574,13 +626,10 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     if (tid < C) bs[tid] = a.b[ch * C + tid];
     st4(Xs + (tid >> 3) * LM + 4 * (tid & 7), ld4(a.X + ch * (C * C) + 4 * tid));
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int t = (tid >> 5) + 8 * i, c = 4 * (tid & 31);
-        f32x4 x = splat(0.f);
-        const long long at = ((ck.tok + t) * a.H + h) * D + c;
-        if (t < ck.nv) x = ld4(a.d_o + at);
-        st4(R0 + t * LD + c, x);
+    {
+        Rows<true> rd;
+        load_rows<true>(rd, a.d_o, a, ck, h, tid);
+        put_rows<true>(rd, R0, tid);
     }
     lds_barrier();
     const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
@@ -606,13 +655,11 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
                 R1[t1 * LD + col] = p1[j];
                 R2[t0 * LD + col] = e0[j];
                 R2[t1 * LD + col] = e1[j];
-                const long long at = ((ck.tok + t0) * a.H + h) * D + col;
-                if (t0 < ck.nv) st_out<F32>(a.dv, at, b0[j] * p0[j]);
-                if (t1 < ck.nv) st_out<F32>(a.dv, at + (long long)16 * a.H * D, b1[j] * p1[j]);
             }
         }
     }
     lds_barrier();
+    store_rows<F32>(a.dv, R1, bs, a, ck, h, tid);
     // dM, dB and dbeta from do e^T and rho e^T: tiles (0,0), (1,1), (1,0) of each
     for (int i = w; i < 6; i += 4) {
         const int tile = i % 3, ro = tile ? 16 : 0, co = tile == 1 ? 16 : 0;
@@ -651,7 +698,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
         }
     };
     load_states(0);
-#pragma unroll
+#pragma unroll 2
     for (int vb = 0; vb < 8; ++vb) {
         f32x4 s[2], ds[2];
 #pragma unroll
@@ -678,11 +725,23 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     }
     lds_barrier();
     {
+        Rows<F32> rk, rq;
+        Rows<true> rg;
+        if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
+        load_rows<F32>(rk, a.k, a, ck, h, tid);
+        load_rows<F32>(rq, a.q, a, ck, h, tid);
+        if (a.scalar_gate && tid < C) part[0][tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
+        if (!a.scalar_gate) put_rows<true>(rg, R0, tid);
+        put_rows<F32>(rk, R1, tid);
+        put_rows<F32>(rq, R2, tid);
+    }
+    lds_barrier();
+    {
         const int c = 32 * w + (l & 31), half = l >> 5;
-        Raw raw;
-        load_raw<F32>(raw, a, ck, h, c, half);
+        float g[16];
+        read_gates(g, a, R0, part[0], c, half);
         Gates s;
-        scan_gates(s, raw, half);
+        scan_gates(s, g, half);
         up[half][c] = expf(s.m + (half ? s.G0 : 0.f));
         dn[half][c] = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
         if (half == 0) {
@@ -690,12 +749,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
             dec[c] = expf(s.G0 + s.G1);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int t = 16 * half + i;
-            R0[t * LD + c] = expf(s.L[i] - s.m);
-            R1[t * LD + c] = raw.k[i];
-            R2[t * LD + c] = raw.q[i];
-        }
+        for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = expf(s.L[i] - s.m);
     }
     lds_barrier();
     const f32x4 M00 = ld4(dMs + r16 * LM + g4), M10 = ld4(dMs + (16 + r16) * LM + g4),
@@ -750,12 +804,9 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 end += kk[i][j] * cy[j];
-                const int t = 16 * i + g4 + j;
-                const long long at = ((ck.tok + t) * a.H + h) * D + col;
-                if (t < ck.nv) {
-                    st_out<F32>(a.dq, at, q_[j]);
-                    st_out<F32>(a.dk, at, r_[j] + c_[j]);
-                }
+                const int o = (16 * i + g4 + j) * LD + col;   // k and q of this place have been read
+                R1[o] = r_[j] + c_[j];
+                R2[o] = q_[j];
             }
         }
         end += dec[col] * sd[ct];
@@ -786,12 +837,13 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
                 continue;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = 16 * i + g4 + j;
-                if (t < ck.nv) a.dg[((ck.tok + t) * a.H + h) * D + col] = dG[i][j];
-            }
+            for (int j = 0; j < 4; ++j) R0[(16 * i + g4 + j) * LD + col] = dG[i][j];
         }
     }
+    lds_barrier();
+    store_rows<F32>(a.dk, R1, nullptr, a, ck, h, tid);
+    store_rows<F32>(a.dq, R2, nullptr, a, ck, h, tid);
+    if (!a.scalar_gate) store_rows<true>(a.dg, R0, nullptr, a, ck, h, tid);
     if (a.scalar_gate) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)

@@ -38,7 +38,9 @@ kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, 
     if (st != KDA_OK) return st;
     if ((long long)d->B * d->T > 0 && (!dq || !dk || !dv || !dg || !dbeta)) return KDA_ERR_NULL;
     if (!shape_ok(d)) return KDA_ERR_SHAPE;
-    if (!aligned16(d_o)) return KDA_ERR_UNSUPPORTED;
+    for (const void* p : {q, k, v, (const void*)d_o, (const void*)dq, (const void*)dk, (const void*)dv})
+        if (!aligned16(p)) return KDA_ERR_UNSUPPORTED;
+    if (!scalar_gate && (!aligned16(g) || !aligned16(dg))) return KDA_ERR_UNSUPPORTED;
     const size_t need = kda_bwd_workspace_size(d);
     if (need > 0 && (!d->workspace || d->workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (!aligned16(d->workspace)) return KDA_ERR_UNSUPPORTED;
