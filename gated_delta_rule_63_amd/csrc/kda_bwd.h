@@ -48,7 +48,7 @@ struct BwdArgs {
 // floor(T / 32) + N, sequence n starting at slot floor(cu[n] / 32) + n.
 long long bwd_slots(int B, int T, int N, bool varlen);
 
-// The four kernels in order.
+// The three kernels in order.
 hipError_t launch_bwd(const BwdArgs& a, int cus, hipStream_t stream);
 
 }  // namespace kda

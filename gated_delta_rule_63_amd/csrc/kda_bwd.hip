@@ -20,12 +20,11 @@
 //        + rowsum(e^G_last S dS')
 // The form with X divides by no beta, so beta = 0 is an ordinary value.
 //
-// Four kernels. Only the two state walks are sequential, and both split over
+// Three kernels. Only the two state walks are sequential, and both split over
 // the columns of V, which the recurrence never mixes:
-//   1 intra   per (chunk, head): X, W, U, M^T do, kc, qr
-//   2 states  per (sequence, head, V-block), forwards: S, e
-//   3 dstates per (sequence, head, V-block), backwards: dS, dD
-//   4 grads   per (chunk, head): everything else
+//   1 intra  per (chunk, head): X, W, U, M^T do, kc, qr
+//   2 walks  per (sequence, head, V-block), forwards: S, e; backwards: dS, dD
+//   3 grads  per (chunk, head): everything else
 // All products run on the fp32 matrix instruction (16x16x4): gradients of fp32
 // leaves (g, beta, the states) come out with fp32 accuracy, and dg is a sum of
 // differences that cancel, where 16-bit operands would leave an error of 1e-3.
@@ -391,25 +390,38 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     }
 }
 
-// ----------------------------------------------------- 2 states, 3 dstates
-// One workgroup per (sequence, head, 16 NV columns of V). Wave w holds rows
-// 32 w .. 32 w + 31 of the state as accumulators (row = channel k, column =
-// v); as such they are also the right operand of the product with W (or kc),
-// of which each wave forms the part of its own channels. The parts meet in
-// LDS, and every wave sums them into the operand of the state's update: one
-// barrier a chunk. A chain's V-blocks run on one XCD, whose L2 serves W, kc
-// and qr to all of them.
+// ----------------------------------------------------------------- 2 walks
+// One workgroup per direction, (sequence, head) and 16 NV columns of V. Wave w
+// holds rows 32 w .. 32 w + 31 of the state as accumulators (row = channel k,
+// column = v); as such they are also the right operand of the product with W
+// (or kc), of which each wave forms the part of its own channels. The parts
+// meet in LDS, and every wave sums them into the operand of the state's
+// update: one barrier a chunk.
+//
+// A chain is a long dependent walk, so what counts is how many of them share
+// a compute unit. The walks forwards and backwards do not need each other and
+// run in one launch: with NV = 2, 96 chains are 768 workgroups, three on
+// every compute unit (registers and LDS are held to that), where one launch
+// after the other left units with one workgroup beside units with two
+// (T = 8192, H = 96: 913 + 1260 us apart, see the table below together).
+// A chain's V-blocks run on one XCD, whose L2 serves W, kc and qr to all.
+//
+// Operands are fetched for the next chunk as soon as this chunk's have been
+// used. Fetches are unconditional (behind the last chunk they fetch it again):
+// loads are waited for by count, and where paths with and without them meet
+// the smaller count holds, which would wait for the fetches just begun.
 struct Walk {
-    int n, h, v0, first, nc;
-    long long tok;
+    int n, h, v0, nc;
+    long long ch0, tok;      // first chunk; first token
+    int len;                 // tokens
     bool on;
 };
 
 template <int NV>
-__device__ __forceinline__ Walk find_walk(const BwdArgs& a) {
+__device__ __forceinline__ Walk find_walk(const BwdArgs& a, int block) {
     constexpr int nb = D / (16 * NV);
     Walk r;
-    const int xcd = blockIdx.x & 7, i = blockIdx.x >> 3;
+    const int xcd = block & 7, i = block >> 3;
     const int chain = (i / nb) * 8 + xcd;
     r.on = chain < a.N * a.H;
     r.v0 = (i % nb) * 16 * NV;
@@ -417,190 +429,224 @@ __device__ __forceinline__ Walk find_walk(const BwdArgs& a) {
     r.h = chain - r.n * a.H;
     int t0 = 0, t1 = a.T;
     if (r.on && a.cu) seq_range(a, r.n, t0, t1);
-    r.nc = (t1 - t0 + C - 1) / C;
-    r.first = a.cu ? t0 / C + r.n : r.n * r.nc;
+    r.len = t1 - t0;
+    r.nc = (r.len + C - 1) / C;
+    r.ch0 = (long long)r.h * a.nslots + (a.cu ? t0 / C + r.n : r.n * r.nc);
     r.tok = a.cu ? t0 : (long long)r.n * a.T;
     return r;
 }
 
-// A chunk's operands for the walk forwards, fetched a chunk ahead: a step is
-// shorter than a fetch from memory.
+// Of the 2 NV tiles of e (or dD), tile 4 o + w is wave w's to add U to and to
+// store; with NV = 1 waves 2 and 3 have none.
 template <int NV>
-struct Fwd {
-    f32x4 W[2][2], Kc[2][2], dec[2], b[2], U[(2 * NV + 3) / 4];
-};
-
+constexpr int kOwn = (2 * NV + 3) / 4;
 template <int NV>
-__device__ __forceinline__ void fetch(Fwd<NV>& x, const BwdArgs& a, long long ch, int w, int r16, int g4, int v0) {
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) x.W[i][kt] = ld4t(a.WT + tile32(ch, 2 * w + kt, i), r16, g4);
-    }
-#pragma unroll
-    for (int tile = 0; tile < 2 * NV; ++tile)
-        if ((tile & 3) == w)
-            x.U[tile / 4] = ld4(a.eT + tile32(ch, v0 / 16 + tile % NV, tile / NV) + 16 * r16 + g4);
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) x.Kc[i][kt] = ld4(a.KcT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
-        x.dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) x.b[i] = ld4(a.b + ch * C + 16 * i + g4);
+__device__ __forceinline__ long long own_tile(long long ch, int v0, int o, int w) {
+    const int t = (4 * o + w) % (2 * NV);
+    return tile32(ch, v0 / 16 + t % NV, t / NV);
 }
 
-template <int NV>
-__global__ __launch_bounds__(256) void kda_bwd_states(BwdArgs a) {
-    const Walk wk = find_walk<NV>(a);
-    if (!wk.on || wk.nc == 0) return;
-    __shared__ __align__(16) float P[2][4][2 * NV][64][4];
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
-    Fwd<NV> next;
-    fetch<NV>(next, a, (long long)wk.h * a.nslots + wk.first, w, r16, g4, wk.v0);
-    f32x4 S[2][NV];
-    const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-        for (int nv = 0; nv < NV; ++nv)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                S[kt][nv][j] = a.h0 ? a.h0[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
-    for (int c = 0; c < wk.nc; ++c) {
-        const long long ch = (long long)wk.h * a.nslots + wk.first + c;
-        const Fwd<NV> x = next;
-        if (c + 1 < wk.nc) fetch<NV>(next, a, ch + 1, w, r16, g4, wk.v0);
-#pragma unroll
-        for (int nv = 0; nv < NV; ++nv)
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-                st4(a.S + tileS(ch, wk.v0 / 16 + nv, 2 * w + kt) + 16 * r16 + g4, S[kt][nv]);
-#pragma unroll
-        for (int tile = 0; tile < 2 * NV; ++tile) {
-            const int i = tile / NV, nv = tile % NV;
-            f32x4 p = mma(x.W[i][1], S[1][nv], mma(x.W[i][0], S[0][nv], splat(0.f)));
-            if ((tile & 3) == w) p -= x.U[tile / 4];
-            st4(P[c & 1][w][tile][l], p);
-        }
-        lds_barrier();
-        f32x4 e[2][NV];
-#pragma unroll
-        for (int tile = 0; tile < 2 * NV; ++tile) {
-            const int i = tile / NV, nv = tile % NV;
-            const f32x4 y = -(ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) +
-                              ld4(P[c & 1][2][tile][l]) + ld4(P[c & 1][3][tile][l]));
-            if ((tile & 3) == w) st4(a.eT + tile32(ch, wk.v0 / 16 + nv, i) + 16 * r16 + g4, y);
-            e[i][nv] = y * x.b[i];
-        }
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int nv = 0; nv < NV; ++nv)
-                S[kt][nv] = mma(x.Kc[1][kt], e[1][nv], mma(x.Kc[0][kt], e[0][nv], S[kt][nv] * x.dec[kt]));
-    }
-}
+constexpr int TR = 20;       // LDS row of a 16 x 16 tile
 
 template <int NV>
-struct Bwd {
-    f32x4 W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], d_o[2][NV], dD[(2 * NV + 3) / 4];
+struct WalkLds {
+    float P[2][4][2 * NV][64][4];    // parts of the product, [buffer][wave][tile]
+    float T[4][2 * 16 * TR];         // tiles on their way to being transposed, per wave
+    float Do[2][NV][C * TR];         // do of this and the next chunk
 };
 
-template <int NV>
-__device__ __forceinline__ void fetch(Bwd<NV>& x, const BwdArgs& a, const Walk& wk, int c, int T1, int w, int r16, int g4) {
-    const long long ch = (long long)wk.h * a.nslots + wk.first + c;
-#pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) x.Kc[i][kt] = ld4t(a.KcT + tile32(ch, 2 * w + kt, i), r16, g4);
-    }
-#pragma unroll
-    for (int tile = 0; tile < 2 * NV; ++tile)
-        if ((tile & 3) == w)
-            x.dD[tile / 4] = ld4(a.dDT + tile32(ch, wk.v0 / 16 + tile % NV, tile / NV) + 16 * r16 + g4);
+// Transposes a wave's four tiles [i][kt] (rows and columns of 16) through its
+// own LDS. Reading them transposed from memory takes four loads a tile, and a
+// load instruction of a wave costs 16 cycles whatever its width: with those
+// the address unit was busy 73% of the time.
+__device__ __forceinline__ void transpose(f32x4 (&x)[2][2], float* t, int r16, int g4) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        x.b[i] = ld4(a.b + ch * C + 16 * i + g4);
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int nv = 0; nv < NV; ++nv)
+        for (int kt = 0; kt < 2; ++kt) st4(t + kt * 16 * TR + r16 * TR + g4, x[i][kt]);
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t = c * C + 16 * i + g4 + j;
-                x.d_o[i][nv][j] = t < T1 ? a.d_o[((wk.tok + t) * a.H + wk.h) * D + wk.v0 + 16 * nv + r16] : 0.f;
-            }
-    }
+        for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-    for (int kt = 0; kt < 2; ++kt) {
-        x.dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            x.W[i][kt] = ld4(a.WT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
-            x.Qr[i][kt] = ld4(a.QrT + tile32(ch, 2 * w + kt, i) + 16 * r16 + g4);
-        }
+            for (int j = 0; j < 4; ++j) x[i][kt][j] = t[kt * 16 * TR + (g4 + j) * TR + r16];
     }
 }
 
+// Four tiles of a 128 x 32 matrix: channels 32 w .. 32 w + 31.
+__device__ __forceinline__ void fetch4(f32x4 (&x)[2][2], const float* p, long long ch, int w, int fr) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) x[i][kt] = ld4(p + tile32(ch, 2 * w + kt, i) + fr);
+}
+
 template <int NV>
-__global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
-    const Walk wk = find_walk<NV>(a);
-    if (!wk.on) return;
-    __shared__ __align__(16) float P[2][4][2 * NV][64][4];
-    const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
-    f32x4 S[2][NV];
-    const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
-    int T1 = a.T;            // the sequence's length
-    if (a.cu) {
-        int t0;
-        seq_range(a, wk.n, t0, T1);
-        T1 -= t0;
-    }
-    Bwd<NV> next;
-    if (wk.nc > 0) fetch<NV>(next, a, wk, wk.nc - 1, T1, w, r16, g4);
+__device__ __forceinline__ void load_state(f32x4 (&S)[2][NV], const float* p, long long sb, int v0, int w, int r16, int g4) {
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
         for (int nv = 0; nv < NV; ++nv)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                S[kt][nv][j] = a.dhT ? a.dhT[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] : 0.f;
-    for (int c = wk.nc - 1; c >= 0; --c) {
-        const long long ch = (long long)wk.h * a.nslots + wk.first + c;
-        const Bwd<NV> x = next;
-        if (c > 0) fetch<NV>(next, a, wk, c - 1, T1, w, r16, g4);
+            for (int j = 0; j < 4; ++j) S[kt][nv][j] = p ? p[sb + (32 * w + 16 * kt + g4 + j) * D + v0 + 16 * nv + r16] : 0.f;
+}
+
+template <int NV>
+__device__ __forceinline__ void store_chunk_state(float* p, const f32x4 (&S)[2][NV], long long ch, int v0, int w, int fr) {
 #pragma unroll
-        for (int nv = 0; nv < NV; ++nv)
+    for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) st4(p + tileS(ch, v0 / 16 + nv, 2 * w + kt) + fr, S[kt][nv]);
+}
+
+// The sum of the four waves' parts of a tile.
+template <int NV>
+__device__ __forceinline__ f32x4 sum_parts(const WalkLds<NV>& m, int buf, int tile, int l) {
+    return ld4(m.P[buf][0][tile][l]) + ld4(m.P[buf][1][tile][l]) + ld4(m.P[buf][2][tile][l]) + ld4(m.P[buf][3][tile][l]);
+}
+
+template <int NV>
+__device__ __forceinline__ void walk_forwards(const BwdArgs& a, const Walk& wk, WalkLds<NV>& m, int w, int l) {
+    if (wk.nc == 0) return;
+    const int r16 = l & 15, g4 = 4 * (l >> 4), fr = 16 * r16 + g4;
+    f32x4 S[2][NV], W[2][2], Kc[2][2], dec[2], b[2], U[kOwn<NV>];
+    const auto fetch_first = [&](long long ch) {
+        fetch4(W, a.WT, ch, w, fr);
+#pragma unroll
+        for (int o = 0; o < kOwn<NV>; ++o) U[o] = ld4(a.eT + own_tile<NV>(ch, wk.v0, o, w) + fr);
+    };
+    const auto fetch_second = [&](long long ch) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            b[i] = ld4(a.b + ch * C + 16 * i + g4);
+            dec[i] = ld4(a.decay + ch * D + 32 * w + 16 * i + g4);
+        }
+        fetch4(Kc, a.KcT, ch, w, fr);
+    };
+    fetch_first(wk.ch0);
+    fetch_second(wk.ch0);
+    load_state<NV>(S, a.h0, ((long long)wk.n * a.H + wk.h) * D * D, wk.v0, w, r16, g4);
+    for (int c = 0; c < wk.nc; ++c) {
+        const long long ch = wk.ch0 + c, next = wk.ch0 + min(c + 1, wk.nc - 1);
+        const int buf = c & 1;
+        transpose(W, m.T[w], r16, g4);
+        store_chunk_state<NV>(a.S, S, ch, wk.v0, w, fr);
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const int i = tile / NV, nv = tile % NV;
+            f32x4 p = mma(W[i][1], S[1][nv], mma(W[i][0], S[0][nv], splat(0.f)));
+            p -= (tile & 3) == w ? U[tile / 4] : splat(0.f);
+            st4(m.P[buf][w][tile][l], p);
+        }
+        fetch_first(next);
+        lds_barrier();
+        f32x4 e[2][NV], own[kOwn<NV>];
+#pragma unroll
+        for (int tile = 0; tile < 2 * NV; ++tile) {
+            const f32x4 y = -sum_parts<NV>(m, buf, tile, l);
+            if ((tile & 3) == w) own[tile / 4] = y;
+            e[tile / NV][tile % NV] = y * b[tile / NV];
+        }
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int nv = 0; nv < NV; ++nv)
+                S[kt][nv] = mma(Kc[1][kt], e[1][nv], mma(Kc[0][kt], e[0][nv], S[kt][nv] * dec[kt]));
+        fetch_second(next);
+        if (NV > 1 || w < 2)
+#pragma unroll
+            for (int o = 0; o < kOwn<NV>; ++o) st4(a.eT + own_tile<NV>(ch, wk.v0, o, w) + fr, own[o]);
+    }
+}
+
+template <int NV>
+__device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk, WalkLds<NV>& m, int tid, int w, int l) {
+    static_assert(NV <= 2, "256 threads fetch the columns of do");
+    const int r16 = l & 15, g4 = 4 * (l >> 4), fr = 16 * r16 + g4;
+    const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
+    f32x4 S[2][NV], W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], dD[kOwn<NV>];
+    // do of a chunk and this workgroup's columns: 16 bytes of a token a thread,
+    // through LDS a chunk ahead
+    const int dt = (tid >> 2) & 31, dn = tid >> 7, dv = 4 * (tid & 3);   // token, column tile, column
+    const auto fetch_do = [&](int c) {
+        const int t = max(c, 0) * C + dt;
+        const f32x4 x = ld4(a.d_o + ((wk.tok + min(t, wk.len - 1)) * a.H + wk.h) * D + wk.v0 + 16 * (dn % NV) + dv);
+        return t < wk.len ? x : splat(0.f);
+    };
+    const auto fetch_first = [&](long long ch) {
+        fetch4(Kc, a.KcT, ch, w, fr);
+#pragma unroll
+        for (int o = 0; o < kOwn<NV>; ++o) dD[o] = ld4(a.dDT + own_tile<NV>(ch, wk.v0, o, w) + fr);
+    };
+    const auto fetch_second = [&](long long ch) {
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
+        fetch4(Qr, a.QrT, ch, w, fr);
+    };
+    const auto fetch_third = [&](long long ch) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) b[i] = ld4(a.b + ch * C + 16 * i + g4);
+        fetch4(W, a.WT, ch, w, fr);
+    };
+    load_state<NV>(S, a.dhT, sb, wk.v0, w, r16, g4);
+    if (wk.nc > 0) {
+        const long long last = wk.ch0 + wk.nc - 1;
+        fetch_first(last);
+        fetch_second(last);
+        fetch_third(last);
+        f32x4 d_next = fetch_do(wk.nc - 1);
+        if (dn < NV) st4(m.Do[(wk.nc - 1) & 1][dn] + dt * TR + dv, d_next);
+        d_next = fetch_do(wk.nc - 2);
+        lds_barrier();
+        for (int c = wk.nc - 1; c >= 0; --c) {
+            const long long ch = wk.ch0 + c, next = wk.ch0 + max(c - 1, 0);
+            const int buf = c & 1;
+            transpose(Kc, m.T[w], r16, g4);
+            store_chunk_state<NV>(a.dS, S, ch, wk.v0, w, fr);
+#pragma unroll
+            for (int tile = 0; tile < 2 * NV; ++tile) {
+                const int i = tile / NV, nv = tile % NV;
+                f32x4 p = mma(Kc[i][1], S[1][nv], mma(Kc[i][0], S[0][nv], splat(0.f)));
+                p += (tile & 3) == w ? dD[tile / 4] : splat(0.f);
+                st4(m.P[buf][w][tile][l], p);
+            }
+            fetch_first(next);
+            f32x4 d_o[2][NV];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int nv = 0; nv < NV; ++nv)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) d_o[i][nv][j] = m.Do[buf][nv][(16 * i + g4 + j) * TR + r16];
+            if (dn < NV) st4(m.Do[1 - buf][dn] + dt * TR + dv, d_next);
+            d_next = fetch_do(c - 2);
+            // the part of the update that does not wait for dD
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
-                st4(a.dS + tileS(ch, wk.v0 / 16 + nv, 2 * w + kt) + 16 * r16 + g4, S[kt][nv]);
 #pragma unroll
-        for (int tile = 0; tile < 2 * NV; ++tile) {
-            const int i = tile / NV, nv = tile % NV;
-            f32x4 p = mma(x.Kc[i][1], S[1][nv], mma(x.Kc[i][0], S[0][nv], splat(0.f)));
-            if ((tile & 3) == w) p += x.dD[tile / 4];
-            st4(P[c & 1][w][tile][l], p);
+                for (int nv = 0; nv < NV; ++nv)
+                    S[kt][nv] = mma(Qr[1][kt], d_o[1][nv], mma(Qr[0][kt], d_o[0][nv], S[kt][nv] * dec[kt]));
+            fetch_second(next);
+            lds_barrier();
+            f32x4 dd[2][NV], own[kOwn<NV>];
+#pragma unroll
+            for (int tile = 0; tile < 2 * NV; ++tile) {
+                const f32x4 y = sum_parts<NV>(m, buf, tile, l);
+                if ((tile & 3) == w) own[tile / 4] = y;
+                dd[tile / NV][tile % NV] = -(y * b[tile / NV]);
+            }
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int nv = 0; nv < NV; ++nv)
+                    S[kt][nv] = mma(W[1][kt], dd[1][nv], mma(W[0][kt], dd[0][nv], S[kt][nv]));
+            fetch_third(next);
+            if (NV > 1 || w < 2)
+#pragma unroll
+                for (int o = 0; o < kOwn<NV>; ++o) st4(a.dDT + own_tile<NV>(ch, wk.v0, o, w) + fr, own[o]);
         }
-        // the part of the update that does not wait for dD
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int nv = 0; nv < NV; ++nv)
-                S[kt][nv] = mma(x.Qr[1][kt], x.d_o[1][nv], mma(x.Qr[0][kt], x.d_o[0][nv], S[kt][nv] * x.dec[kt]));
-        lds_barrier();
-        f32x4 dd[2][NV];
-#pragma unroll
-        for (int tile = 0; tile < 2 * NV; ++tile) {
-            const int i = tile / NV, nv = tile % NV;
-            const f32x4 y = ld4(P[c & 1][0][tile][l]) + ld4(P[c & 1][1][tile][l]) + ld4(P[c & 1][2][tile][l]) +
-                            ld4(P[c & 1][3][tile][l]);
-            if ((tile & 3) == w) st4(a.dDT + tile32(ch, wk.v0 / 16 + nv, i) + 16 * r16 + g4, y);
-            dd[i][nv] = -(y * x.b[i]);
-        }
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int nv = 0; nv < NV; ++nv)
-                S[kt][nv] = mma(x.W[1][kt], dd[1][nv], mma(x.W[0][kt], dd[0][nv], S[kt][nv]));
     }
     if (a.dh0)
 #pragma unroll
@@ -612,7 +658,19 @@ __global__ __launch_bounds__(256) void kda_bwd_dstates(BwdArgs a) {
                     a.dh0[sb + (32 * w + 16 * kt + g4 + j) * D + wk.v0 + 16 * nv + r16] = S[kt][nv][j];
 }
 
-// ------------------------------------------------------------------ 4 grads
+// The first half of the grid walks backwards, which takes longer.
+template <int NV>
+__global__ __launch_bounds__(256, 3) void kda_bwd_walks(BwdArgs a) {
+    __shared__ __align__(16) WalkLds<NV> m;
+    const int half = gridDim.x / 2, tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
+    const bool back = (int)blockIdx.x < half;
+    const Walk wk = find_walk<NV>(a, back ? blockIdx.x : blockIdx.x - half);
+    if (!wk.on) return;
+    if (back) walk_backwards<NV>(a, wk, m, tid, w, l);
+    else walk_forwards<NV>(a, wk, m, w, l);
+}
+
+// ------------------------------------------------------------------ 3 grads
 template <bool F32>
 __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     const int slot = (int)(blockIdx.x / (unsigned)a.H), h = (int)(blockIdx.x % (unsigned)a.H);
@@ -869,20 +927,17 @@ template <bool F32, int NV>
 static hipError_t run_bwd(const BwdArgs& a, hipStream_t s) {
     const long long work = (long long)a.nslots * a.H;
     const int nb = D / (16 * NV);
-    const unsigned walks = (unsigned)(((long long)a.N * a.H + 7) / 8 * 8 * nb);
+    const unsigned walks = (unsigned)(((long long)a.N * a.H + 7) / 8 * 8 * nb * 2);
     if (walks == 0) return hipSuccess;
-    if (work > 0) {
-        hipLaunchKernelGGL(bwd::kda_bwd_intra<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
-        hipLaunchKernelGGL(bwd::kda_bwd_states<NV>, dim3(walks), dim3(256), 0, s, a);
-    }
-    hipLaunchKernelGGL(bwd::kda_bwd_dstates<NV>, dim3(walks), dim3(256), 0, s, a);
+    if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_intra<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(bwd::kda_bwd_walks<NV>, dim3(walks), dim3(256), 0, s, a);
     if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_grads<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_bwd(const BwdArgs& a, int cus, hipStream_t s) {
     (void)cus;
-    return a.f32 ? run_bwd<true, 1>(a, s) : run_bwd<false, 1>(a, s);
+    return a.f32 ? run_bwd<true, 2>(a, s) : run_bwd<false, 2>(a, s);
 }
 
 }  // namespace kda
