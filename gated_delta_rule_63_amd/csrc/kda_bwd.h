@@ -31,11 +31,12 @@ struct BwdArgs {
     float* dbeta;
     float* dh0;          // nullptr: not written
     float* X;            // [32][32]
+    float* MT;           // [32][32], M transposed; the block of tokens 0..15 by 16..31 is unset
     float* b;            // [32] beta, zero behind the last token
     float* decay;        // [128] exp(sum of g over the chunk)
     float* WT;           // 128 x 32
-    float* eT;           // 128 x 32, first U, then e
-    float* dDT;          // 128 x 32, first M^T do, then dDelta
+    float* eT;           // 128 x 32, e
+    float* dDT;          // 128 x 32, dDelta
     float* KcT;          // 128 x 32
     float* QrT;          // 128 x 32
     float* S;            // 128 x 128, [v][k], tiles (v tile, k tile): state entering the chunk

@@ -22,7 +22,7 @@
 //
 // Three kernels. Only the two state walks are sequential, and both split over
 // the columns of V, which the recurrence never mixes:
-//   1 intra  per (chunk, head): X, W, U, M^T do, kc, qr
+//   1 intra  per (chunk, head): X, M, W, kc, qr
 //   2 walks  per (sequence, head, V-block), forwards: S, e; backwards: dS, dD
 //   3 grads  per (chunk, head): everything else
 // All products run on the fp32 matrix instruction (16x16x4): gradients of fp32
@@ -219,13 +219,11 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C], gs[C];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     // everything from memory at once: the latency of one fetch, not of three
-    Rows<F32> rk, rq, rv;
-    Rows<true> rg, rd;
+    Rows<F32> rk, rq;
+    Rows<true> rg;
     load_rows<F32>(rk, a.k, a, ck, h, tid);
     load_rows<F32>(rq, a.q, a, ck, h, tid);
     if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
-    load_rows<F32>(rv, a.v, a, ck, h, tid);
-    load_rows<true>(rd, a.d_o, a, ck, h, tid);
     if (tid < C) {
         const float b = tid < ck.nv ? a.beta[(ck.tok + tid) * a.H + h] : 0.f;
         bs[tid] = b;
@@ -315,9 +313,6 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         else Ms[t * LM + s] = t >= s ? x : 0.f;
     }
     lds_barrier();
-    float *const Vs = KQ, *const Ds = KQ + C * LD;   // the parts have been summed: v and do take their place
-    put_rows<F32>(rv, Vs, tid);
-    put_rows<true>(rd, Ds, tid);
     if (w == 0) {
         // X of the two diagonal blocks by substitution, one lane per column:
         // X_ts = -B_ts - sum_(s < u < t) B_tu b_u X_us
@@ -352,41 +347,29 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     }
     lds_barrier();
     {
-        const int i = 4 * tid;
-        st4(a.X + ch * (C * C) + i, ld4(Xs + (i >> 5) * LM + (i & 31)));
+        const int i = 4 * tid, r = i >> 5, c0 = i & 31;
+        st4(a.X + ch * (C * C) + i, ld4(Xs + r * LM + c0));
+        f32x4 x;             // M transposed; its blocks above the diagonal are not written and not read
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = Ms[(c0 + j) * LM + r];
+        st4(a.MT + ch * (C * C) + i, x);
     }
-    // W, U, M^T do: each wave its own 32 columns
+    // W: each wave its own 32 columns
     const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
     const f32x4 x00 = ld4(Xs + r16 * LM + g4) * b0, x10 = ld4(Xs + (16 + r16) * LM + g4) * b0,
                 x11 = ld4(Xs + (16 + r16) * LM + 16 + g4) * b1;
-    f32x4 m00, m10, m11;     // transposed
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        m00[j] = Ms[(g4 + j) * LM + r16];
-        m10[j] = Ms[(16 + g4 + j) * LM + r16];
-        m11[j] = Ms[(16 + g4 + j) * LM + 16 + r16];
-    }
 #pragma unroll
     for (int ct = 0; ct < 2; ++ct) {
         const int col = 32 * w + 16 * ct + r16;
-        f32x4 f0, f1, v0, v1, d0, d1;
+        f32x4 f0, f1;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int t0 = g4 + j, t1 = 16 + t0;
-            v0[j] = Vs[t0 * LD + col];
-            v1[j] = Vs[t1 * LD + col];
-            d0[j] = Ds[t0 * LD + col];
-            d1[j] = Ds[t1 * LD + col];
-            f0[j] = Kd[t0 * LD + col] * sc[0][col];
-            f1[j] = Kd[t1 * LD + col] * sc[1][col];
+            f0[j] = Kd[(g4 + j) * LD + col] * sc[0][col];
+            f1[j] = Kd[(16 + g4 + j) * LD + col] * sc[1][col];
         }
         const long long o = tile32(ch, 2 * w + ct, 0) + fr;
         st4(a.WT + o, mma(x00, f0, f0));
         st4(a.WT + o + 256, mma(x11, f1, mma(x10, f0, f1)));
-        st4(a.eT + o, mma(x00, v0, v0));
-        st4(a.eT + o + 256, mma(x11, v1, mma(x10, v0, v1)));
-        st4(a.dDT + o, mma(m10, d1, mma(m00, d0, splat(0.f))));
-        st4(a.dDT + o + 256, mma(m11, d1, splat(0.f)));
     }
 }
 
@@ -394,7 +377,8 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
 // One workgroup per direction, (sequence, head) and 16 NV columns of V. Wave w
 // holds rows 32 w .. 32 w + 31 of the state as accumulators (row = channel k,
 // column = v); as such they are also the right operand of the product with W
-// (or kc), of which each wave forms the part of its own channels. The parts
+// (or kc), of which each wave forms the part of its own channels, one of them on
+// top of -U (or M^T do). The parts
 // meet in LDS, and every wave sums them into the operand of the state's
 // update: one barrier a chunk.
 //
@@ -436,14 +420,11 @@ __device__ __forceinline__ Walk find_walk(const BwdArgs& a, int block) {
     return r;
 }
 
-// Of the 2 NV tiles of e (or dD), tile 4 o + w is wave w's to add U to and to
-// store; with NV = 1 waves 2 and 3 have none.
+// Of the 2 NV tiles [token tile][column tile] of e (or dD), tile w is wave
+// w's to start and to store; with NV = 1 waves 2 and 3 have none.
 template <int NV>
-constexpr int kOwn = (2 * NV + 3) / 4;
-template <int NV>
-__device__ __forceinline__ long long own_tile(long long ch, int v0, int o, int w) {
-    const int t = (4 * o + w) % (2 * NV);
-    return tile32(ch, v0 / 16 + t % NV, t / NV);
+__device__ __forceinline__ long long own_tile(long long ch, int v0, int w) {
+    return tile32(ch, v0 / 16 + w % NV, w / NV % 2);
 }
 
 constexpr int TR = 20;       // LDS row of a 16 x 16 tile
@@ -452,7 +433,7 @@ template <int NV>
 struct WalkLds {
     float P[2][4][2 * NV][64][4];    // parts of the product, [buffer][wave][tile]
     float T[4][2 * 16 * TR];         // tiles on their way to being transposed, per wave
-    float Do[2][NV][C * TR];         // do of this and the next chunk
+    float R[2][NV][C * TR];          // rows of v (forwards) or do (backwards), two chunks
 };
 
 // Transposes a wave's four tiles [i][kt] (rows and columns of 16) through its
@@ -507,46 +488,102 @@ __device__ __forceinline__ f32x4 sum_parts(const WalkLds<NV>& m, int buf, int ti
     return ld4(m.P[buf][0][tile][l]) + ld4(m.P[buf][1][tile][l]) + ld4(m.P[buf][2][tile][l]) + ld4(m.P[buf][3][tile][l]);
 }
 
+// Rows of a chunk of v or do, this workgroup's columns: four values of a token
+// a thread, on their way through LDS a chunk ahead of their use.
+template <bool F32, int NV>
+struct Feed {
+    const void* p;
+    const BwdArgs& a;
+    const Walk& wk;
+    const int t, n, v;       // token, column tile, column
+    f32x4 x;
+
+    __device__ __forceinline__ Feed(const void* p, const BwdArgs& a, const Walk& wk, int tid)
+        : p(p), a(a), wk(wk), t((tid >> 2) & 31), n(tid >> 7), v(4 * (tid & 3)) {
+        static_assert(NV <= 2, "256 threads fetch the rows");
+    }
+    __device__ __forceinline__ void fetch(int c) {
+        const int at = min(max(c, 0), wk.nc - 1) * C + t;
+        const long long i = ((wk.tok + min(at, wk.len - 1)) * a.H + wk.h) * D + wk.v0 + 16 * (n % NV) + v;
+        f32x4 y;
+        if constexpr (F32) {
+            y = ld4(static_cast<const float*>(p) + i);
+        } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+            y = f32x4{__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                      __uint_as_float(u.y & 0xffff0000u)};
+        }
+        x = at < wk.len ? y : splat(0.f);
+    }
+    __device__ __forceinline__ void put(WalkLds<NV>& m, int buf) const {
+        if (n < NV) st4(m.R[buf][n] + t * TR + v, x);
+    }
+};
+
 template <int NV>
-__device__ __forceinline__ void walk_forwards(const BwdArgs& a, const Walk& wk, WalkLds<NV>& m, int w, int l) {
+__device__ __forceinline__ f32x4 feed_tile(const WalkLds<NV>& m, int buf, int nv, int i, int r16, int g4) {
+    f32x4 x;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = m.R[buf][nv][(16 * i + g4 + j) * TR + r16];
+    return x;
+}
+
+template <bool F32, int NV>
+__device__ __forceinline__ void walk_forwards(const BwdArgs& a, const Walk& wk, WalkLds<NV>& m, int tid, int w, int l) {
     if (wk.nc == 0) return;
     const int r16 = l & 15, g4 = 4 * (l >> 4), fr = 16 * r16 + g4;
-    f32x4 S[2][NV], W[2][2], Kc[2][2], dec[2], b[2], U[kOwn<NV>];
-    const auto fetch_first = [&](long long ch) {
-        fetch4(W, a.WT, ch, w, fr);
+    const int oi = w / NV % 2;   // token tile of this wave's tile
+    f32x4 S[2][NV], W[2][2], Kc[2][2], dec[2], b[2], bn[2], X[2];
+    const auto fetch_b = [&](f32x4 (&x)[2], long long ch) {
 #pragma unroll
-        for (int o = 0; o < kOwn<NV>; ++o) U[o] = ld4(a.eT + own_tile<NV>(ch, wk.v0, o, w) + fr);
+        for (int i = 0; i < 2; ++i) x[i] = ld4(a.b + ch * C + 16 * i + g4);
+    };
+    const auto fetch_first = [&](long long ch) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) X[i] = ld4(a.X + ch * (C * C) + (16 * oi + r16) * C + 16 * i + g4);
+        fetch4(W, a.WT, ch, w, fr);
     };
     const auto fetch_second = [&](long long ch) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            b[i] = ld4(a.b + ch * C + 16 * i + g4);
-            dec[i] = ld4(a.decay + ch * D + 32 * w + 16 * i + g4);
-        }
+        for (int kt = 0; kt < 2; ++kt) dec[kt] = ld4(a.decay + ch * D + 32 * w + 16 * kt + g4);
         fetch4(Kc, a.KcT, ch, w, fr);
     };
+    Feed<F32, NV> v(a.v, a, wk, tid);
+    fetch_b(b, wk.ch0);
+    v.fetch(0);
     fetch_first(wk.ch0);
     fetch_second(wk.ch0);
     load_state<NV>(S, a.h0, ((long long)wk.n * a.H + wk.h) * D * D, wk.v0, w, r16, g4);
+    v.put(m, 0);
+    v.fetch(1);
+    lds_barrier();
     for (int c = 0; c < wk.nc; ++c) {
         const long long ch = wk.ch0 + c, next = wk.ch0 + min(c + 1, wk.nc - 1);
         const int buf = c & 1;
+        fetch_b(bn, next);
         transpose(W, m.T[w], r16, g4);
         store_chunk_state<NV>(a.S, S, ch, wk.v0, w, fr);
 #pragma unroll
         for (int tile = 0; tile < 2 * NV; ++tile) {
             const int i = tile / NV, nv = tile % NV;
-            f32x4 p = mma(W[i][1], S[1][nv], mma(W[i][0], S[0][nv], splat(0.f)));
-            p -= (tile & 3) == w ? U[tile / 4] : splat(0.f);
+            f32x4 p = splat(0.f);
+            if (tile == w) {     // -U = -(v + X b v)
+                const f32x4 v0 = feed_tile<NV>(m, buf, nv, 0, r16, g4), v1 = feed_tile<NV>(m, buf, nv, 1, r16, g4);
+                p = mma(X[0] * b[0], -v0, i ? -v1 : -v0);
+                if (i) p = mma(X[1] * b[1], -v1, p);
+            }
+            p = mma(W[i][1], S[1][nv], mma(W[i][0], S[0][nv], p));
             st4(m.P[buf][w][tile][l], p);
         }
+        v.put(m, 1 - buf);
+        v.fetch(c + 2);
         fetch_first(next);
         lds_barrier();
-        f32x4 e[2][NV], own[kOwn<NV>];
+        f32x4 e[2][NV], own;
 #pragma unroll
         for (int tile = 0; tile < 2 * NV; ++tile) {
             const f32x4 y = -sum_parts<NV>(m, buf, tile, l);
-            if ((tile & 3) == w) own[tile / 4] = y;
+            if (tile == w) own = y;
             e[tile / NV][tile % NV] = y * b[tile / NV];
         }
 #pragma unroll
@@ -555,30 +592,22 @@ __device__ __forceinline__ void walk_forwards(const BwdArgs& a, const Walk& wk, 
             for (int nv = 0; nv < NV; ++nv)
                 S[kt][nv] = mma(Kc[1][kt], e[1][nv], mma(Kc[0][kt], e[0][nv], S[kt][nv] * dec[kt]));
         fetch_second(next);
-        if (NV > 1 || w < 2)
-#pragma unroll
-            for (int o = 0; o < kOwn<NV>; ++o) st4(a.eT + own_tile<NV>(ch, wk.v0, o, w) + fr, own[o]);
+        if (NV > 1 || w < 2) st4(a.eT + own_tile<NV>(ch, wk.v0, w) + fr, own);
+        b[0] = bn[0];
+        b[1] = bn[1];
     }
 }
 
 template <int NV>
 __device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk, WalkLds<NV>& m, int tid, int w, int l) {
-    static_assert(NV <= 2, "256 threads fetch the columns of do");
     const int r16 = l & 15, g4 = 4 * (l >> 4), fr = 16 * r16 + g4;
+    const int oi = w / NV % 2;
     const long long sb = ((long long)wk.n * a.H + wk.h) * D * D;
-    f32x4 S[2][NV], W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], dD[kOwn<NV>];
-    // do of a chunk and this workgroup's columns: 16 bytes of a token a thread,
-    // through LDS a chunk ahead
-    const int dt = (tid >> 2) & 31, dn = tid >> 7, dv = 4 * (tid & 3);   // token, column tile, column
-    const auto fetch_do = [&](int c) {
-        const int t = max(c, 0) * C + dt;
-        const f32x4 x = ld4(a.d_o + ((wk.tok + min(t, wk.len - 1)) * a.H + wk.h) * D + wk.v0 + 16 * (dn % NV) + dv);
-        return t < wk.len ? x : splat(0.f);
-    };
+    f32x4 S[2][NV], W[2][2], Kc[2][2], Qr[2][2], dec[2], b[2], MT[2];
     const auto fetch_first = [&](long long ch) {
-        fetch4(Kc, a.KcT, ch, w, fr);
 #pragma unroll
-        for (int o = 0; o < kOwn<NV>; ++o) dD[o] = ld4(a.dDT + own_tile<NV>(ch, wk.v0, o, w) + fr);
+        for (int i = 0; i < 2; ++i) MT[i] = ld4(a.MT + ch * (C * C) + (16 * oi + r16) * C + 16 * i + g4);
+        fetch4(Kc, a.KcT, ch, w, fr);
     };
     const auto fetch_second = [&](long long ch) {
 #pragma unroll
@@ -596,32 +625,35 @@ __device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk,
         fetch_first(last);
         fetch_second(last);
         fetch_third(last);
-        f32x4 d_next = fetch_do(wk.nc - 1);
-        if (dn < NV) st4(m.Do[(wk.nc - 1) & 1][dn] + dt * TR + dv, d_next);
-        d_next = fetch_do(wk.nc - 2);
+        Feed<true, NV> d(a.d_o, a, wk, tid);
+        d.fetch(wk.nc - 1);
+        d.put(m, (wk.nc - 1) & 1);
+        d.fetch(wk.nc - 2);
         lds_barrier();
         for (int c = wk.nc - 1; c >= 0; --c) {
             const long long ch = wk.ch0 + c, next = wk.ch0 + max(c - 1, 0);
             const int buf = c & 1;
             transpose(Kc, m.T[w], r16, g4);
             store_chunk_state<NV>(a.dS, S, ch, wk.v0, w, fr);
-#pragma unroll
-            for (int tile = 0; tile < 2 * NV; ++tile) {
-                const int i = tile / NV, nv = tile % NV;
-                f32x4 p = mma(Kc[i][1], S[1][nv], mma(Kc[i][0], S[0][nv], splat(0.f)));
-                p += (tile & 3) == w ? dD[tile / 4] : splat(0.f);
-                st4(m.P[buf][w][tile][l], p);
-            }
-            fetch_first(next);
             f32x4 d_o[2][NV];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int nv = 0; nv < NV; ++nv)
+                for (int nv = 0; nv < NV; ++nv) d_o[i][nv] = feed_tile<NV>(m, buf, nv, i, r16, g4);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) d_o[i][nv][j] = m.Do[buf][nv][(16 * i + g4 + j) * TR + r16];
-            if (dn < NV) st4(m.Do[1 - buf][dn] + dt * TR + dv, d_next);
-            d_next = fetch_do(c - 2);
+            for (int tile = 0; tile < 2 * NV; ++tile) {
+                const int i = tile / NV, nv = tile % NV;
+                f32x4 p = splat(0.f);
+                if (tile == w) { // M^T do
+                    if (!i) p = mma(MT[0], d_o[0][nv], p);
+                    p = mma(MT[1], d_o[1][nv], p);
+                }
+                p = mma(Kc[i][1], S[1][nv], mma(Kc[i][0], S[0][nv], p));
+                st4(m.P[buf][w][tile][l], p);
+            }
+            d.put(m, 1 - buf);
+            d.fetch(c - 2);
+            fetch_first(next);
             // the part of the update that does not wait for dD
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
@@ -630,11 +662,11 @@ __device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk,
                     S[kt][nv] = mma(Qr[1][kt], d_o[1][nv], mma(Qr[0][kt], d_o[0][nv], S[kt][nv] * dec[kt]));
             fetch_second(next);
             lds_barrier();
-            f32x4 dd[2][NV], own[kOwn<NV>];
+            f32x4 dd[2][NV], own;
 #pragma unroll
             for (int tile = 0; tile < 2 * NV; ++tile) {
                 const f32x4 y = sum_parts<NV>(m, buf, tile, l);
-                if ((tile & 3) == w) own[tile / 4] = y;
+                if (tile == w) own = y;
                 dd[tile / NV][tile % NV] = -(y * b[tile / NV]);
             }
 #pragma unroll
@@ -643,9 +675,7 @@ __device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk,
                 for (int nv = 0; nv < NV; ++nv)
                     S[kt][nv] = mma(W[1][kt], dd[1][nv], mma(W[0][kt], dd[0][nv], S[kt][nv]));
             fetch_third(next);
-            if (NV > 1 || w < 2)
-#pragma unroll
-                for (int o = 0; o < kOwn<NV>; ++o) st4(a.dDT + own_tile<NV>(ch, wk.v0, o, w) + fr, own[o]);
+            if (NV > 1 || w < 2) st4(a.dDT + own_tile<NV>(ch, wk.v0, w) + fr, own);
         }
     }
     if (a.dh0)
@@ -659,7 +689,7 @@ __device__ __forceinline__ void walk_backwards(const BwdArgs& a, const Walk& wk,
 }
 
 // The first half of the grid walks backwards, which takes longer.
-template <int NV>
+template <bool F32, int NV>
 __global__ __launch_bounds__(256, 3) void kda_bwd_walks(BwdArgs a) {
     __shared__ __align__(16) WalkLds<NV> m;
     const int half = gridDim.x / 2, tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), l = tid & 63;
@@ -667,7 +697,7 @@ __global__ __launch_bounds__(256, 3) void kda_bwd_walks(BwdArgs a) {
     const Walk wk = find_walk<NV>(a, back ? blockIdx.x : blockIdx.x - half);
     if (!wk.on) return;
     if (back) walk_backwards<NV>(a, wk, m, tid, w, l);
-    else walk_forwards<NV>(a, wk, m, w, l);
+    else walk_forwards<F32, NV>(a, wk, m, tid, w, l);
 }
 
 // ------------------------------------------------------------------ 3 grads
@@ -930,7 +960,7 @@ static hipError_t run_bwd(const BwdArgs& a, hipStream_t s) {
     const unsigned walks = (unsigned)(((long long)a.N * a.H + 7) / 8 * 8 * nb * 2);
     if (walks == 0) return hipSuccess;
     if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_intra<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
-    hipLaunchKernelGGL(bwd::kda_bwd_walks<NV>, dim3(walks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL((bwd::kda_bwd_walks<F32, NV>), dim3(walks), dim3(256), 0, s, a);
     if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_grads<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
     return hipGetLastError();
 }

@@ -12,9 +12,9 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// fp32 values of workspace per (slot, head): X, b, decay, five [128][32] tiles
-// and two states.
-constexpr size_t kPerChunk = 32 * 32 + 32 + 128 + 5 * 128 * 32 + 2 * 128 * 128;
+// fp32 values of workspace per (slot, head): X, M, b, decay, five 128 x 32
+// matrices and two states.
+constexpr size_t kPerChunk = 2 * 32 * 32 + 32 + 128 + 5 * 128 * 32 + 2 * 128 * 128;
 
 // Slots for either use of the descriptor (it does not say whether cu_seqlens
 // comes with it); more than 2^23 chunks (1.7 TiB) are refused.
@@ -63,6 +63,7 @@ kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, 
     a.KcT = take(128 * 32);
     a.QrT = take(128 * 32);
     a.X = take(32 * 32);
+    a.MT = take(32 * 32);
     a.decay = take(128);
     a.b = take(32);
     return kda::launch_bwd(a, 256, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;

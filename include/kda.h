@@ -355,7 +355,7 @@ kda_status_t kda_gdn_bwd(const void* q, const void* k, const void* v, const floa
                          void* dq, void* dk, void* dv, float* dg, float* dbeta, float* dh0,
                          const kda_desc_t* desc, void* stream);
 
-/* Bytes of device workspace kda_bwd and kda_gdn_bwd need: 217,728 per head and
+/* Bytes of device workspace kda_bwd and kda_gdn_bwd need: 221,824 per head and
  * chunk of 32 tokens (a sequence's last chunk may be shorter). 0 for an
  * invalid descriptor. */
 size_t kda_bwd_workspace_size(const kda_desc_t* desc);

@@ -80,12 +80,12 @@ def test_refusals():
         for name in ("q", "k", "v", "g", "beta", "do", "dq", "dk", "dv", "dg", "db"):
             assert call(d(), fn, **{name: None}) == -1, name
         assert call(d(), fn, do=ctypes.c_void_p(0x10004)) == -3          # not 16-byte aligned
-        assert call(d(ws=0), fn) == -5 and call(d(ws=4 * 217728 - 1), fn) == -5
+        assert call(d(ws=0), fn) == -5 and call(d(ws=4 * 221824 - 1), fn) == -5
         assert call(d(B=1 << 12, T=1 << 16, H=64, N=1 << 12), fn) == -2  # 2^29 chunks
     # two chunks of two heads; with B == N == 1 the packed use may need one slot more
     size = lambda x: L.kda_bwd_workspace_size(ctypes.byref(x))
-    assert size(d()) == 3 * 2 * 217728 and size(d(B=2, T=33)) == 4 * 2 * 217728
-    assert size(d(N=5)) == 7 * 2 * 217728 and size(d(K=64)) == 0
+    assert size(d()) == 3 * 2 * 221824 and size(d(B=2, T=33)) == 4 * 2 * 221824
+    assert size(d(N=5)) == 7 * 2 * 221824 and size(d(K=64)) == 0
     assert L.kda_bwd_workspace_size(None) == 0
 
 
