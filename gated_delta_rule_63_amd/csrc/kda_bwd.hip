@@ -133,16 +133,27 @@ struct Rows {
     uint4 x[F32 ? 4 : 2];
 };
 
+// Piece i of thread tid is row t + i 256 / per, 16-byte piece c. One 32-bit
+// offset a lane; the rest of the address is the same for the whole wave.
+template <bool F32>
+struct Place {
+    static constexpr int per = F32 ? 32 : 16, step = 256 / per, row = D * (F32 ? 4 : 2);   // pieces and bytes of a row
+    int t, c;
+    unsigned off;
+    __device__ __forceinline__ Place(const BwdArgs& a, int tid) : t(tid / per), c(tid % per), off((unsigned)(t * a.H) * row + 16 * c) {}
+    __device__ __forceinline__ long long base(const BwdArgs& a, const Chunk& ck, int h, int i) const {
+        return ((ck.tok + step * i) * a.H + h) * row;
+    }
+};
+
 template <bool F32>
 __device__ __forceinline__ void load_rows(Rows<F32>& r, const void* p, const BwdArgs& a, const Chunk& ck, int h, int tid) {
-    constexpr int per = F32 ? 32 : 16, bytes = F32 ? 4 : 2;   // pieces a row
+    const Place<F32> at(a, tid);
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
         r.x[i] = make_uint4(0, 0, 0, 0);
-        if (t < ck.nv)
-            r.x[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) +
-                                                     (((ck.tok + t) * a.H + h) * D) * bytes + 16 * c);
+        if (at.t + at.step * i < ck.nv)
+            r.x[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at.base(a, ck, h, i) + at.off);
     }
 }
 
@@ -169,13 +180,14 @@ __device__ __forceinline__ void put_rows(const Rows<F32>& r, float* to, int tid)
 template <bool F32>
 __device__ __forceinline__ void store_rows(void* p, const float* from, const float* by, const BwdArgs& a,
                                            const Chunk& ck, int h, int tid) {
-    constexpr int per = F32 ? 32 : 16, bytes = F32 ? 4 : 2;
+    const Place<F32> at(a, tid);
+    const int c = at.c;
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
+        const int t = at.t + at.step * i;
         if (t >= ck.nv) continue;
         const float f = by ? by[t] : 1.f;
-        char* const to = static_cast<char*>(p) + (((ck.tok + t) * a.H + h) * D) * bytes + 16 * c;
+        char* const to = static_cast<char*>(p) + at.base(a, ck, h, i) + at.off;
         if constexpr (F32) {
             *reinterpret_cast<f32x4*>(to) = ld4(from + t * LD + 4 * c) * f;
         } else {
@@ -865,7 +877,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
             for (int j = 0; j < 4; ++j) {
                 const int o = (16 * i + g4 + j) * LD + col;
                 E1[i][j] = R0[o];
-                E2[i][j] = 1.f / R0[o];
+                E2[i][j] = __builtin_amdgcn_rcpf(R0[o]);   // to 1 ulp
                 kk[i][j] = R1[o];
                 qq[i][j] = R2[o];
             }

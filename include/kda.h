@@ -334,7 +334,8 @@ kda_status_t kda_fwd_staged(const void* q, const void* k, const void* v, const f
  * q, k, v, g, beta, cu_seqlens, h0 are the forward's own inputs (states inside
  * the sequences are recomputed, nothing is kept from the forward); d_o is
  * [B, T, H, 128] fp32. Every tensor with rows of 128 channels is 16-byte aligned
- * (KDA_ERR_UNSUPPORTED otherwise). Rows of tokens outside [cu[0], cu[N]) are
+ * (KDA_ERR_UNSUPPORTED otherwise), H at most 65,536 and chunks of 32 tokens times
+ * heads at most 2^23 (KDA_ERR_SHAPE). Rows of tokens outside [cu[0], cu[N]) are
  * left as they were. A zero-length sequence has dh0 = dhT.
  * Needs desc->workspace of kda_bwd_workspace_size(desc) bytes, 16-byte aligned
  * (KDA_ERR_WORKSPACE when missing or smaller); nothing is allocated, so the call
