@@ -726,9 +726,18 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     if (tid < C) bs[tid] = a.b[ch * C + tid];
     st4(Xs + (tid >> 3) * LM + 4 * (tid & 7), ld4(a.X + ch * (C * C) + 4 * tid));
+    f32x4 d0[2], d1[2], e0[2], e1[2];
     {
         Rows<true> rd;
         load_rows<true>(rd, a.d_o, a, ck, h, tid);
+#pragma unroll
+        for (int ct = 0; ct < 2; ++ct) {
+            const long long o = tile32(ch, 2 * w + ct, 0) + 16 * r16 + g4;
+            d0[ct] = ld4(a.dDT + o);
+            d1[ct] = ld4(a.dDT + o + 256);
+            e0[ct] = ld4(a.eT + o);
+            e1[ct] = ld4(a.eT + o + 256);
+        }
         put_rows<true>(rd, R0, tid);
     }
     lds_barrier();
@@ -744,17 +753,14 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
 #pragma unroll
         for (int ct = 0; ct < 2; ++ct) {
             const int col = 32 * w + 16 * ct + r16;
-            const long long o = tile32(ch, 2 * w + ct, 0) + 16 * r16 + g4;
-            const f32x4 d0 = ld4(a.dDT + o), d1 = ld4(a.dDT + o + 256);
-            const f32x4 e0 = ld4(a.eT + o), e1 = ld4(a.eT + o + 256);
-            const f32x4 p0 = mma(x10, d1 * b1, mma(x00, d0 * b0, d0)), p1 = mma(x11, d1 * b1, d1);
+            const f32x4 p0 = mma(x10, d1[ct] * b1, mma(x00, d0[ct] * b0, d0[ct])), p1 = mma(x11, d1[ct] * b1, d1[ct]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int t0 = g4 + j, t1 = 16 + t0;
                 R1[t0 * LD + col] = p0[j];
                 R1[t1 * LD + col] = p1[j];
-                R2[t0 * LD + col] = e0[j];
-                R2[t1 * LD + col] = e1[j];
+                R2[t0 * LD + col] = e0[ct][j];
+                R2[t1 * LD + col] = e1[ct][j];
             }
         }
     }
@@ -780,6 +786,13 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
             }
         }
     }
+    // k, q and g for later, on their way behind the products
+    Rows<F32> rk, rq;
+    Rows<true> rg;
+    if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
+    load_rows<F32>(rk, a.k, a, ck, h, tid);
+    load_rows<F32>(rq, a.q, a, ck, h, tid);
+    if (a.scalar_gate && tid < C) part[0][tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
     // products with the states: each wave its own 32 channels
     f32x4 qS[2][2], rS[2][2], eS[2][2];
     float sd[2] = {0.f, 0.f};
@@ -824,17 +837,9 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
         }
     }
     lds_barrier();
-    {
-        Rows<F32> rk, rq;
-        Rows<true> rg;
-        if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
-        load_rows<F32>(rk, a.k, a, ck, h, tid);
-        load_rows<F32>(rq, a.q, a, ck, h, tid);
-        if (a.scalar_gate && tid < C) part[0][tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
-        if (!a.scalar_gate) put_rows<true>(rg, R0, tid);
-        put_rows<F32>(rk, R1, tid);
-        put_rows<F32>(rq, R2, tid);
-    }
+    if (!a.scalar_gate) put_rows<true>(rg, R0, tid);
+    put_rows<F32>(rk, R1, tid);
+    put_rows<F32>(rq, R2, tid);
     lds_barrier();
     {
         const int c = 32 * w + (l & 31), half = l >> 5;
