@@ -128,16 +128,17 @@ struct Gates {
 // whole rows a few lanes, held in registers until LDS is ready for them.
 // (Loads of one channel a lane touch every line several times from several
 // waves; with them alone a kernel took twice as long.)
-template <bool F32>
+template <bool F32, int NT>
 struct Rows {
-    uint4 x[F32 ? 4 : 2];
+    static constexpr int n = (F32 ? 1024 : 512) / NT;   // pieces a thread
+    uint4 x[n];
 };
 
-// Piece i of thread tid is row t + i 256 / per, 16-byte piece c. One 32-bit
+// Piece i of thread tid is row t + i NT / per, 16-byte piece c. One 32-bit
 // offset a lane; the rest of the address is the same for the whole wave.
-template <bool F32>
+template <bool F32, int NT>
 struct Place {
-    static constexpr int per = F32 ? 32 : 16, step = 256 / per, row = D * (F32 ? 4 : 2);   // pieces and bytes of a row
+    static constexpr int per = F32 ? 32 : 16, step = NT / per, row = D * (F32 ? 4 : 2);   // pieces and bytes of a row
     int t, c;
     unsigned off;
     __device__ __forceinline__ Place(const BwdArgs& a, int tid) : t(tid / per), c(tid % per), off((unsigned)(t * a.H) * row + 16 * c) {}
@@ -146,23 +147,23 @@ struct Place {
     }
 };
 
-template <bool F32>
-__device__ __forceinline__ void load_rows(Rows<F32>& r, const void* p, const BwdArgs& a, const Chunk& ck, int h, int tid) {
-    const Place<F32> at(a, tid);
+template <bool F32, int NT>
+__device__ __forceinline__ void load_rows(Rows<F32, NT>& r, const void* p, const BwdArgs& a, const Chunk& ck, int h, int tid) {
+    const Place<F32, NT> at(a, tid);
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    for (int i = 0; i < Rows<F32, NT>::n; ++i) {
         r.x[i] = make_uint4(0, 0, 0, 0);
         if (at.t + at.step * i < ck.nv)
             r.x[i] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at.base(a, ck, h, i) + at.off);
     }
 }
 
-template <bool F32>
-__device__ __forceinline__ void put_rows(const Rows<F32>& r, float* to, int tid) {
+template <bool F32, int NT>
+__device__ __forceinline__ void put_rows(const Rows<F32, NT>& r, float* to, int tid) {
     constexpr int per = F32 ? 32 : 16;
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
-        const int t = (tid + 256 * i) / per, c = (tid + 256 * i) % per;
+    for (int i = 0; i < Rows<F32, NT>::n; ++i) {
+        const int t = (tid + NT * i) / per, c = (tid + NT * i) % per;
         const uint4 u = r.x[i];
         if constexpr (F32) {
             *reinterpret_cast<uint4*>(to + t * LD + 4 * c) = u;
@@ -177,13 +178,13 @@ __device__ __forceinline__ void put_rows(const Rows<F32>& r, float* to, int tid)
 
 // The way back: rows of LDS, each scaled by its token's `by` (nullptr: 1). The
 // gradient of a bf16 tensor is rounded once, here.
-template <bool F32>
+template <bool F32, int NT>
 __device__ __forceinline__ void store_rows(void* p, const float* from, const float* by, const BwdArgs& a,
                                            const Chunk& ck, int h, int tid) {
-    const Place<F32> at(a, tid);
+    const Place<F32, NT> at(a, tid);
     const int c = at.c;
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    for (int i = 0; i < Rows<F32, NT>::n; ++i) {
         const int t = at.t + at.step * i;
         if (t >= ck.nv) continue;
         const float f = by ? by[t] : 1.f;
@@ -202,8 +203,13 @@ __device__ __forceinline__ void store_rows(void* p, const float* from, const flo
 // The gates of this lane's channel and half chunk: G holds them as rows, gs
 // one per token (scalar gate).
 __device__ __forceinline__ void read_gates(float (&g)[16], const BwdArgs& a, const float* G, const float* gs, int c, int half) {
+    if (a.scalar_gate) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) g[i] = a.scalar_gate ? gs[16 * half + i] : G[(16 * half + i) * LD + c];
+        for (int i = 0; i < 16; ++i) g[i] = gs[16 * half + i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) g[i] = G[(16 * half + i) * LD + c];
+    }
 }
 
 __device__ __forceinline__ void scan_gates(Gates& s, const float (&g)[16], int half) {
@@ -231,20 +237,20 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C], gs[C];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     // everything from memory at once: the latency of one fetch, not of three
-    Rows<F32> rk, rq;
-    Rows<true> rg;
-    load_rows<F32>(rk, a.k, a, ck, h, tid);
-    load_rows<F32>(rq, a.q, a, ck, h, tid);
-    if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
+    Rows<F32, 256> rk, rq;
+    Rows<true, 256> rg;
+    load_rows<F32, 256>(rk, a.k, a, ck, h, tid);
+    load_rows<F32, 256>(rq, a.q, a, ck, h, tid);
+    if (!a.scalar_gate) load_rows<true, 256>(rg, a.g, a, ck, h, tid);
     if (tid < C) {
         const float b = tid < ck.nv ? a.beta[(ck.tok + tid) * a.H + h] : 0.f;
         bs[tid] = b;
         a.b[ch * C + tid] = b;
         if (a.scalar_gate) gs[tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
     }
-    put_rows<F32>(rk, Kd, tid);
-    put_rows<F32>(rq, Qd, tid);
-    if (!a.scalar_gate) put_rows<true>(rg, Ki, tid);
+    put_rows<F32, 256>(rk, Kd, tid);
+    put_rows<F32, 256>(rq, Qd, tid);
+    if (!a.scalar_gate) put_rows<true, 256>(rg, Ki, tid);
     lds_barrier();
     {
         // wave w owns channels 32 w .. 32 w + 31, one lane per channel and half
@@ -713,8 +719,13 @@ __global__ __launch_bounds__(256, 3) void kda_bwd_walks(BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ 3 grads
+// Eight waves of 16 channels each: two workgroups a compute unit (LDS) are then
+// four waves a SIMD, which hide each other's phases (four waves of 32 channels:
+// 1572 us at T = 8192, H = 96).
+constexpr int kGradThreads = 512;
+
 template <bool F32>
-__global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
+__global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
     const int slot = (int)(blockIdx.x / (unsigned)a.H), h = (int)(blockIdx.x % (unsigned)a.H);
     const Chunk ck = find_chunk(a, slot);
     if (ck.nv <= 0) return;
@@ -722,23 +733,22 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
     // first do, rho, e as [token][v]; then E1, k, q as [token][k]
     __shared__ __align__(16) float R0[C * LD], R1[C * LD], R2[C * LD];
     __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM];
-    __shared__ __align__(16) float up[2][D], dn[2][D], cs[D], dec[D], bs[C], part[4][C];
+    __shared__ __align__(16) float up[2][D], dn[2][D], cs[D], dec[D], bs[C], part[8][C];
+    constexpr int NT = kGradThreads;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     if (tid < C) bs[tid] = a.b[ch * C + tid];
-    st4(Xs + (tid >> 3) * LM + 4 * (tid & 7), ld4(a.X + ch * (C * C) + 4 * tid));
-    f32x4 d0[2], d1[2], e0[2], e1[2];
+    if (tid < 256) st4(Xs + (tid >> 3) * LM + 4 * (tid & 7), ld4(a.X + ch * (C * C) + 4 * tid));
+    const int col = 16 * w + r16;    // this lane's channel in every tile
+    f32x4 d0, d1, e0, e1;
     {
-        Rows<true> rd;
-        load_rows<true>(rd, a.d_o, a, ck, h, tid);
-#pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            const long long o = tile32(ch, 2 * w + ct, 0) + 16 * r16 + g4;
-            d0[ct] = ld4(a.dDT + o);
-            d1[ct] = ld4(a.dDT + o + 256);
-            e0[ct] = ld4(a.eT + o);
-            e1[ct] = ld4(a.eT + o + 256);
-        }
-        put_rows<true>(rd, R0, tid);
+        Rows<true, NT> rd;
+        load_rows<true, NT>(rd, a.d_o, a, ck, h, tid);
+        const long long o = tile32(ch, w, 0) + 16 * r16 + g4;
+        d0 = ld4(a.dDT + o);
+        d1 = ld4(a.dDT + o + 256);
+        e0 = ld4(a.eT + o);
+        e1 = ld4(a.eT + o + 256);
+        put_rows<true, NT>(rd, R0, tid);
     }
     lds_barrier();
     const f32x4 b0 = ld4(bs + g4), b1 = ld4(bs + 16 + g4);
@@ -750,25 +760,21 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
             x10[j] = Xs[(16 + g4 + j) * LM + r16];
             x11[j] = Xs[(16 + g4 + j) * LM + 16 + r16];
         }
+        const f32x4 p0 = mma(x10, d1 * b1, mma(x00, d0 * b0, d0)), p1 = mma(x11, d1 * b1, d1);
 #pragma unroll
-        for (int ct = 0; ct < 2; ++ct) {
-            const int col = 32 * w + 16 * ct + r16;
-            const f32x4 p0 = mma(x10, d1[ct] * b1, mma(x00, d0[ct] * b0, d0[ct])), p1 = mma(x11, d1[ct] * b1, d1[ct]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int t0 = g4 + j, t1 = 16 + t0;
-                R1[t0 * LD + col] = p0[j];
-                R1[t1 * LD + col] = p1[j];
-                R2[t0 * LD + col] = e0[ct][j];
-                R2[t1 * LD + col] = e1[ct][j];
-            }
+        for (int j = 0; j < 4; ++j) {
+            const int t0 = g4 + j, t1 = 16 + t0;
+            R1[t0 * LD + col] = p0[j];
+            R1[t1 * LD + col] = p1[j];
+            R2[t0 * LD + col] = e0[j];
+            R2[t1 * LD + col] = e1[j];
         }
     }
     lds_barrier();
-    store_rows<F32>(a.dv, R1, bs, a, ck, h, tid);
+    store_rows<F32, NT>(a.dv, R1, bs, a, ck, h, tid);
     // dM, dB and dbeta from do e^T and rho e^T: tiles (0,0), (1,1), (1,0) of each
-    for (int i = w; i < 6; i += 4) {
-        const int tile = i % 3, ro = tile ? 16 : 0, co = tile == 1 ? 16 : 0;
+    if (w < 6) {
+        const int i = w, tile = i % 3, ro = tile ? 16 : 0, co = tile == 1 ? 16 : 0;
         const float* A = i < 3 ? R0 : R1;
         f32x4 x = splat(0.f);
 #pragma unroll
@@ -786,62 +792,44 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
             }
         }
     }
-    // k, q and g for later, on their way behind the products
-    Rows<F32> rk, rq;
-    Rows<true> rg;
-    if (!a.scalar_gate) load_rows<true>(rg, a.g, a, ck, h, tid);
-    load_rows<F32>(rk, a.k, a, ck, h, tid);
-    load_rows<F32>(rq, a.q, a, ck, h, tid);
+    // k, q and g for later, on their way behind the products (fetched behind
+    // them instead: 1579 -> 1790 us)
+    Rows<F32, NT> rk, rq;
+    Rows<true, NT> rg;
+    if (!a.scalar_gate) load_rows<true, NT>(rg, a.g, a, ck, h, tid);
+    load_rows<F32, NT>(rk, a.k, a, ck, h, tid);
+    load_rows<F32, NT>(rq, a.q, a, ck, h, tid);
     if (a.scalar_gate && tid < C) part[0][tid] = tid < ck.nv ? a.g[(ck.tok + tid) * a.H + h] : 0.f;
-    // products with the states: each wave its own 32 channels
-    f32x4 qS[2][2], rS[2][2], eS[2][2];
-    float sd[2] = {0.f, 0.f};
+    // products with the states
+    f32x4 qS[2], rS[2], eS[2];
+    float sd = 0.f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) qS[i][kt] = rS[i][kt] = eS[i][kt] = splat(0.f);
-    const float* Sp = a.S + tileS(ch, 0, 2 * w);
-    const float* dSp = a.dS + tileS(ch, 0, 2 * w);
-    f32x4 sn[2], dsn[2];     // 16 columns of v ahead
-    const auto load_states = [&](int vb) {
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            sn[kt] = ld4t(Sp + (8 * vb + kt) * 256, r16, g4);
-            dsn[kt] = ld4t(dSp + (8 * vb + kt) * 256, r16, g4);
-        }
-    };
-    load_states(0);
+    for (int i = 0; i < 2; ++i) qS[i] = rS[i] = eS[i] = splat(0.f);
+    const float* Sp = a.S + tileS(ch, 0, w);
+    const float* dSp = a.dS + tileS(ch, 0, w);
+    f32x4 sn = ld4t(Sp, r16, g4), dsn = ld4t(dSp, r16, g4);   // 16 columns of v ahead
 #pragma unroll 2
     for (int vb = 0; vb < 8; ++vb) {
-        f32x4 s[2], ds[2];
+        const f32x4 s = sn, ds = dsn;
+        const int nb = min(vb + 1, 7) * 8 * 256;
+        sn = ld4t(Sp + nb, r16, g4);
+        dsn = ld4t(dSp + nb, r16, g4);
 #pragma unroll
-        for (int kt = 0; kt < 2; ++kt) {
-            s[kt] = sn[kt];
-            ds[kt] = dsn[kt];
-        }
-        if (vb < 7) load_states(vb + 1);
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sd[kt] += s[kt][j] * ds[kt][j];
+        for (int j = 0; j < 4; ++j) sd += s[j] * ds[j];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int o = (16 * i + r16) * LD + 16 * vb + g4;
-            const f32x4 x = ld4(R0 + o), y = ld4(R1 + o), z = ld4(R2 + o);
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt) {
-                qS[i][kt] = mma(x, s[kt], qS[i][kt]);
-                rS[i][kt] = mma(y, s[kt], rS[i][kt]);
-                eS[i][kt] = mma(z, ds[kt], eS[i][kt]);
-            }
+            qS[i] = mma(ld4(R0 + o), s, qS[i]);
+            rS[i] = mma(ld4(R1 + o), s, rS[i]);
+            eS[i] = mma(ld4(R2 + o), ds, eS[i]);
         }
     }
     lds_barrier();
-    if (!a.scalar_gate) put_rows<true>(rg, R0, tid);
-    put_rows<F32>(rk, R1, tid);
-    put_rows<F32>(rq, R2, tid);
+    if (!a.scalar_gate) put_rows<true, NT>(rg, R0, tid);
+    put_rows<F32, NT>(rk, R1, tid);
+    put_rows<F32, NT>(rq, R2, tid);
     lds_barrier();
-    {
+    if (w < 4) {
         const int c = 32 * w + (l & 31), half = l >> 5;
         float g[16];
         read_gates(g, a, R0, part[0], c, half);
@@ -857,24 +845,16 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
         for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = expf(s.L[i] - s.m);
     }
     lds_barrier();
-    const f32x4 M00 = ld4(dMs + r16 * LM + g4), M10 = ld4(dMs + (16 + r16) * LM + g4),
-                M11 = ld4(dMs + (16 + r16) * LM + 16 + g4);
-    const f32x4 N00 = ld4(dBs + r16 * LM + g4), N10 = ld4(dBs + (16 + r16) * LM + g4),
-                N11 = ld4(dBs + (16 + r16) * LM + 16 + g4);
-    f32x4 M00t, M10t, M11t, N00t, N10t, N11t;
+    // fragments of dM and dB, and of their transposes
+    const auto row_of = [&](const float* p, int i, int j) { return ld4(p + (16 * i + r16) * LM + 16 * j + g4); };
+    const auto col_of = [&](const float* p, int i, int j) {
+        f32x4 y;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        M00t[j] = dMs[(g4 + j) * LM + r16];
-        M10t[j] = dMs[(16 + g4 + j) * LM + r16];
-        M11t[j] = dMs[(16 + g4 + j) * LM + 16 + r16];
-        N00t[j] = dBs[(g4 + j) * LM + r16];
-        N10t[j] = dBs[(16 + g4 + j) * LM + r16];
-        N11t[j] = dBs[(16 + g4 + j) * LM + 16 + r16];
-    }
-    f32x4 dgs[2] = {splat(0.f), splat(0.f)};   // scalar gate: this lane's channels summed
-#pragma unroll
-    for (int ct = 0; ct < 2; ++ct) {
-        const int col = 32 * w + 16 * ct + r16;
+        for (int u = 0; u < 4; ++u) y[u] = p[(16 * i + g4 + u) * LM + 16 * j + r16];
+        return y;
+    };
+    f32x4 dG[2];
+    {
         f32x4 E1[2], E2[2], kk[2], qq[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -890,20 +870,19 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
                     qd0 = qq[0] * E1[0], qd1 = qq[1] * E1[1];
         const f32x4 z = splat(0.f), x = splat(cs[col]);
         f32x4 dq[2], row[2], cl[2];
-        dq[0] = mma(M00, ki0, z);
-        dq[1] = mma(M11, ki1, mma(M10, ki0, z) * x);
-        row[0] = mma(N00, ki0, z);
-        row[1] = mma(N11, ki1, mma(N10, ki0, z) * x);
-        cl[0] = mma(N00t, kd0, mma(M00t, qd0, mma(N10t, kd1, mma(M10t, qd1, z)) * x));
-        cl[1] = mma(N11t, kd1, mma(M11t, qd1, z));
-        f32x4 dG[2];
+        dq[0] = mma(row_of(dMs, 0, 0), ki0, z);
+        dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0, z) * x);
+        row[0] = mma(row_of(dBs, 0, 0), ki0, z);
+        row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0, z) * x);
+        cl[0] = mma(col_of(dBs, 0, 0), kd0, mma(col_of(dMs, 0, 0), qd0, mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x));
+        cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
         float end = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const f32x4 bb = i ? b1 : b0, u = splat(up[i][col]);
-            const f32x4 q_ = E1[i] * (dq[i] + u * qS[i][ct]);
-            const f32x4 r_ = E1[i] * (row[i] - u * (bb * rS[i][ct]));
-            const f32x4 cy = E2[i] * splat(dn[i][col]) * (bb * eS[i][ct]);
+            const f32x4 q_ = E1[i] * (dq[i] + u * qS[i]);
+            const f32x4 r_ = E1[i] * (row[i] - u * (bb * rS[i]));
+            const f32x4 cy = E2[i] * splat(dn[i][col]) * (bb * eS[i]);
             const f32x4 c_ = E2[i] * cl[i] + cy;
             dG[i] = qq[i] * q_ + kk[i] * (r_ - c_);
 #pragma unroll
@@ -914,7 +893,7 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
                 R2[o] = q_[j];
             }
         }
-        end += dec[col] * sd[ct];
+        end += dec[col] * sd;
         end += __shfl_xor(end, 16);
         end += __shfl_xor(end, 32);
         // dg: sum over the tokens from t on
@@ -937,30 +916,32 @@ __global__ __launch_bounds__(256, 2) void kda_bwd_grads(BwdArgs a) {
         dG[0] += splat(tot[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            if (a.scalar_gate) {
-                dgs[i] += dG[i];
-                continue;
-            }
+            if (a.scalar_gate) continue;
 #pragma unroll
             for (int j = 0; j < 4; ++j) R0[(16 * i + g4 + j) * LD + col] = dG[i][j];
         }
     }
     lds_barrier();
-    store_rows<F32>(a.dk, R1, nullptr, a, ck, h, tid);
-    store_rows<F32>(a.dq, R2, nullptr, a, ck, h, tid);
-    if (!a.scalar_gate) store_rows<true>(a.dg, R0, nullptr, a, ck, h, tid);
+    store_rows<F32, NT>(a.dk, R1, nullptr, a, ck, h, tid);
+    store_rows<F32, NT>(a.dq, R2, nullptr, a, ck, h, tid);
+    if (!a.scalar_gate) store_rows<true, NT>(a.dg, R0, nullptr, a, ck, h, tid);
     if (a.scalar_gate) {
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                float x = dgs[i][j];
+                float x = dG[i][j];
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) x += __shfl_xor(x, o);
                 if (r16 == 0) part[w][16 * i + g4 + j] = x;
             }
         lds_barrier();
-        if (tid < ck.nv) a.dg[(ck.tok + tid) * a.H + h] = part[0][tid] + part[1][tid] + part[2][tid] + part[3][tid];
+        if (tid < ck.nv) {
+            float x = part[0][tid];
+#pragma unroll
+            for (int u = 1; u < 8; ++u) x += part[u][tid];
+            a.dg[(ck.tok + tid) * a.H + h] = x;
+        }
     }
 }
 
@@ -978,7 +959,7 @@ static hipError_t run_bwd(const BwdArgs& a, hipStream_t s) {
     if (walks == 0) return hipSuccess;
     if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_intra<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
     hipLaunchKernelGGL((bwd::kda_bwd_walks<F32, NV>), dim3(walks), dim3(256), 0, s, a);
-    if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_grads<F32>, dim3((unsigned)work), dim3(256), 0, s, a);
+    if (work > 0) hipLaunchKernelGGL(bwd::kda_bwd_grads<F32>, dim3((unsigned)work), dim3(bwd::kGradThreads), 0, s, a);
     return hipGetLastError();
 }
 
