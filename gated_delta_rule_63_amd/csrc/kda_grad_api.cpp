@@ -7,10 +7,11 @@
 #include <stdint.h>
 
 #include "kda_bwd.h"
+#include "kda_host.h"
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using kda::aligned16;
 
 // fp32 values of workspace per (slot, head): X, M, b, decay, five 128 x 32
 // matrices and two states.
@@ -38,9 +39,7 @@ kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, 
     if (st != KDA_OK) return st;
     if ((long long)d->B * d->T > 0 && (!dq || !dk || !dv || !dg || !dbeta)) return KDA_ERR_NULL;
     if (!shape_ok(d)) return KDA_ERR_SHAPE;
-    for (const void* p : {q, k, v, (const void*)d_o, (const void*)dq, (const void*)dk, (const void*)dv})
-        if (!aligned16(p)) return KDA_ERR_UNSUPPORTED;
-    if (!scalar_gate && (!aligned16(g) || !aligned16(dg))) return KDA_ERR_UNSUPPORTED;
+    if (!aligned16(q, k, v, d_o, dq, dk, dv) || (!scalar_gate && !aligned16(g, dg))) return KDA_ERR_UNSUPPORTED;
     const size_t need = kda_bwd_workspace_size(d);
     if (need > 0 && (!d->workspace || d->workspace_bytes < need)) return KDA_ERR_WORKSPACE;
     if (!aligned16(d->workspace)) return KDA_ERR_UNSUPPORTED;
@@ -66,7 +65,7 @@ kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, 
     a.MT = take(32 * 32);
     a.decay = take(128);
     a.b = take(32);
-    return kda::launch_bwd(a, 256, static_cast<hipStream_t>(stream)) == hipSuccess ? KDA_OK : KDA_ERR_HIP;
+    return kda::status(kda::launch_bwd(a, kda::compute_units(), static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace

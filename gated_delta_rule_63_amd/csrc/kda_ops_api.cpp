@@ -3,19 +3,18 @@
 // validation on the host, then kernel launches.
 #include "../../include/kda.h"
 
-#include <atomic>
 #include <math.h>
 #include <stdint.h>
 
 #include "kda_block.h"
+#include "kda_host.h"
 #include "kda_recurrent.h"
 
 namespace {
 
-template <typename... P>
-bool aligned16(const P*... p) {
-    return (... && ((reinterpret_cast<uintptr_t>(p) & 15u) == 0));
-}
+using kda::aligned16;
+using kda::compute_units;
+using kda::status;
 
 template <typename... P>
 bool all_there(const P*... p) {
@@ -28,19 +27,6 @@ kda_status_t check_desc(const kda_desc_t* d) {
     const float* p = &zero;   // never dereferenced
     const int32_t* cu = d && d->num_seqs != d->B ? reinterpret_cast<const int32_t*>(p) : nullptr;
     return kda_fwd_check(p, p, p, p, p, cu, p, p, p, d);
-}
-
-kda_status_t status(hipError_t e) { return e == hipSuccess ? KDA_OK : KDA_ERR_HIP; }
-
-// Compute units of the current device, read once per device.
-int compute_units() {
-    static std::atomic<int> cache[64];
-    int dev = 0, n = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0) return 256;
-    if (dev < 64 && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
-    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) n = 256;
-    if (dev < 64) cache[dev].store(n, std::memory_order_relaxed);
-    return n;
 }
 
 kda_status_t recurrent(bool scalar_gate, const void* q, const void* k, const void* v, const float* g,
