@@ -231,9 +231,14 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     const Chunk ck = find_chunk(a, slot);
     if (ck.nv <= 0) return;
     const long long ch = (long long)h * a.nslots + slot;
+    // 52 KiB, three workgroups a compute unit (two with the tiles below in
+    // memory of their own: 600 us at T = 8192, H = 96)
     __shared__ __align__(16) float Kd[C * LD], KQ[2 * C * LD];
     float *const Ki = KQ, *const Qd = KQ + C * LD;
-    __shared__ __align__(16) float Bs[C * LM], Ms[C * LM], Xs[C * LM];
+    float* const P = KQ;                // [wave][6][64][4], when Ki and Qd have been used
+    float *const Bs = KQ + 4 * 6 * 256, *const Ms = Bs + C * LM;
+    float* const Xs = KQ;               // when the parts have been summed
+    static_assert(4 * 6 * 256 + 2 * C * LM <= 2 * C * LD, "B and M lie behind the parts");
     __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C], gs[C];
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     // everything from memory at once: the latency of one fetch, not of three
@@ -312,7 +317,6 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         pm[2] = mma(qd1 * x, ki0, pm[2]);
     }
     lds_barrier();         // the partial tiles take the place of Ki and Qd
-    float* const P = KQ;     // [wave][6][64][4]: 24 of the 33 KiB
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
         st4(P + ((w * 6 + i) * 64 + l) * 4, pb[i]);
