@@ -197,7 +197,7 @@ def _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar_gate, _devic
     _rows("A_log", A_log, q.shape[2:3], torch.float32, q, _device)
     if dt_bias is not None:
         _rows("dt_bias", dt_bias, gate[2:], torch.float32, q, _device)
-    if lower_bound is not None and not lower_bound < 0:
+    if lower_bound is not None and not ctypes.c_float(lower_bound).value < 0:
         raise ValueError("lower_bound must be negative (None: no bound)")
 
 

@@ -118,6 +118,9 @@ __device__ __forceinline__ Chunk find_chunk(const BwdArgs& a, int slot) {
     return r;
 }
 
+constexpr float kLog2e = 1.44269504088896f;
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }   // to 1 ulp
+
 // The gates of 16 tokens of one channel: this lane's half of the chunk.
 struct Gates {
     float L[16];             // cumulative within the sub-block
@@ -213,9 +216,11 @@ __device__ __forceinline__ void read_gates(float (&g)[16], const BwdArgs& a, con
 }
 
 __device__ __forceinline__ void scan_gates(Gates& s, const float (&g)[16], int half) {
-    s.L[0] = g[0];
+    // in units of log 2, so that an exponential is one instruction: scaling the
+    // gates first rounds like summing them does
+    s.L[0] = g[0] * kLog2e;
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + g[i];
+    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + g[i] * kLog2e;
     s.m = s.L[7];
     const float other = __shfl_xor(s.L[15], 32), mo = __shfl_xor(s.m, 32);
     s.G0 = half ? other : s.L[15];
@@ -265,18 +270,18 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         read_gates(g, a, Ki, gs, c, half);
         Gates s;
         scan_gates(s, g, half);
-        const float up = expf(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
-        const float dn = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
+        const float up = exp2_(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
+        const float dn = exp2_((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
         sc[half][c] = up;
         sc2[half][c] = dn;
         if (half == 0) {
-            cs[c] = expf(s.m1 + s.G0 - s.m0);
-            a.decay[ch * D + c] = expf(s.G0 + s.G1);
+            cs[c] = exp2_(s.m1 + s.G0 - s.m0);
+            a.decay[ch * D + c] = exp2_(s.G0 + s.G1);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int o = (16 * half + i) * LD + c;
-            const float kk = Kd[o], E1 = expf(s.L[i] - s.m), E2 = expf(s.m - s.L[i]);
+            const float kk = Kd[o], E1 = exp2_(s.L[i] - s.m), E2 = exp2_(s.m - s.L[i]);
             Kd[o] = kk * E1;
             Ki[o] = kk * E2;
             Qd[o] *= E1;
@@ -839,14 +844,14 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         read_gates(g, a, R0, part[0], c, half);
         Gates s;
         scan_gates(s, g, half);
-        up[half][c] = expf(s.m + (half ? s.G0 : 0.f));
-        dn[half][c] = expf((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
+        up[half][c] = exp2_(s.m + (half ? s.G0 : 0.f));
+        dn[half][c] = exp2_((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
         if (half == 0) {
-            cs[c] = expf(s.m1 + s.G0 - s.m0);
-            dec[c] = expf(s.G0 + s.G1);
+            cs[c] = exp2_(s.m1 + s.G0 - s.m0);
+            dec[c] = exp2_(s.G0 + s.G1);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = expf(s.L[i] - s.m);
+        for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = exp2_(s.L[i] - s.m);
     }
     lds_barrier();
     // fragments of dM and dB, and of their transposes

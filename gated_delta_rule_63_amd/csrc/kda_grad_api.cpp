@@ -29,7 +29,8 @@ bool shape_ok(const kda_desc_t* d) {
     static const float zero = 0.f;
     const float* p = &zero;   // never dereferenced
     const int32_t* cu = d && d->num_seqs != d->B ? reinterpret_cast<const int32_t*>(p) : nullptr;
-    return kda_fwd_check(p, p, p, p, p, cu, p, p, p, d) == KDA_OK && d->H <= (1 << 16) && max_slots(d) * d->H <= (1LL << 23);
+    return kda_fwd_check(p, p, p, p, p, cu, p, p, p, d) == KDA_OK && d->H <= (1 << 16) &&
+           (long long)d->num_seqs * d->H <= (1 << 22) && max_slots(d) * d->H <= (1LL << 23);
 }
 
 kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, const float* g, const float* beta,

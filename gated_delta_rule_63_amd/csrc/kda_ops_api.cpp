@@ -58,7 +58,7 @@ constexpr long long kMaxRows = 1LL << 29;
 kda_status_t check_block(const kda_desc_t* d, float eps) {
     const kda_status_t st = check_desc(d);
     if (st != KDA_OK) return st;
-    if ((long long)d->B * d->T > kMaxRows / d->H) return KDA_ERR_SHAPE;
+    if (d->H > (1 << 16) || (long long)d->B * d->T > kMaxRows / d->H) return KDA_ERR_SHAPE;
     return eps >= 0.f && isfinite(eps) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
@@ -109,6 +109,7 @@ kda_status_t block_in_bwd(bool scalar_gate, const void* q, const void* k, const 
     if (!aligned16(dq_out, dk_out, dq, dk) || (!scalar_gate && !aligned16(dg, df))) return KDA_ERR_UNSUPPORTED;
     const size_t need = block_in_bytes(scalar_gate, d);
     if (need > 0 && (!d->workspace || d->workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(d->workspace)) return KDA_ERR_UNSUPPORTED;
     a.dq_out = dq_out; a.dk_out = dk_out; a.dg = dg; a.dbeta = dbeta;
     a.dq = dq; a.dk = dk; a.df = df; a.db = db; a.dA_log = dA_log; a.ddt_bias = ddt_bias;
     a.part = static_cast<float*>(d->workspace);
@@ -198,6 +199,7 @@ kda_status_t kda_block_out_bwd(const float* o, const void* z, const float* weigh
     if (!aligned16(dy, d_o, dz)) return KDA_ERR_UNSUPPORTED;
     const size_t need = kda_block_out_bwd_workspace_size(desc);
     if (need > 0 && (!desc->workspace || desc->workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+    if (!aligned16(desc->workspace)) return KDA_ERR_UNSUPPORTED;
     a.dy = dy; a.d_o = d_o; a.dz = dz; a.dweight = dweight;
     a.part = static_cast<float*>(desc->workspace);
     return status(kda::launch_block_out_bwd(a, static_cast<hipStream_t>(stream)));

@@ -333,10 +333,11 @@ kda_status_t kda_fwd_staged(const void* q, const void* k, const void* v, const f
  *     dh0         [N, H, 128, 128] fp32 (NULL: not written)
  * q, k, v, g, beta, cu_seqlens, h0 are the forward's own inputs (states inside
  * the sequences are recomputed, nothing is kept from the forward); d_o is
- * [B, T, H, 128] fp32. Every tensor with rows of 128 channels is 16-byte aligned
- * (KDA_ERR_UNSUPPORTED otherwise), H at most 65,536 and chunks of 32 tokens times
- * heads at most 2^23 (KDA_ERR_SHAPE). Rows of tokens outside [cu[0], cu[N]) are
- * left as they were. A zero-length sequence has dh0 = dhT.
+ * [B, T, H, 128] fp32. Tensors with rows of 128 channels and the workspace are
+ * 16-byte aligned (KDA_ERR_UNSUPPORTED otherwise); H is at most 65,536,
+ * (sequence, head) pairs at most 2^22 and chunks of 32 tokens times heads at
+ * most 2^23 (KDA_ERR_SHAPE). Rows of tokens outside [cu[0], cu[N]) are left as
+ * they were. A zero-length sequence has dh0 = dhT.
  * Needs desc->workspace of kda_bwd_workspace_size(desc) bytes, 16-byte aligned
  * (KDA_ERR_WORKSPACE when missing or smaller); nothing is allocated, so the call
  * may be captured. A workspace is used by one call at a time.
@@ -415,7 +416,7 @@ kda_status_t kda_gdn_recurrent(const void* q, const void* k, const void* v, cons
  * desc: shapes and in_dtype; num_seqs is not used beyond kda_fwd's checks. A
  * positive or non-finite lower_bound, a negative or non-finite eps, or a pointer
  * to rows of 128 channels that is not 16-byte aligned is KDA_ERR_UNSUPPORTED;
- * more than 2^29 (token, head) rows is KDA_ERR_SHAPE. q_out == q and k_out == k
+ * more than 2^29 (token, head) rows or 65,536 heads is KDA_ERR_SHAPE. q_out == q and k_out == k
  * are allowed. With eps == 0 a zero row gives NaN. */
 kda_status_t kda_block_in(const void* q, const void* k, const void* f, const void* b, const float* A_log,
                           const float* dt_bias, float lower_bound, float eps, void* q_out, void* k_out,
@@ -429,8 +430,8 @@ kda_status_t kda_gdn_block_in(const void* q, const void* k, const void* f, const
  * dg and dbeta (fp32) the gradients with respect to its outputs; dq, dk, df, db
  * (in_dtype), dA_log [H] and ddt_bias (fp32, like dt_bias; NULL: not written)
  * the results. No output may overlap an input. Needs desc->workspace of
- * kda_block_in_bwd_workspace_size(desc) bytes (KDA_ERR_WORKSPACE), used by one
- * call at a time; sums over tokens are fp32 in a fixed order. T = 0 gives zero
+ * kda_block_in_bwd_workspace_size(desc) bytes (KDA_ERR_WORKSPACE), 16-byte
+ * aligned, used by one call at a time; sums over tokens are fp32 in a fixed order. T = 0 gives zero
  * sums. */
 kda_status_t kda_block_in_bwd(const void* q, const void* k, const void* f, const void* b, const float* A_log,
                               const float* dt_bias, float lower_bound, float eps, const void* dq_out,

@@ -104,7 +104,7 @@ def test_binding_refusals():
     ok()
     ok(bound=-5.0, bias=None)
     ok(f=b, bias=z(4), dg=b, s=True)
-    for kw in (dict(q=q.half()), dict(k=q.bfloat16()), dict(f=b), dict(b=z(2, 3)), dict(A=z(3)), dict(bias=z(4)),
+    for kw in (dict(bound=-1e-50), dict(q=q.half()), dict(k=q.bfloat16()), dict(f=b), dict(b=z(2, 3)), dict(A=z(3)), dict(bias=z(4)),
                dict(bound=5.0), dict(bound=0.0), dict(dg=q.bfloat16()), dict(dq=z(2, 3, 4, 64)),
                dict(k=z(2, 3, 128, 4).transpose(2, 3))):
         with pytest.raises(ValueError):
@@ -211,6 +211,26 @@ def test_no_tokens(gpu):
     got = kda.block_in_bwd(q, q, q, b, A, q, q, q, b, dt_bias=bias)
     assert not bool(got[4].any()) and not bool(got[5].any())
     assert kda.block_out(q, q, e(128)).numel() == 0 and not bool(kda.block_out_bwd(q, q, e(128), q)[2].any())
+
+
+@pytest.mark.gpu
+def test_in_place(gpu):
+    """What include/kda.h allows to share memory does."""
+    import gated_delta_rule_63_amd as kda
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    B, T, H = 2, 65, 5
+    q, k, f, b, A, o, z, w, dy = (n(B, T, H, 128), n(B, T, H, 128), n(B, T, H, 128), n(B, T, H), n(H), n(B, T, H, 128),
+                                  n(B, T, H, 128), n(128), n(B, T, H, 128))
+    want = kda.block_in(q, k, f, b, A), kda.block_out_bwd(o, z, w, dy)
+    g, beta, dw, ws = torch.empty_like(f), torch.empty_like(b), torch.empty_like(w), torch.empty(1 << 20, device="cuda")
+    d = kda.Desc(B, T, H, 128, 128, B, 1, 1, ws.data_ptr(), ws.numel() * 4)
+    p = lambda x: ctypes.c_void_p(x.data_ptr())
+    L = kda.lib()
+    assert L.kda_block_in(p(q), p(k), p(f), p(b), p(A), None, 0.0, 1e-6, p(q), p(k), p(g), p(beta), ctypes.byref(d), None) == 0
+    assert L.kda_block_out_bwd(p(o), p(z), p(w), 1e-5, 0, p(dy), p(o), p(dy), p(dw), ctypes.byref(d), None) == 0
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip((q, k, g, beta, o, dy, dw), (*want[0], *want[1])))
 
 
 @pytest.mark.gpu

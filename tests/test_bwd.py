@@ -80,6 +80,12 @@ def test_refusals():
         for name in ("q", "k", "v", "g", "beta", "do", "dq", "dk", "dv", "dg", "db"):
             assert call(d(), fn, **{name: None}) == -1, name
         assert call(d(), fn, do=ctypes.c_void_p(0x10004)) == -3          # not 16-byte aligned
+        for name in ("q", "k", "v", "dq", "dk", "dv"):
+            assert call(d(), fn, **{name: ctypes.c_void_p(0x10008)}) == -3, name
+        x = d()
+        x.workspace = 0x10008
+        assert call(x, fn) == -3
+        assert call(d(H=1 << 17, T=1), fn) == -2 and call(d(B=1 << 13, T=1, H=1 << 10, N=1 << 13), fn) == -2
         assert call(d(ws=0), fn) == -5 and call(d(ws=4 * 221824 - 1), fn) == -5
         assert call(d(B=1 << 12, T=1 << 16, H=64, N=1 << 12), fn) == -2  # 2^29 chunks
     # two chunks of two heads; with B == N == 1 the packed use may need one slot more
@@ -160,6 +166,9 @@ CASES = [
     (W.variant("tiny_fp32", T=65, H=2, gate="mild", keys="onehot"), False),
     (W.variant("tiny_fp32", T=40, H=2, beta="zero", h0=True), True),
     (W.variant("T8192_H96", T=515, H=17, gate="mild"), False),
+    # above 32 (sequence, head) pairs the walks take 32 columns of V at a time
+    (W.variant("T8192_H96", T=98, H=24, seq_lens=(0, 33, 1, 64), h0=True), True),
+    (W.variant("tiny_fp32", B=3, T=35, H=20, gate="mild", h0=True), True),
 ]
 
 
@@ -177,6 +186,7 @@ def test_bwd(torch_gpu, cfg, dhT):
 @pytest.mark.parametrize("cfg", [
     W.variant("tiny_fp32", B=2, T=67, H=3, gate="scalar", h0=True),
     W.variant("T8192_H96", T=130, H=2, seq_lens=(64, 1, 0, 65), gate="scalar_mild", h0=True),
+    W.variant("T8192_H96", T=71, H=20, seq_lens=(40, 31), gate="scalar", h0=True),
 ], ids=lambda c: c.name)
 def test_gdn_bwd(torch_gpu, cfg):
     inp = W.make_inputs(cfg, 8)
@@ -278,3 +288,40 @@ def test_bwd_leaves_other_rows(torch_gpu):
     assert all(bool((x[:, 70:] == 7.0).all()) for x in outs)
     ref = rule_bwd(inp.q, inp.k, inp.v, inp.g, inp.beta, do, inp.seq_bounds(), inp.h0, dh)
     _check([x[:, :70] for x in outs] + [state], ref, inp, "padded")
+
+
+@pytest.mark.gpu
+def test_bwd_without_tokens(torch_gpu):
+    """T = 0: empty gradients, and the state's passes through."""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    e = lambda *s: torch.zeros(*s, device="cuda")
+    q, b, dh = e(2, 0, 3, 128), e(2, 0, 3), torch.randn(2, 3, 128, 128, device="cuda")
+    got = kda.bwd(q, q, q, q, b, q, initial_state=dh, d_final_state=dh)
+    assert all(x.numel() == 0 for x in got[:5]) and torch.equal(got[5], dh)
+    got = kda.gdn_bwd(q, q, q, b, b, q)
+    assert not bool(got[5].any())
+
+
+@pytest.mark.gpu
+def test_bwd_in_segments(torch_gpu):
+    """A sequence's gradient in two calls, the second segment's state gradient handed to
+    the first, is the gradient in one. The state between them comes from recurrent(),
+    fp32 throughout; both ways are held to 1e-4 of the RMS each."""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    from gpu_util import to_device
+    inp = W.make_inputs(W.variant("tiny_fp32", T=2500, H=3, gate="mild", h0=True), 9)
+    do, dh = (torch.from_numpy(x).cuda() for x in _grads(inp, 10))
+    t = to_device(inp, "fp32")
+    x = [t[n] for n in ("q", "k", "v", "g", "beta")] + [do]
+    whole = kda.bwd(*x, initial_state=t["h0"], d_final_state=dh)
+    cut = 1111
+    one, two = [u[:, :cut].contiguous() for u in x], [u[:, cut:].contiguous() for u in x]
+    mid = t["h0"].clone()
+    kda.recurrent(*one[:5], mid)
+    b = kda.bwd(*two, initial_state=mid, d_final_state=dh)
+    a = kda.bwd(*one, initial_state=t["h0"], d_final_state=b[5])
+    for name, w, u, v in zip("dq dk dv dg dbeta".split(), whole, a, b):
+        within(torch.cat([u, v], 1).cpu().numpy(), w.cpu().numpy(), name, tol=2e-4)
+    within(a[5].cpu().numpy(), whole[5].cpu().numpy(), "dh0", tol=2e-4)
