@@ -29,11 +29,11 @@
 // leaves (g, beta, the states) come out with fp32 accuracy, and dg is a sum of
 // differences that cancel, where 16-bit operands would leave an error of 1e-3.
 //
-// Gates inside a chunk: two sub-blocks of 16 tokens, each with its own
-// cumulative sum L and its value m after 8 tokens; E1 = e^(L - m) and
-// 1 / E1 stay within e^+-40 for g >= -5. A product within a sub-block pairs
-// E1 with 1 / E1; from sub-block 0 to 1 the same factors are scaled by
-// cs = e^(m_1 + G_0 - m_0) per channel.
+// Gates inside a chunk: two sub-blocks of 16 tokens, each with its decay E1
+// counted from behind its eighth token; E1 and 1 / E1 stay within e^+-40 for
+// g >= -5. A product within a sub-block pairs E1 with 1 / E1; from sub-block 0
+// to 1 the same factors are scaled by cs, the decay from the middle of the one
+// to the middle of the other, per channel.
 #include "kda_bwd.h"
 #include "kda_device.h"
 
@@ -121,10 +121,14 @@ __device__ __forceinline__ Chunk find_chunk(const BwdArgs& a, int slot) {
 constexpr float kLog2e = 1.44269504088896f;
 __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }   // to 1 ulp
 
-// The gates of 16 tokens of one channel: this lane's half of the chunk.
+// The gates of 16 tokens of one channel, this lane's half of the chunk, in
+// units of log 2, so that an exponential is one instruction. Summed from the
+// middle outwards: the sums stay short, and so does their rounding, which every
+// decay inherits.
 struct Gates {
-    float L[16];             // cumulative within the sub-block
-    float m, G0, G1, m0, m1; // its value after 8 tokens; the sub-blocks' totals and midpoints
+    float L[16];             // sum of the gates from behind token 7 to t (negated for t < 7)
+    float m0, t0, m1, t1;    // sums of tokens 0 .. 7 and 8 .. 15 of both sub-blocks
+    float up, dn, cs, total; // exponents: e^G = E1 2^up, e^(G_last - G) = 2^dn / E1, see cs above
 };
 
 // Rows of a [tokens, H, 128] tensor, one chunk of them: 16 bytes a lane and
@@ -215,18 +219,23 @@ __device__ __forceinline__ void read_gates(float (&g)[16], const BwdArgs& a, con
     }
 }
 
-__device__ __forceinline__ void scan_gates(Gates& s, const float (&g)[16], int half) {
-    // in units of log 2, so that an exponential is one instruction: scaling the
-    // gates first rounds like summing them does
-    s.L[0] = g[0] * kLog2e;
+__device__ __forceinline__ void scan_gates(Gates& s, float (&g)[16], int half) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s.L[i] = s.L[i - 1] + g[i] * kLog2e;
-    s.m = s.L[7];
-    const float other = __shfl_xor(s.L[15], 32), mo = __shfl_xor(s.m, 32);
-    s.G0 = half ? other : s.L[15];
-    s.G1 = half ? s.L[15] : other;
-    s.m0 = half ? mo : s.m;
-    s.m1 = half ? s.m : mo;
+    for (int i = 0; i < 16; ++i) g[i] *= kLog2e;
+    s.L[7] = 0.f;
+#pragma unroll
+    for (int i = 6; i >= 0; --i) s.L[i] = s.L[i + 1] - g[i + 1];
+#pragma unroll
+    for (int i = 8; i < 16; ++i) s.L[i] = s.L[i - 1] + g[i];
+    const float m = g[0] - s.L[0], t = s.L[15], mo = __shfl_xor(m, 32), to = __shfl_xor(t, 32);
+    s.m0 = half ? mo : m;
+    s.t0 = half ? to : t;
+    s.m1 = half ? m : mo;
+    s.t1 = half ? t : to;
+    s.up = half ? (s.m0 + s.t0) + s.m1 : s.m0;
+    s.dn = half ? s.t1 : s.t0 + (s.m1 + s.t1);
+    s.cs = s.m1 + s.t0;
+    s.total = (s.m0 + s.t0) + (s.m1 + s.t1);
 }
 
 // ------------------------------------------------------------------ 1 intra
@@ -270,18 +279,16 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         read_gates(g, a, Ki, gs, c, half);
         Gates s;
         scan_gates(s, g, half);
-        const float up = exp2_(s.m + (half ? s.G0 : 0.f));                    // e^G = E1 up
-        const float dn = exp2_((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));  // e^(G_last - G) = dn / E1
-        sc[half][c] = up;
-        sc2[half][c] = dn;
+        sc[half][c] = exp2_(s.up);
+        sc2[half][c] = exp2_(s.dn);
         if (half == 0) {
-            cs[c] = exp2_(s.m1 + s.G0 - s.m0);
-            a.decay[ch * D + c] = exp2_(s.G0 + s.G1);
+            cs[c] = exp2_(s.cs);
+            a.decay[ch * D + c] = exp2_(s.total);
         }
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int o = (16 * half + i) * LD + c;
-            const float kk = Kd[o], E1 = exp2_(s.L[i] - s.m), E2 = exp2_(s.m - s.L[i]);
+            const float kk = Kd[o], E1 = exp2_(s.L[i]), E2 = exp2_(-s.L[i]);
             Kd[o] = kk * E1;
             Ki[o] = kk * E2;
             Qd[o] *= E1;
@@ -844,14 +851,14 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         read_gates(g, a, R0, part[0], c, half);
         Gates s;
         scan_gates(s, g, half);
-        up[half][c] = exp2_(s.m + (half ? s.G0 : 0.f));
-        dn[half][c] = exp2_((half ? s.G1 : s.G0) - s.m + (half ? 0.f : s.G1));
+        up[half][c] = exp2_(s.up);
+        dn[half][c] = exp2_(s.dn);
         if (half == 0) {
-            cs[c] = exp2_(s.m1 + s.G0 - s.m0);
-            dec[c] = exp2_(s.G0 + s.G1);
+            cs[c] = exp2_(s.cs);
+            dec[c] = exp2_(s.total);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = exp2_(s.L[i] - s.m);
+        for (int i = 0; i < 16; ++i) R0[(16 * half + i) * LD + c] = exp2_(s.L[i]);
     }
     lds_barrier();
     // fragments of dM and dB, and of their transposes
@@ -883,30 +890,40 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0, z) * x);
         row[0] = mma(row_of(dBs, 0, 0), ki0, z);
         row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0, z) * x);
-        cl[0] = mma(col_of(dBs, 0, 0), kd0, mma(col_of(dMs, 0, 0), qd0, mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x));
+        const f32x4 cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x;   // from sub-block 1 to 0
+        cl[0] = mma(col_of(dBs, 0, 0), kd0, mma(col_of(dMs, 0, 0), qd0, cross));
         cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
-        float end = 0.f;
+        // What passes the end of each sub-block: end[1] as in the formula at the
+        // top; end[0] is the sum of sub-block 1's dG and end[1] without the pairs
+        // within sub-block 1, which cancel in it. (Summed with them, dg's error
+        // is 1.4 times this.)
+        float end[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const f32x4 bb = i ? b1 : b0, u = splat(up[i][col]);
-            const f32x4 q_ = E1[i] * (dq[i] + u * qS[i]);
-            const f32x4 r_ = E1[i] * (row[i] - u * (bb * rS[i]));
+            const f32x4 qs = u * qS[i], rs = u * (bb * rS[i]);
+            const f32x4 q_ = E1[i] * (dq[i] + qs);
+            const f32x4 r_ = E1[i] * (row[i] - rs);
             const f32x4 cy = E2[i] * splat(dn[i][col]) * (bb * eS[i]);
             const f32x4 c_ = E2[i] * cl[i] + cy;
             dG[i] = qq[i] * q_ + kk[i] * (r_ - c_);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                end += kk[i][j] * cy[j];
+                end[1] += kk[i][j] * cy[j];
+                if (i) end[0] += E1[1][j] * (qq[1][j] * qs[j] - kk[1][j] * rs[j]);
+                else end[0] += kk[0][j] * (E2[0][j] * cross[j] + cy[j]);
                 const int o = (16 * i + g4 + j) * LD + col;   // k and q of this place have been read
                 R1[o] = r_[j] + c_[j];
                 R2[o] = q_[j];
             }
         }
-        end += dec[col] * sd;
-        end += __shfl_xor(end, 16);
-        end += __shfl_xor(end, 32);
-        // dg: sum over the tokens from t on
-        float tot[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            end[i] += dec[col] * sd;
+            end[i] += __shfl_xor(end[i], 16);
+            end[i] += __shfl_xor(end[i], 32);
+        }
+        // dg: sum over the sub-block's tokens from t on
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             dG[i][2] += dG[i][3];
@@ -919,10 +936,8 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
                 const float y = __shfl(x0, (l + 16 * u) & 63);
                 later += (l >> 4) + u < 4 ? y : 0.f;
             }
-            tot[i] = __shfl(x0 + later, r16);
-            dG[i] += splat(later + end);
+            dG[i] += splat(later + end[i]);
         }
-        dG[0] += splat(tot[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             if (a.scalar_gate) continue;
