@@ -29,6 +29,12 @@
 // leaves (g, beta, the states) come out with fp32 accuracy, and dg is a sum of
 // differences that cancel, where 16-bit operands would leave an error of 1e-3.
 //
+// T = 8192, H = 96, bf16, one sequence (786,432 tokens x heads): 450 + 1900 +
+// 1480 us in a row (3.7 ms). 1 is bound by memory (2.2 GB written and read, 4.9
+// TB/s). 2 moves 6.8 GB (3.6 TB/s) and keeps the matrix unit 56% busy, 3 moves
+// 6.2 GB (4.2 TB/s) at 58%. The states that pass from 2 to 3, fp32 [128][128]
+// twice a chunk, are 6.4 of the 15 GB.
+//
 // Gates inside a chunk: two sub-blocks of 16 tokens, each with its decay E1
 // counted from behind its eighth token; E1 and 1 / E1 stay within e^+-40 for
 // g >= -5. A product within a sub-block pairs E1 with 1 / E1; from sub-block 0
@@ -421,7 +427,7 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
 // run in one launch: with NV = 2, 96 chains are 768 workgroups, three on
 // every compute unit (registers and LDS are held to that), where one launch
 // after the other left units with one workgroup beside units with two
-// (T = 8192, H = 96: 913 + 1260 us apart, see the table below together).
+// (T = 8192, H = 96: 913 + 1260 us apart, 1900 together).
 // A chain's V-blocks run on one XCD, whose L2 serves W, kc and qr to all.
 //
 // Operands are fetched for the next chunk as soon as this chunk's have been
@@ -735,9 +741,9 @@ __global__ __launch_bounds__(256, 3) void kda_bwd_walks(BwdArgs a) {
 }
 
 // ------------------------------------------------------------------ 3 grads
-// Eight waves of 16 channels each: two workgroups a compute unit (LDS) are then
-// four waves a SIMD, which hide each other's phases (four waves of 32 channels:
-// 1572 us at T = 8192, H = 96).
+// Eight waves of 16 channels each; LDS holds two workgroups a compute unit, four
+// waves a SIMD. (Four waves of 32 channels are as fast at full size and take
+// 19.0 us for 17.4 where there are 16 chunks.)
 constexpr int kGradThreads = 512;
 
 template <bool F32>
@@ -809,7 +815,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         }
     }
     // k, q and g for later, on their way behind the products (fetched behind
-    // them instead: 1579 -> 1790 us)
+    // them instead, the kernel takes 13% longer)
     Rows<F32, NT> rk, rq;
     Rows<true, NT> rg;
     if (!a.scalar_gate) load_rows<true, NT>(rg, a.g, a, ck, h, tid);
@@ -830,6 +836,9 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         const int nb = min(vb + 1, 7) * 8 * 256;
         sn = ld4t(Sp + nb, r16, g4);
         dsn = ld4t(dSp + nb, r16, g4);
+        // the loads go out here: moved down to their use by the compiler, the
+        // kernel takes 1680 us for 1480 (T = 8192, H = 96)
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int j = 0; j < 4; ++j) sd += s[j] * ds[j];
 #pragma unroll
@@ -871,28 +880,34 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
     };
     f32x4 dG[2];
     {
-        f32x4 E1[2], E2[2], kk[2], qq[2];
+        const auto at = [&](const float* p, int i) {
+            f32x4 y;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
+            for (int u = 0; u < 4; ++u) y[u] = p[(16 * i + g4 + u) * LD + col];
+            return y;
+        };
+        const auto inverse = [&](const f32x4& y) {
+            f32x4 r;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int o = (16 * i + g4 + j) * LD + col;
-                E1[i][j] = R0[o];
-                E2[i][j] = __builtin_amdgcn_rcpf(R0[o]);   // to 1 ulp
-                kk[i][j] = R1[o];
-                qq[i][j] = R2[o];
-            }
-        const f32x4 ki0 = kk[0] * E2[0], ki1 = kk[1] * E2[1], kd0 = kk[0] * E1[0], kd1 = kk[1] * E1[1],
-                    qd0 = qq[0] * E1[0], qd1 = qq[1] * E1[1];
+            for (int u = 0; u < 4; ++u) r[u] = __builtin_amdgcn_rcpf(y[u]);   // to 1 ulp
+            return r;
+        };
         const f32x4 z = splat(0.f), x = splat(cs[col]);
-        f32x4 dq[2], row[2], cl[2];
-        dq[0] = mma(row_of(dMs, 0, 0), ki0, z);
-        dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0, z) * x);
-        row[0] = mma(row_of(dBs, 0, 0), ki0, z);
-        row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0, z) * x);
-        const f32x4 cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x;   // from sub-block 1 to 0
-        cl[0] = mma(col_of(dBs, 0, 0), kd0, mma(col_of(dMs, 0, 0), qd0, cross));
-        cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
+        f32x4 dq[2], row[2], cl[2], cross;   // cross: from sub-block 1 to 0
+        const f32x4 E[2] = {at(R0, 0), at(R0, 1)}, ks[2] = {at(R1, 0), at(R1, 1)}, qv[2] = {at(R2, 0), at(R2, 1)};
+        {
+            const f32x4 ki0 = ks[0] * inverse(E[0]), ki1 = ks[1] * inverse(E[1]);
+            dq[0] = mma(row_of(dMs, 0, 0), ki0, z);
+            dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0, z) * x);
+            row[0] = mma(row_of(dBs, 0, 0), ki0, z);
+            row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0, z) * x);
+        }
+        {
+            const f32x4 kd1 = ks[1] * E[1], qd1 = qv[1] * E[1];
+            cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x;
+            cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
+        }
+        cl[0] = mma(col_of(dBs, 0, 0), ks[0] * E[0], mma(col_of(dMs, 0, 0), qv[0] * E[0], cross));
         // What passes the end of each sub-block: end[1] as in the formula at the
         // top; end[0] is the sum of sub-block 1's dG and end[1] without the pairs
         // within sub-block 1, which cancel in it. (Summed with them, dg's error
@@ -900,18 +915,19 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         float end[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const f32x4 bb = i ? b1 : b0, u = splat(up[i][col]);
+            const f32x4 bb = ld4(bs + 16 * i + g4), u = splat(up[i][col]);
+            const f32x4 E1 = E[i], E2 = inverse(E1), kk = ks[i], qq = qv[i];
             const f32x4 qs = u * qS[i], rs = u * (bb * rS[i]);
-            const f32x4 q_ = E1[i] * (dq[i] + qs);
-            const f32x4 r_ = E1[i] * (row[i] - rs);
-            const f32x4 cy = E2[i] * splat(dn[i][col]) * (bb * eS[i]);
-            const f32x4 c_ = E2[i] * cl[i] + cy;
-            dG[i] = qq[i] * q_ + kk[i] * (r_ - c_);
+            const f32x4 q_ = E1 * (dq[i] + qs);
+            const f32x4 r_ = E1 * (row[i] - rs);
+            const f32x4 cy = E2 * splat(dn[i][col]) * (bb * eS[i]);
+            const f32x4 c_ = E2 * cl[i] + cy;
+            dG[i] = qq * q_ + kk * (r_ - c_);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                end[1] += kk[i][j] * cy[j];
-                if (i) end[0] += E1[1][j] * (qq[1][j] * qs[j] - kk[1][j] * rs[j]);
-                else end[0] += kk[0][j] * (E2[0][j] * cross[j] + cy[j]);
+                end[1] += kk[j] * cy[j];
+                if (i) end[0] += E1[j] * (qq[j] * qs[j] - kk[j] * rs[j]);
+                else end[0] += kk[j] * (E2[j] * cross[j] + cy[j]);
                 const int o = (16 * i + g4 + j) * LD + col;   // k and q of this place have been read
                 R1[o] = r_[j] + c_[j];
                 R2[o] = q_[j];
