@@ -67,8 +67,10 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta
     """Gradient of fwd(). The first arguments are the forward's; do (fp32 [B, T, H, 128],
     16-byte aligned) and d_final_state (fp32 [N, H, 128, 128]; None: zero) are the
     gradients with respect to its outputs. Returns (dq, dk, dv, dg, dbeta,
-    d_initial_state): dq, dk, dv in q's dtype, the others fp32. Nothing is kept from
-    the forward; states are recomputed. workspace: an optional uint8 device tensor of
+    d_initial_state): dq, dk, dv in q's dtype, the others fp32. Rows of tokens that
+    belong to no sequence (cu_seqlens) are unset, as fwd()'s are: hand the first cu[N]
+    tokens alone to block_out() and to the gradients of the block operators, whose sums
+    take every row. Nothing is kept from the forward; states are recomputed. workspace: an optional uint8 device tensor of
     bwd_workspace_size() bytes, used by one call at a time; allocated otherwise."""
     return _bwd("kda_bwd", q, k, v, g, beta, do, cu_seqlens, initial_state, d_final_state, stream, workspace)
 

@@ -10,7 +10,16 @@
 // bytes each way. A row (token, head) is 128 channels on 16 lanes, eight
 // channels each (16 bytes of bf16), so its sums are four exchanges within 16
 // lanes and nothing needs LDS. Norms, gates and sums are fp32; only what is
-// stored in bf16 is rounded, once.
+// stored in bf16 is rounded, once. The forward kernels give each lane group one
+// row: four of them one after the other were slower at every size (T = 8192,
+// H = 96: 252 -> 278 us before the rule, 139 -> 146 after it; 512 rows: 4.0 ->
+// 10.7 and 2.4 -> 4.6).
+//
+// bf16, T = 8192, H = 96: before the rule 279 us (1.41 GB, 5.1 TB/s), after it
+// 139 us (0.81 GB, 5.8 TB/s). Gradients: before, H = 64, 279 + 5 us (1.35 GB, 4.8
+// TB/s), after, 4 x 1001 tokens, H = 64, 88 + 5 us (0.46 GB, 4.9 TB/s). A large
+// copy reaches 4.8 to 5.0. 512 rows of a decode step: 4.0 us, a launch and a trip
+// to memory each way.
 //
 // Sums over tokens (dA_log, ddt_bias, dweight) stay in registers over the rows
 // that a lane group visits, one partial row per group goes to the workspace,
@@ -116,39 +125,37 @@ __device__ __forceinline__ void gate_bwd(float x, float a, float bound, float& d
 
 // ---------------------------------------------------------------------- before
 constexpr int kRows = 16;          // rows of a workgroup at a time
-constexpr int kSteps = 4;          // rows of a lane group of the forward kernels
+// Workgroups that sum over tokens: four per compute unit keep enough in flight
+// and leave few partial rows. T = 8192, H = 64, whole call, with eight per unit
+// instead: scalar gate 174 -> 185 us, fp32 476 -> 554, the gated norm 187 ->
+// 190; with sixteen 172, 486, 194.
+constexpr int kSumGroups = 1024;
 
-template <bool F32, bool SCALAR, int STEPS>
+template <bool F32, bool SCALAR>
 __global__ __launch_bounds__(256) void kda_block_in_kernel(BlockInArgs a) {
-    const int gi = threadIdx.x >> 4, i = threadIdx.x & 15;
-    const long long first = (long long)blockIdx.x * (kRows * STEPS), rows = a.tokens * a.H;
-    const unsigned h0 = (unsigned)(first % a.H);
+    const int i = threadIdx.x & 15;
+    const unsigned row = blockIdx.x * kRows + (threadIdx.x >> 4);   // at most 2^27 of them
+    if (row >= a.tokens * a.H) return;
+    const int h = (int)(row % (unsigned)a.H);
+    const long long o = (long long)row * D + 8 * i;
+    const f32x8 q = ld8<F32>(a.q, o), k = ld8<F32>(a.k, o);
+    const float A = expf(a.A_log[h]);
+    if constexpr (SCALAR) {
+        if (i == 0) a.g[row] = gate(ld_in<F32>(a.f, row) + (a.dt_bias ? a.dt_bias[h] : 0.f), A, a.lower_bound);
+    } else {
+        f32x8 x = ld8<F32>(a.f, o);
+        if (a.dt_bias) x += ld8(a.dt_bias + h * D + 8 * i);
 #pragma unroll
-    for (int step = 0; step < STEPS; ++step) {
-        const int at = step * kRows + gi;
-        const long long row = first + at;
-        if (row >= rows) return;
-        const int h = (int)((h0 + at) % (unsigned)a.H);
-        const long long o = row * D + 8 * i;
-        const f32x8 q = ld8<F32>(a.q, o), k = ld8<F32>(a.k, o);
-        const float A = expf(a.A_log[h]);
-        if constexpr (SCALAR) {
-            if (i == 0) a.g[row] = gate(ld_in<F32>(a.f, row) + (a.dt_bias ? a.dt_bias[h] : 0.f), A, a.lower_bound);
-        } else {
-            f32x8 x = ld8<F32>(a.f, o);
-            if (a.dt_bias) x += ld8(a.dt_bias + h * D + 8 * i);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = gate(x[j], A, a.lower_bound);
-            st8(a.g + o, x);
-        }
-        if (i == 0) {
-            float s, c;
-            sigmoid(ld_in<F32>(a.b, row), s, c);
-            a.beta[row] = s;
-        }
-        st8<F32>(a.q_out, o, q * (1.f / sqrtf(sum16(dot8(q, q)) + a.eps)));
-        st8<F32>(a.k_out, o, k * (1.f / sqrtf(sum16(dot8(k, k)) + a.eps)));
+        for (int j = 0; j < 8; ++j) x[j] = gate(x[j], A, a.lower_bound);
+        st8(a.g + o, x);
     }
+    if (i == 0) {
+        float s, c;
+        sigmoid(ld_in<F32>(a.b, row), s, c);
+        a.beta[row] = s;
+    }
+    st8<F32>(a.q_out, o, q * (1.f / sqrtf(sum16(dot8(q, q)) + a.eps)));
+    st8<F32>(a.k_out, o, k * (1.f / sqrtf(sum16(dot8(k, k)) + a.eps)));
 }
 
 // Gradient of u = x r, r = (|x|^2 + eps)^-1/2:  dx = r (du - u (u . du))
@@ -169,8 +176,8 @@ __host__ __device__ inline Split split(long long tokens, int H) {
     s.hp = H < kRows ? H : kRows;
     s.tp = kRows / s.hp;
     s.hb = (H + s.hp - 1) / s.hp;
-    // about 2048 workgroups, eight per compute unit, each with at least four steps
-    long long nb = (2048 + s.hb - 1) / s.hb;
+    // about kSumGroups workgroups, each with at least four steps
+    long long nb = (kSumGroups + s.hb - 1) / s.hb;
     const long long most = (tokens + 4 * s.tp - 1) / (4 * s.tp);
     if (nb > most) nb = most;
     if (nb < 1) nb = 1;
@@ -273,25 +280,21 @@ __global__ __launch_bounds__(1024) void kda_block_in_sum(BlockInArgs a, long lon
 }
 
 // ----------------------------------------------------------------------- after
-template <bool F32, int STEPS>
+template <bool F32>
 __global__ __launch_bounds__(256) void kda_block_out_kernel(BlockOutArgs a) {
-    const int gi = threadIdx.x >> 4, i = threadIdx.x & 15;
-    const f32x8 w = ld8(a.weight + 8 * i);
+    const int i = threadIdx.x & 15;
+    const long long row = (long long)blockIdx.x * kRows + (threadIdx.x >> 4);
+    if (row >= a.rows) return;
+    const long long at = row * D + 8 * i;
+    const f32x8 w = ld8(a.weight + 8 * i), o = ld8(a.o + at), z = ld8<F32>(a.z, at);
+    f32x8 act;
 #pragma unroll
-    for (int step = 0; step < STEPS; ++step) {
-        const long long row = ((long long)blockIdx.x * STEPS + step) * kRows + gi;
-        if (row >= a.rows) return;
-        const long long at = row * D + 8 * i;
-        const f32x8 o = ld8(a.o + at), z = ld8<F32>(a.z, at);
-        f32x8 act;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            float s, c;
-            sigmoid(z[j], s, c);
-            act[j] = a.silu ? z[j] * s : s;
-        }
-        st8<F32>(a.y, at, o * w * act * (1.f / sqrtf(sum16(dot8(o, o)) * (1.f / D) + a.eps)));
+    for (int j = 0; j < 8; ++j) {
+        float s, c;
+        sigmoid(z[j], s, c);
+        act[j] = a.silu ? z[j] * s : s;
     }
+    st8<F32>(a.y, at, o * w * act * (1.f / sqrtf(sum16(dot8(o, o)) * (1.f / D) + a.eps)));
 }
 
 // n = o r:  do = r (dn - n mean(n dn)), dn = dy w act;  dz = dy n w act';  dw = sum dy n act
@@ -336,26 +339,15 @@ __global__ __launch_bounds__(1024) void kda_block_out_sum(BlockOutArgs a, int P)
     if (threadIdx.x < 32) a.dweight[col] = x;
 }
 
-// Four rows of a lane group one after the other hide the cost of a workgroup's
-// start; too few rows to give every compute unit a workgroup take one each.
-template <typename K1, typename K4, typename A>
-hipError_t forward(K1 one, K4 four, long long rows, const A& a, hipStream_t s) {
-    const bool few = rows < (long long)kRows * kSteps * 256;
-    const long long per = few ? kRows : kRows * kSteps;
-    hipLaunchKernelGGL(few ? one : four, dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0, s, a);
-    return hipGetLastError();
-}
-
 }  // namespace block
 
 int block_in_partials(long long tokens, int H) {
     const block::Split s = block::split(tokens, H);
     return s.nb * s.tp;
 }
-// about 2048 workgroups, eight per compute unit
 int block_out_partials(long long rows) {
     const long long n = (rows + block::kRows - 1) / block::kRows;
-    return (int)(n < 2048 ? n : 2048);
+    return (int)(n < block::kSumGroups ? n : block::kSumGroups);
 }
 
 #define KDA_BLOCK_LAUNCH(kernel, grid, threads, ...) hipLaunchKernelGGL((kernel), dim3(grid), dim3(threads), 0, s, __VA_ARGS__)
@@ -363,7 +355,8 @@ int block_out_partials(long long rows) {
 template <bool F32, bool SCALAR>
 static hipError_t run_block_in(const BlockInArgs& a, hipStream_t s) {
     using namespace block;
-    return forward(kda_block_in_kernel<F32, SCALAR, 1>, kda_block_in_kernel<F32, SCALAR, kSteps>, a.tokens * a.H, a, s);
+    KDA_BLOCK_LAUNCH((kda_block_in_kernel<F32, SCALAR>), (unsigned)((a.tokens * a.H + kRows - 1) / kRows), 256, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_block_in(const BlockInArgs& a, hipStream_t s) {
@@ -395,8 +388,10 @@ hipError_t launch_block_in_bwd(const BlockInArgs& a, hipStream_t s) {
 hipError_t launch_block_out(const BlockOutArgs& a, hipStream_t s) {
     using namespace block;
     if (a.rows == 0) return hipSuccess;
-    if (a.f32) return forward(kda_block_out_kernel<true, 1>, kda_block_out_kernel<true, kSteps>, a.rows, a, s);
-    return forward(kda_block_out_kernel<false, 1>, kda_block_out_kernel<false, kSteps>, a.rows, a, s);
+    const unsigned n = (unsigned)((a.rows + kRows - 1) / kRows);
+    if (a.f32) KDA_BLOCK_LAUNCH(kda_block_out_kernel<true>, n, 256, a);
+    else KDA_BLOCK_LAUNCH(kda_block_out_kernel<false>, n, 256, a);
+    return hipGetLastError();
 }
 
 hipError_t launch_block_out_bwd(const BlockOutArgs& a, hipStream_t s) {

@@ -38,7 +38,7 @@ kda_status_t recurrent(bool scalar_gate, const void* q, const void* k, const voi
     if (pool_dtype != KDA_BF16 && pool_dtype != KDA_F32) return KDA_ERR_DTYPE;
     if (num_slots < 0 || (!slots && num_slots < d->num_seqs)) return KDA_ERR_SHAPE;
     if ((long long)d->num_seqs * d->H > (1LL << 23)) return KDA_ERR_SHAPE;
-    if (d->T == 0 || d->num_seqs == 0) return KDA_OK;
+    if (d->T == 0 || d->num_seqs == 0 || num_slots == 0) return KDA_OK;   // no slot: every place is empty
     if (!pool) return KDA_ERR_NULL;
     if (!aligned16(q, k, v, g, pool, o)) return KDA_ERR_UNSUPPORTED;
     kda::RecurrentArgs a{};
@@ -52,8 +52,9 @@ kda_status_t recurrent(bool scalar_gate, const void* q, const void* k, const voi
     return status(kda::launch_recurrent(a, compute_units(), static_cast<hipStream_t>(stream)));
 }
 
-// Rows of [tokens, H, 128] tensors that the block operators take.
-constexpr long long kMaxRows = 1LL << 29;
+// Rows of [tokens, H, 128] tensors that the block operators take: 16 lanes each,
+// well within a launch's 2^32, and 137 GB in and out for the smaller of the two.
+constexpr long long kMaxRows = 1LL << 27;
 
 kda_status_t check_block(const kda_desc_t* d, float eps) {
     const kda_status_t st = check_desc(d);

@@ -335,9 +335,10 @@ kda_status_t kda_fwd_staged(const void* q, const void* k, const void* v, const f
  * the sequences are recomputed, nothing is kept from the forward); d_o is
  * [B, T, H, 128] fp32. Tensors with rows of 128 channels and the workspace are
  * 16-byte aligned (KDA_ERR_UNSUPPORTED otherwise); H is at most 65,536,
- * (sequence, head) pairs at most 2^22 and chunks of 32 tokens times heads at
- * most 2^23 (KDA_ERR_SHAPE). Rows of tokens outside [cu[0], cu[N]) are left as
- * they were. A zero-length sequence has dh0 = dhT.
+ * (sequence, head) pairs at most 2^20 and chunks of 32 tokens times heads at
+ * most 2^22 (KDA_ERR_SHAPE). Rows of tokens outside [cu[0], cu[N]) are left as
+ * they were (the sums over tokens of kda_block_in_bwd and kda_block_out_bwd take
+ * every row: give those the tokens of the sequences alone). A zero-length sequence has dh0 = dhT.
  * Needs desc->workspace of kda_bwd_workspace_size(desc) bytes, 16-byte aligned
  * (KDA_ERR_WORKSPACE when missing or smaller); nothing is allocated, so the call
  * may be captured. A workspace is used by one call at a time.
@@ -381,7 +382,7 @@ size_t kda_bwd_workspace_size(const kda_desc_t* desc);
  * unless one of the slots is its own.
  * Within a call, a slot that is written may not be read or written for another
  * sequence, nor for two tokens of one (its contents would be undefined; no
- * access leaves the pool). A zero-length sequence changes nothing. The state is
+ * access leaves the pool; num_slots == 0: every place is empty). A zero-length sequence changes nothing. The state is
  * fp32 within the call; a bf16 pool is rounded when a state is written.
  * q, k, v, pool, o and, per channel, g must be 16-byte aligned
  * (KDA_ERR_UNSUPPORTED). num_slots < N without slots, or more than 2^23
@@ -416,7 +417,7 @@ kda_status_t kda_gdn_recurrent(const void* q, const void* k, const void* v, cons
  * desc: shapes and in_dtype; num_seqs is not used beyond kda_fwd's checks. A
  * positive or non-finite lower_bound, a negative or non-finite eps, or a pointer
  * to rows of 128 channels that is not 16-byte aligned is KDA_ERR_UNSUPPORTED;
- * more than 2^29 (token, head) rows or 65,536 heads is KDA_ERR_SHAPE. q_out == q and k_out == k
+ * more than 2^27 (token, head) rows or 65,536 heads is KDA_ERR_SHAPE. q_out == q and k_out == k
  * are allowed. With eps == 0 a zero row gives NaN. */
 kda_status_t kda_block_in(const void* q, const void* k, const void* f, const void* b, const float* A_log,
                           const float* dt_bias, float lower_bound, float eps, void* q_out, void* k_out,

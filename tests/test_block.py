@@ -78,6 +78,7 @@ def test_refusals():
         assert call(True, d=desc(ws=0)) == -5 and call(True, d=desc(ws=4)) == -5
         assert call(False, d=desc(K=64)) == -3 and call(False, d=desc(dt=9)) == -4 and call(False, d=desc(T=-1)) == -2
         assert call(False, d=desc(B=1 << 15, T=1 << 15)) == -2          # 2^31 rows
+        assert call(True, d=desc(B=1 << 14, T=1 << 13, H=2)) == -2       # 2^28
 
     def out(bwd, act=0, eps=1e-5, d=None, **kw):
         a = {n: kw.get(n, P) for n in "o z w".split()}

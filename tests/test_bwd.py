@@ -88,6 +88,7 @@ def test_refusals():
         assert call(d(H=1 << 17, T=1), fn) == -2 and call(d(B=1 << 13, T=1, H=1 << 10, N=1 << 13), fn) == -2
         assert call(d(ws=0), fn) == -5 and call(d(ws=4 * 221824 - 1), fn) == -5
         assert call(d(B=1 << 12, T=1 << 16, H=64, N=1 << 12), fn) == -2  # 2^29 chunks
+        assert call(d(B=1 << 6, T=0, H=1 << 15), fn) == -2               # 2^21 chains without a chunk
     # two chunks of two heads; with B == N == 1 the packed use may need one slot more
     size = lambda x: L.kda_bwd_workspace_size(ctypes.byref(x))
     assert size(d()) == 3 * 2 * 221824 and size(d(B=2, T=33)) == 4 * 2 * 221824

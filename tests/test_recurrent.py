@@ -53,6 +53,7 @@ def test_refusals():
         assert call(fn, slots=None, num=1) == -2                   # fewer slots than sequences
         assert call(fn, B=1 << 20, H=16) == -2                     # 2^24 chains
         assert call(fn, T=0, pool=None) == 0                       # nothing to do
+        assert call(fn, num=0, pool=None) == 0 and call(fn, num=0, q=None) == -1   # a pool without slots
 
 
 def test_binding_refusals():
