@@ -18,7 +18,7 @@ using kda::aligned16;
 constexpr size_t kPerChunk = 2 * 32 * 32 + 32 + 128 + 5 * 128 * 32 + 2 * 128 * 128;
 
 // Slots for either use of the descriptor (it does not say whether cu_seqlens
-// comes with it); more than 2^23 chunks (1.7 TiB) are refused.
+// comes with it); more than 2^22 chunks (930 GB) are refused.
 long long max_slots(const kda_desc_t* d) {
     long long s = kda::bwd_slots(d->B, d->T, d->num_seqs, d->num_seqs != d->B);
     if (d->B == 1) s = std::max(s, kda::bwd_slots(1, d->T, d->num_seqs, true));
@@ -30,7 +30,7 @@ bool shape_ok(const kda_desc_t* d) {
     const float* p = &zero;   // never dereferenced
     const int32_t* cu = d && d->num_seqs != d->B ? reinterpret_cast<const int32_t*>(p) : nullptr;
     return kda_fwd_check(p, p, p, p, p, cu, p, p, p, d) == KDA_OK && d->H <= (1 << 16) &&
-           (long long)d->num_seqs * d->H <= (1 << 22) && max_slots(d) * d->H <= (1LL << 23);
+           (long long)d->num_seqs * d->H <= (1 << 20) && max_slots(d) * d->H <= (1LL << 22);
 }
 
 kda_status_t run(bool scalar_gate, const void* q, const void* k, const void* v, const float* g, const float* beta,
