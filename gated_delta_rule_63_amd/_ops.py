@@ -9,10 +9,19 @@ from typing import Optional, Tuple
 
 import torch
 
-from . import D, _check_inputs, _check_out, _check_state, _desc, _ptr
+from . import D, _check_inputs, _check_out, _check_state, _desc
 from ._lib import ACTIVATIONS, KDA_BF16, KDA_F32, Desc, KDAError, lib
 
 _Tensor = Optional[torch.Tensor]
+_DTYPES = {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}
+
+
+def _ptr(t: _Tensor) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _f32(t: torch.Tensor) -> torch.Tensor:
+    return torch.empty_like(t, dtype=torch.float32)   # 1.2 us; torch.empty with shape and device 3.0
 
 
 class _Here:
@@ -99,11 +108,11 @@ def _bwd(entry, q, k, v, g, beta, do, cu_seqlens, initial_state, d_final_state, 
     with _on(q.device, stream) as s:
         if workspace is None:
             need = int(lib().kda_bwd_workspace_size(ctypes.byref(d)))
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+            workspace = q.new_empty(need, dtype=torch.uint8)
         d.workspace = workspace.data_ptr()
         d.workspace_bytes = workspace.numel() * workspace.element_size()
         outs = [torch.empty_like(x) for x in (q, k, v, g, beta)]
-        dh0 = torch.empty(sshape, dtype=torch.float32, device=q.device)
+        dh0 = q.new_empty(sshape, dtype=torch.float32)
         _call(entry, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(initial_state), _ptr(do),
               _ptr(d_final_state), *map(_ptr, outs), _ptr(dh0), ctypes.byref(d), s)
     return (*outs, dh0)
@@ -152,7 +161,7 @@ def _check_recurrent(q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, 
 def _recurrent(entry, q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, stream):
     d = _check_recurrent(q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, entry == "kda_gdn_recurrent")
     with _on(q.device, stream) as s:
-        o = out if out is not None else torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        o = out if out is not None else _f32(q)
         _call(entry, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(slots), _ptr(out_slots),
               _ptr(pool), pool.shape[0], KDA_BF16 if pool.dtype == torch.bfloat16 else KDA_F32, _ptr(o),
               ctypes.byref(d), s)
@@ -179,26 +188,28 @@ def gdn_block_in(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Ten
     return _block_in("kda_gdn_block_in", q, k, f, b, A_log, dt_bias, lower_bound, eps, stream)
 
 
-def _rows(name, t, shape, dtype, like, _device=True):
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or t.device != like.device \
-            or (_device and not t.is_cuda):
+def _rows(name, t, shape, dtype, device, _device=True):
+    if (t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != device
+            or (_device and device.type != "cuda")):
         raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} device tensor on the first argument's device")
 
 
 def _rows_desc(x):
     B, T, H, K = x.shape
-    return Desc(B, T, H, K, K, B, {torch.bfloat16: KDA_BF16, torch.float32: KDA_F32}.get(x.dtype, -1), KDA_F32, None, 0)
+    return Desc(B, T, H, K, K, B, _DTYPES.get(x.dtype, -1), KDA_F32, None, 0)
 
 
 def _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar_gate, _device=True):
-    if q.dim() != 4 or q.dtype not in (torch.bfloat16, torch.float32):
+    if q.dim() != 4 or q.dtype not in _DTYPES:
         raise ValueError("q must be a bfloat16 or float32 [B, T, H, 128] tensor")
-    gate = q.shape[:3] if scalar_gate else q.shape
-    for name, t, shape in (("q", q, q.shape), ("k", k, q.shape), ("f", f, gate), ("b", b, q.shape[:3])):
-        _rows(name, t, shape, q.dtype, q, _device)
-    _rows("A_log", A_log, q.shape[2:3], torch.float32, q, _device)
+    rows, dtype, device = q.shape, q.dtype, q.device
+    heads = rows[:3]
+    gate = heads if scalar_gate else rows
+    for name, t, shape in (("q", q, rows), ("k", k, rows), ("f", f, gate), ("b", b, heads)):
+        _rows(name, t, shape, dtype, device, _device)
+    _rows("A_log", A_log, rows[2:3], torch.float32, device, _device)
     if dt_bias is not None:
-        _rows("dt_bias", dt_bias, gate[2:], torch.float32, q, _device)
+        _rows("dt_bias", dt_bias, gate[2:], torch.float32, device, _device)
     if lower_bound is not None and not ctypes.c_float(lower_bound).value < 0:
         raise ValueError("lower_bound must be negative (None: no bound)")
 
@@ -207,8 +218,7 @@ def _block_in(entry, q, k, f, b, A_log, dt_bias, lower_bound, eps, stream):
     scalar = entry == "kda_gdn_block_in"
     _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar)
     with _on(q.device, stream) as s:
-        outs = [torch.empty_like(q), torch.empty_like(k), torch.empty(f.shape, dtype=torch.float32, device=q.device),
-                torch.empty(b.shape, dtype=torch.float32, device=q.device)]
+        outs = [torch.empty_like(q), torch.empty_like(k), _f32(f), _f32(b)]
         _call(entry, _ptr(q), _ptr(k), _ptr(f), _ptr(b), _ptr(A_log), _ptr(dt_bias), lower_bound or 0.0, eps,
               *map(_ptr, outs), ctypes.byref(_rows_desc(q)), s)
     return tuple(outs)
@@ -237,7 +247,7 @@ def _check_block_in_bwd(q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bou
     _check_block_in(q, k, f, b, A_log, dt_bias, lower_bound, scalar_gate, _device)
     for name, t, like, dtype in (("dq", dq, q, q.dtype), ("dk", dk, q, q.dtype), ("dg", dg, f, torch.float32),
                                  ("dbeta", dbeta, b, torch.float32)):
-        _rows(name, t, like.shape, dtype, q, _device)
+        _rows(name, t, like.shape, dtype, q.device, _device)
 
 
 def _block_in_bwd(entry, q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps, stream):
@@ -245,7 +255,7 @@ def _block_in_bwd(entry, q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bo
     _check_block_in_bwd(q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, scalar)
     d = _rows_desc(q)
     with _on(q.device, stream) as s:
-        ws = torch.empty(int(lib().kda_block_in_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty(int(lib().kda_block_in_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8)
         d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
         outs = [torch.empty_like(x) for x in (q, k, f, b, A_log)]
         dbias = torch.empty_like(dt_bias) if dt_bias is not None else None
@@ -270,15 +280,15 @@ def block_out(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, activation
 
 
 def _check_block_out(o, z, weight, activation, dy=None, _device=True):
-    if z.dim() != 4 or z.dtype not in (torch.bfloat16, torch.float32):
+    if z.dim() != 4 or z.dtype not in _DTYPES:
         raise ValueError("z must be a bfloat16 or float32 [B, T, H, 128] tensor")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    _rows("z", z, z.shape, z.dtype, z, _device)
-    _rows("o", o, z.shape, torch.float32, z, _device)
-    _rows("weight", weight, (D,), torch.float32, z, _device)
+    _rows("z", z, z.shape, z.dtype, z.device, _device)
+    _rows("o", o, z.shape, torch.float32, z.device, _device)
+    _rows("weight", weight, (D,), torch.float32, z.device, _device)
     if dy is not None:
-        _rows("dy", dy, z.shape, z.dtype, z, _device)
+        _rows("dy", dy, z.shape, z.dtype, z.device, _device)
 
 
 def block_out_bwd(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
@@ -288,7 +298,7 @@ def block_out_bwd(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, dy: to
     _check_block_out(o, z, weight, activation, dy)
     d = _rows_desc(z)
     with _on(z.device, stream) as s:
-        ws = torch.empty(int(lib().kda_block_out_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8, device=z.device)
+        ws = z.new_empty(int(lib().kda_block_out_bwd_workspace_size(ctypes.byref(d))), dtype=torch.uint8)
         d.workspace, d.workspace_bytes = ws.data_ptr(), ws.numel()
         do, dz, dw = torch.empty_like(o), torch.empty_like(z), torch.empty_like(weight)
         _call("kda_block_out_bwd", _ptr(o), _ptr(z), _ptr(weight), eps, ACTIVATIONS[activation], _ptr(dy), _ptr(do),
