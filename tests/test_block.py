@@ -215,6 +215,31 @@ def test_no_tokens(gpu):
 
 
 @pytest.mark.gpu
+def test_far_rows(gpu):
+    """Rows whose elements lie beyond 2^31 are those of a call on them alone."""
+    import gated_delta_rule_63_amd as kda
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    T, H, m = 140000, 120, 7
+    assert T * H * 128 > 2 ** 31
+    def tail(dtype, *s):
+        x = torch.zeros(1, T, *s, dtype=dtype, device="cuda")
+        x[:, -m:] = torch.randn(1, m, *s, generator=gen, device="cuda").to(dtype)
+        return x
+    q, f, b, g, db = (tail(torch.bfloat16, H, 128), tail(torch.bfloat16, H, 128), tail(torch.bfloat16, H),
+                      tail(torch.float32, H, 128), tail(torch.float32, H))
+    A, w = torch.rand(H, generator=gen, device="cuda"), torch.rand(128, generator=gen, device="cuda")
+    last = lambda x: x[:, -m:].contiguous()
+    for fn, args, rest in ((kda.block_in, (q, q, f, b), (A,)), (kda.block_out, (g, q), (w,)),
+                           (lambda *x: kda.block_in_bwd(*x[:4], A, *x[4:])[:4], (q, f, f, b, f, q, g, db), ()),
+                           (lambda *x: kda.block_out_bwd(*x[:2], w, x[2])[:2], (g, q, f), ())):
+        got, want = fn(*args, *rest), fn(*map(last, args), *rest)
+        if torch.is_tensor(got):
+            got, want = [got], [want]
+        assert all(torch.equal(x[:, -m:], y) for x, y in zip(got, want))
+        del got, want
+
+
+@pytest.mark.gpu
 def test_in_place(gpu):
     """What include/kda.h allows to share memory does."""
     import gated_delta_rule_63_amd as kda

@@ -292,6 +292,34 @@ def test_bwd_leaves_other_rows(torch_gpu):
 
 
 @pytest.mark.gpu
+def test_bwd_far_elements(torch_gpu):
+    """Elements of the tensors and of the workspace beyond 2^31: the last heads of a
+    long, wide call are those of a call on them alone."""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    T, H, m = 140000, 121, 40          # m alone: still 32 columns of V a workgroup
+    assert T * H * 128 > 2 ** 31
+    if torch.cuda.get_device_properties(0).total_memory < 230 << 30:
+        pytest.skip("needs 170 GB of device memory")
+    torch.cuda.empty_cache()
+    gen = torch.Generator(device="cuda").manual_seed(2)
+
+    def wide(dtype, scale, *s):
+        x = torch.zeros(1, T, H, *s, dtype=dtype, device="cuda")
+        x[:, :, -m:] = (torch.randn(1, T, m, *s, generator=gen, device="cuda") * scale).to(dtype)
+        return x
+    k, v, do = wide(torch.bfloat16, 128 ** -0.5, 128), wide(torch.bfloat16, 1.0, 128), wide(torch.float32, 1.0, 128)
+    g, b = wide(torch.float32, 0.5, 128).abs_().neg_(), wide(torch.float32, 1.0).sigmoid_()
+    args = (v, k, v, g, b, do)
+    got = [x[:, :, -m:].clone() if x.dim() < 4 or x.shape[1] == T else x[:, -m:].clone() for x in kda.bwd(*args)]
+    args = [x[:, :, -m:].contiguous() for x in args]
+    want = kda.bwd(*args)
+    assert all(bool(torch.isfinite(x).all()) and torch.equal(x, y) for x, y in zip(got, want))
+    del k, v, do, g, b, args, got, want
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.gpu
 def test_bwd_without_tokens(torch_gpu):
     """T = 0: empty gradients, and the state's passes through."""
     torch = torch_gpu

@@ -95,11 +95,16 @@ def make(torch, B, T, H, dtype, scalar, P, pool_dtype, seed):
 CASES = [  # lengths (None: rows of T), T, B, H, inputs, gate, pool, out_slots
     (None, 1, 1, 1, "float32", False, "float32", False),
     (None, 1, 7, 3, "bfloat16", False, "bfloat16", False),
-    (None, 1, 33, 9, "float32", True, "bfloat16", False),       # above 256 (sequence, head) pairs: four waves a head
+    (None, 1, 33, 9, "float32", True, "bfloat16", False),
     (None, 4, 40, 7, "bfloat16", False, "float32", True),
     (None, 17, 2, 5, "bfloat16", True, "float32", True),
     ((0, 3, 1, 0, 70, 5), 79, 6, 2, "float32", False, "float32", False),
     ((1, 0, 8, 2), 11, 4, 3, "bfloat16", False, "bfloat16", True),
+    # above 1.5 (sequence, head) pairs a compute unit: four waves a head
+    (None, 1, 45, 9, "float32", True, "bfloat16", False),
+    (None, 4, 56, 7, "bfloat16", False, "float32", True),
+    ((0, 3, 1, 0, 7, 5), 16, 6, 66, "bfloat16", True, "float32", False),
+    ((2, 9, 0, 1), 12, 4, 97, "float32", False, "bfloat16", True),
 ]
 
 
