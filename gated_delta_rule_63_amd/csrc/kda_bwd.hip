@@ -16,8 +16,12 @@
 //   dk = row + col,  row = -e^G (r S^T) + sum_s dB_ts k_s e^(G_t - G_s)
 //   col_s = sum_t (dM_ts q_t + dB_ts k_t) e^(G_t - G_s) + carry_s,
 //   carry_s = e^(G_last - G_s) (b_s e_s dS'^T)
-//   dG = q dq + k (row - col),  dg_t = sum_(u >= t) dG_u + sum_s k_s carry_s
-//        + rowsum(e^G_last S dS')
+//   dG = q dq + k (row - (col - carry)),
+//   dg_t = sum_(u >= t) dG_u + sum_(s < t) k_s carry_s + rowsum(e^G_last S dS')
+// A gate at t acts on what passes from tokens before t to tokens from t on. What
+// does not pass through it is left out of its sum rather than added and taken
+// away again: dM's diagonal (its terms of dq, dM_tt k_t, and of col, dM_tt q_t,
+// are equal in dG), and carry from t on.
 // The form with X divides by no beta, so beta = 0 is an ordinary value.
 //
 // Three kernels. Only the two state walks are sequential, and both split over
@@ -755,7 +759,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
     const long long ch = (long long)h * a.nslots + slot;
     // first do, rho, e as [token][v]; then E1, k, q as [token][k]
     __shared__ __align__(16) float R0[C * LD], R1[C * LD], R2[C * LD];
-    __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM];
+    __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM], dMd[C];   // dM below its diagonal; the diagonal
     __shared__ __align__(16) float up[2][D], dn[2][D], cs[D], dec[D], bs[C], part[8][C];
     constexpr int NT = kGradThreads;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
@@ -808,7 +812,8 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         for (int j = 0; j < 4; ++j) {
             const int t = ro + g4 + j;
             if (i < 3) {
-                dMs[t * LM + s] = t >= s ? bs[s] * x[j] : 0.f;
+                dMs[t * LM + s] = t > s ? bs[s] * x[j] : 0.f;
+                if (t == s) dMd[t] = bs[t] * x[j];
             } else {
                 dBs[t * LM + s] = t > s ? -bs[t] * bs[s] * x[j] : 0.f;
                 if (t == s && t < ck.nv) a.dbeta[(ck.tok + t) * a.H + h] = x[j];
@@ -908,30 +913,33 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
             cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x;
             cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
         }
-        cl[0] = mma(col_of(dBs, 0, 0), ks[0] * E[0], mma(col_of(dMs, 0, 0), qv[0] * E[0], cross));
-        // What passes the end of each sub-block: end[1] as in the formula at the
-        // top; end[0] is the sum of sub-block 1's dG and end[1] without the pairs
-        // within sub-block 1, which cancel in it. (Summed with them, dg's error
-        // is 1.4 times this.)
+        cl[0] = mma(col_of(dBs, 0, 0), ks[0] * E[0], mma(col_of(dMs, 0, 0), qv[0] * E[0], z));
+        // dg of a token t, in three parts. dG: what tokens of the same sub-block leave
+        // for its sum over u >= t, without dM's diagonal. ahead: what passes from one
+        // token to the next sub-block or the next chunk, for its sum over s < t. end:
+        // what reaches t from the other sub-block and the states. (With the diagonal
+        // and with carry from t on in the sums, dg's error at g = -5 everywhere was 4e-5
+        // of its RMS: what equal terms leave when rounded does not shrink with e^g.)
         float end[2] = {0.f, 0.f};
+        f32x4 ahead[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const f32x4 bb = ld4(bs + 16 * i + g4), u = splat(up[i][col]);
-            const f32x4 E1 = E[i], E2 = inverse(E1), kk = ks[i], qq = qv[i];
+            const f32x4 bb = ld4(bs + 16 * i + g4), u = splat(up[i][col]), dd = ld4(dMd + 16 * i + g4);
+            // k and q read again: held from above, a register goes to scratch
+            const f32x4 E1 = E[i], E2 = inverse(E1), kk = at(R1, i), qq = at(R2, i);
             const f32x4 qs = u * qS[i], rs = u * (bb * rS[i]);
             const f32x4 q_ = E1 * (dq[i] + qs);
-            const f32x4 r_ = E1 * (row[i] - rs);
-            const f32x4 cy = E2 * splat(dn[i][col]) * (bb * eS[i]);
-            const f32x4 c_ = E2 * cl[i] + cy;
+            const f32x4 r_ = E1 * (row[i] - rs), c_ = E2 * cl[i];
+            const f32x4 cy = E2 * splat(dn[i][col]) * (bb * eS[i]), on = i ? cy : E2 * cross + cy;
             dG[i] = qq * q_ + kk * (r_ - c_);
+            ahead[i] = kk * on;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                end[1] += kk[j] * cy[j];
                 if (i) end[0] += E1[j] * (qq[j] * qs[j] - kk[j] * rs[j]);
-                else end[0] += kk[j] * (E2[j] * cross[j] + cy[j]);
+                else end[1] += kk[j] * cy[j];
                 const int o = (16 * i + g4 + j) * LD + col;   // k and q of this place have been read
-                R1[o] = r_[j] + c_[j];
-                R2[o] = q_[j];
+                R1[o] = (r_[j] + (c_[j] + on[j])) + dd[j] * qq[j];
+                R2[o] = q_[j] + dd[j] * kk[j];
             }
         }
 #pragma unroll
@@ -940,20 +948,20 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
             end[i] += __shfl_xor(end[i], 16);
             end[i] += __shfl_xor(end[i], 32);
         }
-        // dg: sum over the sub-block's tokens from t on
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             dG[i][2] += dG[i][3];
             dG[i][1] += dG[i][2];
             dG[i][0] += dG[i][1];
-            const float x0 = dG[i][0];
-            float later = 0.f;
+            const float p1 = ahead[i][0], p2 = p1 + ahead[i][1], p3 = p2 + ahead[i][2], p4 = p3 + ahead[i][3], x0 = dG[i][0];
+            float rest = 0.f;    // of dG from the lanes with later tokens, of ahead from those with earlier ones
 #pragma unroll
             for (int u = 1; u < 4; ++u) {
-                const float y = __shfl(x0, (l + 16 * u) & 63);
-                later += (l >> 4) + u < 4 ? y : 0.f;
+                const int from = (l + 16 * u) & 63;
+                const float y = __shfl(x0, from), x = __shfl(p4, from);
+                rest += from > l ? y : x;
             }
-            dG[i] += splat(later + end[i]);
+            dG[i] += splat(rest + end[i]) + f32x4{0.f, p1, p2, p3};
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {

@@ -354,3 +354,61 @@ def test_bwd_in_segments(torch_gpu):
     for name, w, u, v in zip("dq dk dv dg dbeta".split(), whole, a, b):
         within(torch.cat([u, v], 1).cpu().numpy(), w.cpu().numpy(), name, tol=2e-4)
     within(a[5].cpu().numpy(), whole[5].cpu().numpy(), "dh0", tol=2e-4)
+
+
+# ---- the fp32 gradients' own accuracy, measured on their own size
+
+def _rms_off(got, ref):
+    got, ref = np.asarray(got, np.float64), np.asarray(ref, np.float64)
+    assert got.shape == ref.shape and np.all(np.isfinite(got))
+    return W.rms(got - ref) / W.rms(ref)
+
+
+# RMS of the error over RMS of the result. A sum of 128 products rounds by 2^-24
+# sqrt(128) = 7e-7 of itself, ten in a row by 2.2e-6. A decay's exponent, up to 58 for
+# gates of -5, is a sum of up to eight gates, each partial sum rounded by at most
+# 2^-19 ln 2 = 1.3e-6, 0.8e-6 RMS: 2e-6 together. 3e-6 of both; a factor of 3 for the
+# terms of a sum over 16 tokens that exceed it.
+RMS_BAR = 1e-5
+
+
+def _check_rms(got, ref, what, bar=RMS_BAR):
+    for n, i in (("dg", 3), ("dbeta", 4), ("dh0", 5)):
+        off = _rms_off(got[i].cpu().numpy(), ref[i])
+        print(f"{what} {n}: rms {off:.2e}", flush=True)
+        assert off <= bar, f"{what} {n}: rms off by {off:.2e} (bar {bar:.0e})"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cfg,scalar", [
+    (W.variant("tiny_fp32", T=64, H=2, gate="floor", h0=True), False),
+    (W.variant("tiny_fp32", T=64, H=2, gate="floor"), False),
+    (W.variant("T8192_H96", T=131, H=3, gate="floor", seq_lens=(33, 2, 96), h0=True), False),
+    (W.variant("T8192_H96", T=70, H=40, gate="floor"), False),
+    (W.variant("tiny_fp32", T=64, H=2, gate="floor", h0=True), True),
+    (W.variant("T8192_H96", T=131, H=3, gate="floor", seq_lens=(33, 2, 96)), True),
+    (W.variant("tiny_fp32", T=100, H=2, h0=True), False),
+    (W.variant("tiny_fp32", T=100, H=2, gate="scalar", h0=True), True),
+    (W.variant("tiny_fp32", T=2500, H=1, gate="mild", h0=True), False),
+    (W.variant("tiny_fp32", T=700, H=1, gate="scalar_mild", h0=True), True),
+], ids=lambda c: getattr(c, "name", str(c)))
+def test_bwd_fp32_gradients(torch_gpu, cfg, scalar):
+    """dg, dbeta and dh0 on their own size, also where every gate is at its floor: dg
+    then is e^-5 of the products q dq and k dk that it is a difference of."""
+    inp = W.make_inputs(cfg, 12)
+    do, dh = _grads(inp, 13)
+    got = _run(torch_gpu, inp, do, dh, scalar=scalar)
+    ref = rule_bwd(inp.q, inp.k, inp.v, inp.g_scalar() if scalar else inp.g, inp.beta, do, inp.seq_bounds(), inp.h0, dh)
+    _check_rms(got, ref, cfg.name)
+    within(got[3].cpu().numpy(), ref[3], f"{cfg.name} dg")     # no element off by 1e-4 of the RMS
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scalar", [False, True])
+def test_bwd_gate_of_a_zero_state(torch_gpu, scalar):
+    """A token that starts from nothing has no gate gradient: exactly zero, and not what
+    is left of two equal terms."""
+    inp = W.make_inputs(W.variant("tiny_fp32", B=5, T=1, H=3, gate="scalar"), 14)
+    do, dh = _grads(inp, 15)
+    got = _run(torch_gpu, inp, do, dh, scalar=scalar)
+    assert bool(got[0].any()) and not bool(got[3].any())
