@@ -42,9 +42,12 @@
 //
 // Gates inside a chunk: two sub-blocks of 16 tokens, each with its decay E1
 // counted from behind its eighth token; E1 and 1 / E1 stay within e^+-40 for
-// g >= -5. A product within a sub-block pairs E1 with 1 / E1; from sub-block 0
-// to 1 the same factors are scaled by cs, the decay from the middle of the one
-// to the middle of the other, per channel.
+// g >= -5. A product within a sub-block pairs E1 with 1 / E1. From sub-block 0
+// to 1 the factor of 0 is scaled by c0, the decay from its middle to its end, and
+// the factor of 1 by c1, that from its start to its middle, per channel: c0 / E1
+// and c1 E1 are decays, at most 1, where c0 c1 alone would underflow for gates of
+// -5.46 and take those products along. 1 / E1 overflows (to NaN) where eight
+// gates sum to less than -87, at -10.9 each.
 #include "kda_bwd.h"
 #include "kda_device.h"
 
@@ -139,7 +142,7 @@ __device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(
 struct Gates {
     float L[16];             // sum of the gates from behind token 7 to t (negated for t < 7)
     float m0, t0, m1, t1;    // sums of tokens 0 .. 7 and 8 .. 15 of both sub-blocks
-    float up, dn, cs, total; // exponents: e^G = E1 2^up, e^(G_last - G) = 2^dn / E1, see cs above
+    float up, dn, total;     // exponents: e^G = E1 2^up, e^(G_last - G) = 2^dn / E1; c0 = 2^t0, c1 = 2^m1
 };
 
 // Rows of a [tokens, H, 128] tensor, one chunk of them: 16 bytes a lane and
@@ -245,7 +248,6 @@ __device__ __forceinline__ void scan_gates(Gates& s, float (&g)[16], int half) {
     s.t1 = half ? t : to;
     s.up = half ? (s.m0 + s.t0) + s.m1 : s.m0;
     s.dn = half ? s.t1 : s.t0 + (s.m1 + s.t1);
-    s.cs = s.m1 + s.t0;
     s.total = (s.m0 + s.t0) + (s.m1 + s.t1);
 }
 
@@ -264,7 +266,10 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
     float *const Bs = KQ + 4 * 6 * 256, *const Ms = Bs + C * LM;
     float* const Xs = KQ;               // when the parts have been summed
     static_assert(4 * 6 * 256 + 2 * C * LM <= 2 * C * LD, "B and M lie behind the parts");
-    __shared__ __align__(16) float cs[D], sc[2][D], sc2[2][D], bs[C], gs[C];
+    __shared__ __align__(16) float c0[D], sc[2][D], sc2[2][D], bs[C], gs[C];
+    // c1 has its place behind the rows of Kd: 512 bytes more would leave two workgroups
+    const auto c1 = [&](int c) { return Kd + (c >> 2) * LD + D + (c & 3); };
+    static_assert(LD >= D + 4 && 4 * C >= D, "four floats behind each row");
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     // everything from memory at once: the latency of one fetch, not of three
     Rows<F32, 256> rk, rq;
@@ -293,7 +298,8 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         sc[half][c] = exp2_(s.up);
         sc2[half][c] = exp2_(s.dn);
         if (half == 0) {
-            cs[c] = exp2_(s.cs);
+            c0[c] = exp2_(s.t0);
+            *c1(c) = exp2_(s.m1);
             a.decay[ch * D + c] = exp2_(s.total);
         }
 #pragma unroll
@@ -331,13 +337,13 @@ __global__ __launch_bounds__(256) void kda_bwd_intra(BwdArgs a) {
         const f32x4 kd0 = ld4(Kd + r16 * LD + c), kd1 = ld4(Kd + (16 + r16) * LD + c);
         const f32x4 qd0 = ld4(Qd + r16 * LD + c), qd1 = ld4(Qd + (16 + r16) * LD + c);
         const f32x4 ki0 = ld4(Ki + r16 * LD + c), ki1 = ld4(Ki + (16 + r16) * LD + c);
-        const f32x4 x = ld4(cs + c);
+        const f32x4 x1 = ld4(c1(c)), end0 = ki0 * ld4(c0 + c);
         pb[0] = mma(kd0, ki0, pb[0]);
         pb[1] = mma(kd1, ki1, pb[1]);
-        pb[2] = mma(kd1 * x, ki0, pb[2]);
+        pb[2] = mma(kd1 * x1, end0, pb[2]);
         pm[0] = mma(qd0, ki0, pm[0]);
         pm[1] = mma(qd1, ki1, pm[1]);
-        pm[2] = mma(qd1 * x, ki0, pm[2]);
+        pm[2] = mma(qd1 * x1, end0, pm[2]);
     }
     lds_barrier();         // the partial tiles take the place of Ki and Qd
 #pragma unroll
@@ -760,7 +766,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
     // first do, rho, e as [token][v]; then E1, k, q as [token][k]
     __shared__ __align__(16) float R0[C * LD], R1[C * LD], R2[C * LD];
     __shared__ __align__(16) float Xs[C * LM], dMs[C * LM], dBs[C * LM], dMd[C];   // dM below its diagonal; the diagonal
-    __shared__ __align__(16) float up[2][D], dn[2][D], cs[D], dec[D], bs[C], part[8][C];
+    __shared__ __align__(16) float up[2][D], dn[2][D], c0[D], c1[D], dec[D], bs[C], part[8][C];
     constexpr int NT = kGradThreads;
     const int tid = threadIdx.x, w = tid >> 6, l = tid & 63, r16 = l & 15, g4 = 4 * (l >> 4);
     if (tid < C) bs[tid] = a.b[ch * C + tid];
@@ -869,7 +875,8 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
         up[half][c] = exp2_(s.up);
         dn[half][c] = exp2_(s.dn);
         if (half == 0) {
-            cs[c] = exp2_(s.cs);
+            c0[c] = exp2_(s.t0);
+            c1[c] = exp2_(s.m1);
             dec[c] = exp2_(s.total);
         }
 #pragma unroll
@@ -898,19 +905,19 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
             for (int u = 0; u < 4; ++u) r[u] = __builtin_amdgcn_rcpf(y[u]);   // to 1 ulp
             return r;
         };
-        const f32x4 z = splat(0.f), x = splat(cs[col]);
-        f32x4 dq[2], row[2], cl[2], cross;   // cross: from sub-block 1 to 0
+        const f32x4 z = splat(0.f), x0 = splat(c0[col]), x1 = splat(c1[col]);
+        f32x4 dq[2], row[2], cl[2], cross;   // cross: from sub-block 1 to 0, its own factor x0 / E1 apart
         const f32x4 E[2] = {at(R0, 0), at(R0, 1)}, ks[2] = {at(R1, 0), at(R1, 1)}, qv[2] = {at(R2, 0), at(R2, 1)};
         {
             const f32x4 ki0 = ks[0] * inverse(E[0]), ki1 = ks[1] * inverse(E[1]);
             dq[0] = mma(row_of(dMs, 0, 0), ki0, z);
-            dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0, z) * x);
+            dq[1] = mma(row_of(dMs, 1, 1), ki1, mma(row_of(dMs, 1, 0), ki0 * x0, z) * x1);
             row[0] = mma(row_of(dBs, 0, 0), ki0, z);
-            row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0, z) * x);
+            row[1] = mma(row_of(dBs, 1, 1), ki1, mma(row_of(dBs, 1, 0), ki0 * x0, z) * x1);
         }
         {
             const f32x4 kd1 = ks[1] * E[1], qd1 = qv[1] * E[1];
-            cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x;
+            cross = mma(col_of(dBs, 1, 0), kd1, mma(col_of(dMs, 1, 0), qd1, z)) * x1;
             cl[1] = mma(col_of(dBs, 1, 1), kd1, mma(col_of(dMs, 1, 1), qd1, z));
         }
         cl[0] = mma(col_of(dBs, 0, 0), ks[0] * E[0], mma(col_of(dMs, 0, 0), qv[0] * E[0], z));
@@ -930,7 +937,7 @@ __global__ __launch_bounds__(kGradThreads, 4) void kda_bwd_grads(BwdArgs a) {
             const f32x4 qs = u * qS[i], rs = u * (bb * rS[i]);
             const f32x4 q_ = E1 * (dq[i] + qs);
             const f32x4 r_ = E1 * (row[i] - rs), c_ = E2 * cl[i];
-            const f32x4 cy = E2 * splat(dn[i][col]) * (bb * eS[i]), on = i ? cy : E2 * cross + cy;
+            const f32x4 cy = E2 * splat(dn[i][col]) * (bb * eS[i]), on = i ? cy : E2 * x0 * cross + cy;
             dG[i] = qq * q_ + kk * (r_ - c_);
             ahead[i] = kk * on;
 #pragma unroll

@@ -346,8 +346,11 @@ kda_status_t kda_fwd_staged(const void* q, const void* k, const void* v, const f
  * [-5, 0], beta in [0, 1] and L2-normalised keys the error of dg, dbeta and dh0
  * has an RMS of 2e-7 to 7e-7 of the result's (measured, gates of -5 everywhere
  * and the scalar gate included; held to 1e-5), and no element is off by 1e-4 of
- * that RMS; dq, dk, dv are accurate to their type's rounding. Results do not
- * depend on the order of execution (no atomics).
+ * that RMS; dq, dk, dv are accurate to their type's rounding. Gates may be
+ * stronger than kda_fwd takes them: -8 throughout (1e-6 to 2e-6 there, held to
+ * 2e-5), and more where only a few are; once eight tokens in a row have gates of a
+ * channel that sum to less than -87 (-10.9 each), the gradient may be NaN.
+ * Results do not depend on the order of execution (no atomics).
  * No output may overlap an input, except dh0 == dhT. Other errors as kda_fwd. */
 kda_status_t kda_bwd(const void* q, const void* k, const void* v, const float* g, const float* beta,
                      const int32_t* cu_seqlens, const float* h0, const float* d_o, const float* dhT,

@@ -412,3 +412,26 @@ def test_bwd_gate_of_a_zero_state(torch_gpu, scalar):
     do, dh = _grads(inp, 15)
     got = _run(torch_gpu, inp, do, dh, scalar=scalar)
     assert bool(got[0].any()) and not bool(got[3].any())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scalar", [False, True])
+@pytest.mark.parametrize("low,high", [(-5.5, -5.5), (-6.0, -6.0), (-8.0, -8.0), (-8.0, 0.0), (-16.0, 0.0)])
+def test_bwd_stronger_gates(torch_gpu, scalar, low, high):
+    """Gates below kda_fwd's range: down to -8 throughout, and lower where they are rare
+    (-16 among gates of -0.1, one token in eight).
+    Exponents reach 92, whose partial sums round by 2^-18 ln 2 = 2.6e-6 instead of 1.3e-6:
+    twice RMS_BAR and, for single elements of dg, twice the bar of 1e-4."""
+    inp = W.make_inputs(W.variant("tiny_fp32", T=101, H=2, gate="scalar" if scalar else "bj", h0=True), 16)
+    rng = np.random.default_rng(17)
+    g = rng.uniform(low, high, inp.g.shape).astype(np.float32)
+    if low == -16.0:
+        g = np.where(np.arange(101)[:, None, None] % 8 == 5, np.float32(-16.0), np.float32(-0.1)) * np.ones_like(g)
+    inp.g[:] = g[..., :1] if scalar else g
+    do, dh = _grads(inp, 18)
+    got = _run(torch_gpu, inp, do, dh, scalar=scalar)
+    ref = rule_bwd(inp.q, inp.k, inp.v, inp.g_scalar() if scalar else inp.g, inp.beta, do, inp.seq_bounds(), inp.h0, dh)
+    for n, x, r in zip("dq dk dv".split(), got, ref):
+        within(x.cpu().numpy(), r, n)
+    _check_rms(got, ref, f"[{low}, {high}]", 2 * RMS_BAR)
+    within(got[3].cpu().numpy(), ref[3], "dg", tol=2e-4)
