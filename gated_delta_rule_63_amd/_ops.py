@@ -79,7 +79,10 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta
     d_initial_state): dq, dk, dv in q's dtype, the others fp32. Rows of tokens that
     belong to no sequence (cu_seqlens) are unset, as fwd()'s are: hand the first cu[N]
     tokens alone to block_out() and to the gradients of the block operators, whose sums
-    take every row. Nothing is kept from the forward; states are recomputed. workspace: an optional uint8 device tensor of
+    take every row. Nothing is kept from the forward; states are recomputed.
+    Gates may go down to -8; where eight tokens in a row have gates that sum to less
+    than -87 the gradient may be NaN, without an error (fwd() ends earlier, at about
+    -5.4 over 16 tokens). workspace: an optional uint8 device tensor of
     bwd_workspace_size() bytes, used by one call at a time; allocated otherwise."""
     return _bwd("kda_bwd", q, k, v, g, beta, do, cu_seqlens, initial_state, d_final_state, stream, workspace)
 
@@ -87,7 +90,8 @@ def bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta
 def gdn_bwd(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, do: torch.Tensor,
             cu_seqlens: _Tensor = None, initial_state: _Tensor = None, d_final_state: _Tensor = None,
             stream: Optional[torch.cuda.Stream] = None, workspace: _Tensor = None) -> Tuple[torch.Tensor, ...]:
-    """Gradient of gdn_fwd(): as bwd(), with g and dg [B, T, H]."""
+    """Gradient of gdn_fwd(): as bwd(), with g and dg [B, T, H], and with its limit on
+    the gates."""
     return _bwd("kda_gdn_bwd", q, k, v, g, beta, do, cu_seqlens, initial_state, d_final_state, stream, workspace)
 
 
@@ -177,14 +181,19 @@ def block_in(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor,
     gate g from f, and beta = sigmoid(b). With x = f + dt_bias,
     g = -exp(A_log) softplus(x), or with a lower bound (< 0) lower_bound *
     sigmoid(exp(A_log) x). q, k, f [B, T, H, 128] and b [B, T, H] share a dtype (bf16
-    or fp32); A_log [H], dt_bias [H, 128] fp32. Returns (q, k, g, beta)."""
+    or fp32); A_log [H], dt_bias [H, 128] fp32. Returns (q, k, g, beta).
+    lower_bound=-5.0 keeps g where fwd() and bwd() are defined. Without a bound nothing
+    does: gates of about -5.4 or less over 16 tokens turn fwd()'s results into inf or
+    NaN, and -10.9 over eight bwd()'s, without an error (exp(A_log) = 16 and a raw gate
+    of 0 give -11). recurrent() takes any gate."""
     return _block_in("kda_block_in", q, k, f, b, A_log, dt_bias, lower_bound, eps, stream)
 
 
 def gdn_block_in(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Tensor, A_log: torch.Tensor,
                  dt_bias: _Tensor = None, lower_bound: Optional[float] = None, eps: float = 1e-6,
                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
-    """block_in() for gdn_fwd(): f [B, T, H], dt_bias [H], g [B, T, H]."""
+    """block_in() for gdn_fwd(): f [B, T, H], dt_bias [H], g [B, T, H]. The same holds of
+    its gate without a bound."""
     return _block_in("kda_gdn_block_in", q, k, f, b, A_log, dt_bias, lower_bound, eps, stream)
 
 

@@ -413,7 +413,11 @@ kda_status_t kda_gdn_recurrent(const void* q, const void* k, const void* v, cons
  *     q_out = q / sqrt(|q|^2 + eps),  k_out alike,  beta = sigmoid(b)
  *     x = f + dt_bias,  g = -exp(A_log) softplus(x)          lower_bound == 0
  *                       g = lower_bound sigmoid(exp(A_log) x)   lower_bound < 0
- * so that a lower bound of -5 keeps g in the domain of kda_fwd.
+ * so that a lower bound of -5 keeps g in the domain of kda_fwd and kda_bwd.
+ * Without a bound g has no floor: exp(A_log) = 16 and softplus(x) = 0.7 give
+ * -11, and where such gates last, kda_fwd (16 tokens that sum to less than about
+ * -86) and kda_bwd (eight that sum to less than -87) overflow to inf and NaN.
+ * Nothing here checks that; kda_recurrent takes any gate.
  *     q, k, q_out, k_out [B, T, H, 128] in_dtype
  *     f        [B, T, H, 128] in_dtype (kda_gdn_block_in: [B, T, H])
  *     b        [B, T, H] in_dtype

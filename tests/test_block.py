@@ -352,3 +352,37 @@ def test_whole_block(gpu, scalar, dtype):
     for name, x, r in [("y", y, r_y), ("dz", dz, r_dz), ("dw", dw, r_dw), ("dv", d[2], r_d[2]),
                        *zip("dq dk df db dA dbias".split(), got, r_got)]:
         within(np_(x), r.detach().numpy(), "whole " + name, tol=4e-4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scalar", [False, True])
+def test_default_gate_into_the_rule(gpu, scalar):
+    """The gate without a bound goes below -5 where raw gates are large, and the rule takes
+    that as long as such gates are rare (16 tokens sum to more than -80): forwards and
+    back, each step to its own bar at the inputs the step before it left."""
+    import gated_delta_rule_63_amd as kda
+    B, T, H = 1, 90, 2
+    gen = torch.Generator().manual_seed(21)
+    n = lambda *s: torch.randn(*s, generator=gen)
+    gate = (B, T, H) if scalar else (B, T, H, 128)
+    f, b = n(*gate), n(B, T, H)
+    f[:, 5::12] += 2.5
+    q, k, v, do = (n(B, T, H, 128) for _ in range(4))
+    c = lambda x: x.cuda()
+    pre = "gdn_" if scalar else ""
+    q1, k1, g, beta = getattr(kda, pre + "block_in")(c(q), c(k), c(f), c(b), c(torch.full((H,), 1.0)))
+    lows = g.unfold(1, 16, 1).sum(-1).min().item()
+    assert g.min().item() < -6.0 and lows > -80.0, (g.min().item(), lows)
+    o, hT = getattr(kda, pre + "fwd")(q1, k1, c(v), g, beta)
+    d = getattr(kda, pre + "bwd")(q1, k1, c(v), g, beta, c(do))
+    x = [t.cpu().double().numpy() for t in (q1, k1, c(v), g, beta)]
+    S, ref_o = np.zeros((H, 128, 128)), []
+    for t in range(T):
+        S = np.exp(x[3][0, t])[..., None, None] * S if scalar else np.exp(x[3][0, t])[..., None] * S
+        e = x[2][0, t] - np.einsum("hk,hkv->hv", x[1][0, t], S)
+        S = S + np.einsum("hk,hv->hkv", x[1][0, t], x[4][0, t][:, None] * e)
+        ref_o.append(np.einsum("hk,hkv->hv", x[0][0, t], S))
+    within(o[0].cpu().numpy(), np.stack(ref_o), "o")
+    within(hT[0].cpu().numpy(), S, "hT")
+    for name, u, r in zip("dq dk dv dg dbeta dh0".split(), d, rule_bwd(*x, do.double().numpy(), [(0, 0, T)])):
+        within(u.cpu().numpy(), r, name)
