@@ -142,7 +142,9 @@ def recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor
 def gdn_recurrent(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor,
                   pool: torch.Tensor, slots: _Tensor = None, out_slots: _Tensor = None, cu_seqlens: _Tensor = None,
                   out: _Tensor = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
-    """recurrent() with one gate per (token, head): g [B, T, H]."""
+    """recurrent() with one gate per (token, head): g [B, T, H]. As q, k, v, pool and out, it
+    has to start on a multiple of 16 bytes (a slice of tokens of one sequence with an odd
+    number of heads may not: clone() it)."""
     return _recurrent("kda_gdn_recurrent", q, k, v, g, beta, pool, slots, out_slots, cu_seqlens, out, stream)
 
 

@@ -389,8 +389,8 @@ size_t kda_bwd_workspace_size(const kda_desc_t* desc);
  * sequence, nor for two tokens of one (its contents would be undefined; no
  * access leaves the pool; num_slots == 0: every place is empty). A zero-length sequence changes nothing. The state is
  * fp32 within the call; a bf16 pool is rounded when a state is written.
- * q, k, v, pool, o and, per channel, g must be 16-byte aligned
- * (KDA_ERR_UNSUPPORTED). num_slots < N without slots, or more than 2^23
+ * q, k, v, g, pool and o must be 16-byte aligned (KDA_ERR_UNSUPPORTED), g also
+ * with one gate per (token, head). num_slots < N without slots, or more than 2^23
  * (sequence, head) pairs, is KDA_ERR_SHAPE; other errors as kda_fwd.
  * desc->workspace is ignored. Time grows with the tokens of a sequence: for
  * whole prompts use kda_fwd. */

@@ -222,3 +222,25 @@ def test_draft_and_accept(torch_gpu):
     ref = list(steps(np.zeros((3, 128, 128)), *(x[n][0].double().numpy() for n in ("q", "k", "v", "g", "beta"))))
     within(o[0].cpu().numpy(), np.stack([y for y, _ in ref[52:]]), "o", tol=2e-4)
     within(pool[1].cpu().numpy(), ref[-1][1], "state", tol=2e-4)
+
+
+@pytest.mark.gpu
+def test_scalar_gate_of_a_slice(torch_gpu):
+    """A slice of tokens whose gates do not start on 16 bytes is refused, before anything
+    runs, and its clone is taken."""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    x, pool, _ = make(torch, 1, 6, 3, torch.float32, True, 1, torch.float32, 9)
+    part = [x[n].cuda()[:, 1:4] for n in ("q", "k", "v", "g", "beta")]
+    p, start = pool.cuda(), pool.cuda()
+    assert part[3].is_contiguous() and part[3].data_ptr() % 16
+    with pytest.raises(kda.KDAError) as e:
+        kda.gdn_recurrent(*part, p)
+    assert e.value.code == -3 and torch.equal(p, start)
+    part[3] = part[3].clone()
+    o = kda.gdn_recurrent(*part, p)
+    a = [x[n][0, 1:4].double().numpy() for n in ("q", "k", "v", "g", "beta")]
+    a[3] = a[3][..., None]
+    ref = list(steps(pool[0].double().numpy(), *a))
+    within(o[0].cpu().numpy(), np.stack([y for y, _ in ref]), "o")
+    within(p[0].cpu().numpy(), ref[-1][1], "state")
