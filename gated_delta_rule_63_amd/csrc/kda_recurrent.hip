@@ -24,10 +24,11 @@
 // 4.7 us, the latency of a launch and of one trip to memory each way.
 //
 // Every product and sum of the state's update is rounded by itself, and P^T k
-// is summed in eight interleaved parts of 16 rows (even parts, then odd ones):
-// the bits of the formula evaluated operation by operation. A fused or
-// reordered form would be as accurate, but a bf16 pool turns a difference in
-// the last bit into a whole bf16 step whenever it falls on a rounding boundary.
+// is summed in eight interleaved parts of 16 rows (even parts, then odd ones), for
+// either number of waves: the states' bits are those of that order on any fp32
+// machine. A fused or reordered form would be as accurate, but a bf16 pool turns a
+// difference in the last bit into a whole bf16 step whenever it falls on a rounding
+// boundary. (o is fused, and not part of this.)
 #include "kda_device.h"
 #include "kda_recurrent.h"
 

@@ -244,3 +244,40 @@ def test_scalar_gate_of_a_slice(torch_gpu):
     ref = list(steps(pool[0].double().numpy(), *a))
     within(o[0].cpu().numpy(), np.stack([y for y, _ in ref]), "o")
     within(p[0].cpu().numpy(), ref[-1][1], "state")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pool_dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("N,H,scalar", [(2, 3, False), (3, 2, True), (70, 6, False), (39, 10, True)])
+def test_bits_of_the_states(torch_gpu, pool_dtype, N, H, scalar):
+    """The states' bits are those of fp32 arithmetic on the CPU, one rounding an
+    operation, in the kernel's order: P^T k in eight sums over rows r, r + 8, ..., of
+    which 0, 2, 4, 6 are added in turn, then 1, 3, 5, 7, then both. (The decays come from
+    the kernel: e^g is what a state of ones becomes where k and beta are zero.) Eight
+    waves a head and four, 6 and 420 or 390 pairs on 256 compute units."""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    T = 3
+    x, pool, _ = make(torch, N, T, H, torch.bfloat16, scalar, N, getattr(torch, pool_dtype), 23)
+    d = {n: t.cuda() for n, t in x.items()}
+    f = kda.gdn_recurrent if scalar else kda.recurrent
+    ones = torch.ones(N * T, H, 128, 128, device="cuda")
+    zero, flat = torch.zeros(N * T, 1, H, 128, device="cuda"), lambda t: t.reshape(N * T, 1, *t.shape[2:])
+    f(zero, zero, zero, flat(d["g"]), torch.zeros(N * T, 1, H, device="cuda"), ones)
+    decay = ones[..., :1].reshape(N, T, H, 128, 1).cpu().numpy()
+    got = pool.cuda()
+    f(*(d[n] for n in ("q", "k", "v", "g", "beta")), got)
+    S = pool.float().numpy()
+    k, v, beta = (x[n].float().numpy() for n in ("k", "v", "beta"))
+    for t in range(T):
+        Pt = S * decay[:, t]
+        kk = k[:, t, :, :, None]
+        pk = (Pt * kk).reshape(N, H, 16, 8, 128)
+        a = pk[:, :, 0]
+        for m in range(1, 16):
+            a = a + pk[:, :, m]
+        half = [((a[:, :, i] + a[:, :, i + 2]) + a[:, :, i + 4]) + a[:, :, i + 6] for i in (0, 1)]
+        be = beta[:, t, :, None] * (v[:, t] - (half[0] + half[1]))
+        S = Pt + kk * be[:, :, None, :]
+        assert S.dtype == np.float32
+    assert torch.equal(got.cpu(), torch.from_numpy(S).to(got.dtype))
