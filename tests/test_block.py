@@ -386,3 +386,23 @@ def test_default_gate_into_the_rule(gpu, scalar):
     within(hT[0].cpu().numpy(), S, "hT")
     for name, u, r in zip("dq dk dv dg dbeta dh0".split(), d, rule_bwd(*x, do.double().numpy(), [(0, 0, T)])):
         within(u.cpu().numpy(), r, name)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once(gpu):
+    """The gradients' partial sums of two calls that run at the same time stay apart."""
+    import gated_delta_rule_63_amd as kda
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    B, T, H = 1, 2048, 16
+    q, f, b, A, bias, g, o, w = n(B, T, H, 128), n(B, T, H, 128), n(B, T, H), n(H), n(H, 128), n(B, T, H, 128), n(B, T, H, 128), n(128)
+    up = [n(B, T, H, 128), n(B, T, H, 128)]
+    run = lambda u, **k: (*kda.block_in_bwd(q, f, f, b, A, u, o, u, b, dt_bias=bias, **k), *kda.block_out_bwd(o, q, w, u, **k))
+    alone = [run(u) for u in up]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [run(u, stream=s) for _ in range(3) for u, s in zip(up, streams)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(out, alone[i % 2])), i
+    assert not torch.equal(alone[0][4], alone[1][4])

@@ -435,3 +435,25 @@ def test_bwd_stronger_gates(torch_gpu, scalar, low, high):
         within(x.cpu().numpy(), r, n)
     _check_rms(got, ref, f"[{low}, {high}]", 2 * RMS_BAR)
     within(got[3].cpu().numpy(), ref[3], "dg", tol=2e-4)
+
+
+@pytest.mark.gpu
+def test_bwd_two_calls_at_once(torch_gpu):
+    """Calls that run at the same time on two streams, on the same inputs and each with a
+    gradient of its own, give what each gives alone: their workspaces are apart. (On long
+    sequences with few heads, so that one does not fill the chip.)"""
+    torch = torch_gpu
+    import gated_delta_rule_63_amd as kda
+    from gpu_util import to_device
+    inp = W.make_inputs(W.variant("T8192_H96", T=4096, H=4, h0=True), 19)
+    t = to_device(inp, "bf16")
+    do = [torch.from_numpy(_grads(inp, seed, False)[0]).cuda() for seed in (20, 21)]
+    run = lambda d, **kw: kda.bwd(t["q"], t["k"], t["v"], t["g"], t["beta"], d, initial_state=t["h0"], **kw)
+    alone = [run(d) for d in do]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [run(d, stream=s) for _ in range(3) for d, s in zip(do, streams)]
+    torch.cuda.synchronize()
+    for i, out in enumerate(got):
+        assert all(torch.equal(x, y) for x, y in zip(out, alone[i % 2])), i
+    assert not torch.equal(alone[0][0], alone[1][0])
