@@ -1,6 +1,11 @@
 """Torch marshalling of the operators around the rule: its gradient, its recurrent
 form over a pool of states, and what comes right before and after it
-(include/kda.h). Outputs and workspaces are allocated on the call's stream."""
+(include/kda.h). Outputs and workspaces are allocated on the call's stream.
+
+Nothing here (nor fwd() and its kin) is recorded by torch.autograd: results do not
+require gradients whatever the inputs do, and a model that trains through these calls
+joins each with its gradient itself, in a torch.autograd.Function whose forward calls
+the one and whose backward calls the other."""
 from __future__ import annotations
 
 import contextlib
@@ -241,7 +246,9 @@ def block_in_bwd(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch.Ten
                  stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
     """Gradient of block_in(): its inputs, and the gradients with respect to its outputs
     (as bwd() returns them). Returns (dq, dk, df, db, dA_log, ddt_bias), the first four
-    in q's dtype, the sums over tokens fp32 (ddt_bias None without dt_bias)."""
+    in q's dtype, the sums over tokens fp32 (ddt_bias None without dt_bias). Every row is
+    summed: with packed sequences that end before T, cut all arguments to the first cu[N]
+    tokens, since bwd() leaves the rows behind them unset."""
     return _block_in_bwd("kda_block_in_bwd", q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps, stream)
 
 
@@ -249,7 +256,7 @@ def gdn_block_in_bwd(q: torch.Tensor, k: torch.Tensor, f: torch.Tensor, b: torch
                      dq: torch.Tensor, dk: torch.Tensor, dg: torch.Tensor, dbeta: torch.Tensor,
                      dt_bias: _Tensor = None, lower_bound: Optional[float] = None, eps: float = 1e-6,
                      stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
-    """Gradient of gdn_block_in()."""
+    """Gradient of gdn_block_in(), as block_in_bwd() (which rows are summed, too)."""
     return _block_in_bwd("kda_gdn_block_in_bwd", q, k, f, b, A_log, dq, dk, dg, dbeta, dt_bias, lower_bound, eps,
                          stream)
 
@@ -305,7 +312,8 @@ def _check_block_out(o, z, weight, activation, dy=None, _device=True):
 def block_out_bwd(o: torch.Tensor, z: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor,
                   activation: str = "sigmoid", eps: float = 1e-5,
                   stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, ...]:
-    """Gradient of block_out(). Returns (do fp32, dz in z's dtype, dweight fp32)."""
+    """Gradient of block_out(). Returns (do fp32, dz in z's dtype, dweight fp32). dweight
+    takes every row: cut padded ones off, as for block_in_bwd()."""
     _check_block_out(o, z, weight, activation, dy)
     d = _rows_desc(z)
     with _on(z.device, stream) as s:

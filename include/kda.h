@@ -439,7 +439,9 @@ kda_status_t kda_gdn_block_in(const void* q, const void* k, const void* f, const
 /* Its gradient. q .. eps are the forward's inputs; dq_out, dk_out (in_dtype),
  * dg and dbeta (fp32) the gradients with respect to its outputs; dq, dk, df, db
  * (in_dtype), dA_log [H] and ddt_bias (fp32, like dt_bias; NULL: not written)
- * the results. No output may overlap an input. Needs desc->workspace of
+ * the results. The sums take every row: with packed sequences that end before T,
+ * describe the cu[N] tokens alone (the rows behind them are not written by kda_bwd).
+ * No output may overlap an input. Needs desc->workspace of
  * kda_block_in_bwd_workspace_size(desc) bytes (KDA_ERR_WORKSPACE), 16-byte
  * aligned, used by one call at a time; sums over tokens are fp32 in a fixed order. T = 0 gives zero
  * sums. */
@@ -463,7 +465,8 @@ size_t kda_block_in_bwd_workspace_size(const kda_desc_t* desc);   /* enough for 
  *     weight [128] fp32;  activation a kda_activation_t: sigmoid(z) or z sigmoid(z)
  * and its gradient: d_o (fp32), dz (in_dtype) and dweight (fp32) from dy
  * (in_dtype), with desc->workspace of kda_block_out_bwd_workspace_size(desc)
- * bytes (KDA_ERR_WORKSPACE). Errors as kda_block_in; every pointer to rows of 128
+ * bytes (KDA_ERR_WORKSPACE); dweight takes every row, as kda_block_in_bwd's sums do.
+ * Errors as kda_block_in; every pointer to rows of 128
  * channels, weight included, is 16-byte aligned. d_o may take o's place, dz that of z or dy. */
 typedef enum { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_activation_t;
 

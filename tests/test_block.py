@@ -406,3 +406,71 @@ def test_two_calls_at_once(gpu):
     for i, out in enumerate(got):
         assert all(torch.equal(x, y) for x, y in zip(out, alone[i % 2])), i
     assert not torch.equal(alone[0][4], alone[1][4])
+
+
+@pytest.mark.gpu
+def test_joined_by_autograd_functions(gpu):
+    """The calls joined with their gradients in torch.autograd.Function, as the binding
+    describes it: a step's gradients are those of the calls made one by one, and stay so
+    on a side stream. The calls alone leave no graph."""
+    import gated_delta_rule_63_amd as kda
+
+    class In(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, f, b, A, bias):
+            ctx.save_for_backward(q, k, f, b, A, bias)
+            return kda.block_in(q, k, f, b, A, dt_bias=bias, lower_bound=-5.0)
+
+        @staticmethod
+        def backward(ctx, *up):
+            *x, bias = ctx.saved_tensors
+            return kda.block_in_bwd(*x, *(u.contiguous() for u in up), dt_bias=bias, lower_bound=-5.0)
+
+    class Rule(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, *x):
+            ctx.save_for_backward(*x)
+            return kda.fwd(*x, output_final_state=False)[0]
+
+        @staticmethod
+        def backward(ctx, do):
+            return kda.bwd(*ctx.saved_tensors, do.contiguous())[:5]
+
+    class Out(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, o, z, w):
+            ctx.save_for_backward(o, z, w)
+            return kda.block_out(o, z, w)
+
+        @staticmethod
+        def backward(ctx, dy):
+            return kda.block_out_bwd(*ctx.saved_tensors, dy.contiguous())
+
+    gen = torch.Generator(device="cuda").manual_seed(31)
+    n = lambda *s: torch.randn(*s, device="cuda", generator=gen)
+    B, T, H = 2, 70, 3
+    leaves = [n(B, T, H, 128), n(B, T, H, 128), n(B, T, H, 128), n(B, T, H), 0.3 * n(H), n(H, 128), n(B, T, H, 128),
+              n(B, T, H, 128), 1 + 0.1 * n(128)]
+    dy = n(B, T, H, 128)
+    q, k, f, b, A, bias, v, z, w = leaves
+    ins = kda.block_in(q, k, f, b, A, dt_bias=bias, lower_bound=-5.0)
+    o = kda.fwd(ins[0], ins[1], v, *ins[2:], output_final_state=False)[0]
+    do, dz, dw = kda.block_out_bwd(o, z, w, dy)
+    dq, dk, dv, dg, db, _ = kda.bwd(ins[0], ins[1], v, *ins[2:], do)
+    want = [*kda.block_in_bwd(q, k, f, b, A, dq, dk, dg, db, dt_bias=bias, lower_bound=-5.0), dv, dz, dw]
+
+    def step():
+        x = [t.detach().clone().requires_grad_() for t in leaves]
+        q1, k1, g1, b1 = In.apply(*x[:6])
+        y = Out.apply(Rule.apply(q1, k1, x[6], g1, b1), *x[7:])
+        return torch.autograd.grad((y * dy).sum(), x)
+
+    assert not kda.block_out(o.requires_grad_(), z, w).requires_grad
+    side = torch.cuda.Stream()
+    got = [step()]
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got.append(step())
+    torch.cuda.synchronize()
+    for grads_ in got:
+        assert all(torch.equal(x, y) for x, y in zip(grads_, want))
