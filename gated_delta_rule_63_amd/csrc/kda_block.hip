@@ -12,14 +12,14 @@
 // lanes, without LDS. Norms, gates and sums are fp32; only what is
 // stored in bf16 is rounded, once. The forward kernels give each lane group one
 // row: four of them one after the other were slower at every size (T = 8192,
-// H = 96: 252 -> 278 us before the rule, 139 -> 146 after it; 512 rows: 4.0 ->
-// 10.7 and 2.4 -> 4.6).
+// H = 96, whole calls on one box: 273 -> 304 us before the rule, 139 -> 146 after
+// it; 512 rows, the kernels: 4.0 -> 10.7 and 2.4 -> 4.6).
 //
-// bf16, T = 8192, H = 96: before the rule 279 us (1.41 GB, 5.1 TB/s), after it
-// 139 us (0.81 GB, 5.8 TB/s). Gradients: before, H = 64, 279 + 5 us (1.35 GB, 4.8
-// TB/s), after, 4 x 1001 tokens, H = 64, 88 + 5 us (0.46 GB, 4.9 TB/s). A large
-// copy reaches 4.8 to 5.0. 512 rows of a decode step: 4.0 us, a launch and a trip
-// to memory each way.
+// Kernel trace, means, bf16, T = 8192, H = 96: before the rule 278 us (1.41 GB, 5.1
+// TB/s; 271 a call untraced), after it 139 us (0.81 GB, 5.8 TB/s). Gradients:
+// before, H = 64, 279 + 5 us (1.35 GB, 4.8 TB/s), after, 4 x 1001 tokens, H = 64, 89
+// + 5 us (0.46 GB, 4.9 TB/s). A large copy reaches 5.0 to 5.1. 512 rows of a decode
+// step: 4.2 us, a launch and a trip to memory each way.
 //
 // Sums over tokens (dA_log, ddt_bias, dweight) stay in fp32 registers over the rows
 // that a lane group visits. One partial row goes to the workspace, per group (dA_log,
@@ -92,7 +92,9 @@ __device__ __forceinline__ float dot8(const f32x8& a, const f32x8& b) {
     return s;
 }
 
-// s = sigmoid(x), c = 1 - s, both to full relative accuracy.
+// s = sigmoid(x), c = 1 - s, neither by cancellation. The reciprocals here and in
+// softplus() are the instruction's, to 1 ulp: an fp32 call's error is 1.1e-7 to 1.3e-7
+// of its result, where the formulas in elementary operations leave 0.8e-7.
 __device__ __forceinline__ void sigmoid(float x, float& s, float& c) {
     const float E = expf(-fabsf(x)), r = __builtin_amdgcn_rcpf(1.f + E), e = E * r;
     s = x >= 0.f ? r : e;

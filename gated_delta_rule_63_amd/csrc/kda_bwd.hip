@@ -33,12 +33,12 @@
 // leaves (g, beta, the states) come out with fp32 accuracy, and dg is a sum of
 // differences that cancel, where 16-bit operands would leave an error of 1e-3.
 //
-// T = 8192, H = 96, bf16, one sequence (786,432 tokens x heads): 450 + 1900 +
-// 1490 us in a row (3.7 ms). 1 is bound by memory (2.3 GB read and written, 5.0
-// TB/s). 2 moves 8.3 GB (4.3 TB/s; 1.5 GB of it operands read again by V-blocks
-// that drifted apart) and keeps the matrix unit 57% busy, 3 moves 6.4 GB (4.3
-// TB/s) at 56%. The states that pass from 2 to 3, fp32 [128][128] twice a chunk,
-// are 6.4 of the 17 GB.
+// T = 8192, H = 96, bf16, one sequence (786,432 tokens x heads): 453 + 1947 +
+// 1535 us as a kernel trace's means (432 + 1824 + 1408 at best), 3.72 ms a call
+// untraced. 1 is bound by memory (2.3 GB read and written, 5.0 TB/s). 2 moves 8.4 GB
+// (4.3 TB/s; 1.6 GB of it operands read again by V-blocks that drifted apart) and
+// keeps the matrix unit 57% busy, 3 moves 6.4 GB (4.2 TB/s) at 57%. The states that
+// pass from 2 to 3, fp32 [128][128] twice a chunk, are 6.4 of the 17 GB.
 //
 // Gates inside a chunk: two sub-blocks of 16 tokens, each with its decay E1
 // counted from behind its eighth token; E1 and 1 / E1 stay within e^+-40 for

@@ -18,10 +18,10 @@
 // a wave. NC = 4 gives 128-byte row pieces and 4 waves a head; NC = 2 gives
 // 64-byte pieces and 8 waves a head, for batches too small to occupy the chip.
 //
-// 256 sequences x 32 heads, one token, bf16 pool: 102 us, 0.54 GB at 5.3 TB/s.
-// 16 x 5 drafted tokens, 96 heads, fp32 pool, every state kept: 125 us, 0.62 GB
-// at 4.9 TB/s (a large copy: 4.8 to 5.0). One sequence of 32 heads, one token:
-// 4.7 us, the latency of a launch and of one trip to memory each way.
+// 256 sequences x 32 heads, one token, bf16 pool: 103 us, 0.54 GB at 5.2 TB/s.
+// 16 x 5 drafted tokens, 96 heads, fp32 pool, every state kept: 124 us, 0.62 GB
+// at 5.0 TB/s (a large copy: 5.0 to 5.1). One sequence of 32 heads, one token:
+// 4.5 us, the latency of a launch and of one trip to memory each way.
 //
 // Every product and sum of the state's update is rounded by itself, and P^T k
 // is summed in eight interleaved parts of 16 rows (even parts, then odd ones), for
