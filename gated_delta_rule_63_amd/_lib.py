@@ -25,13 +25,33 @@ EXPORTS = ["kda_status_string", "kda_version", "kda_fwd_check", "kda_fwd", "kda_
            "kda_bwd", "kda_gdn_bwd", "kda_bwd_workspace_size", "kda_recurrent", "kda_gdn_recurrent",
            "kda_block_in", "kda_gdn_block_in", "kda_block_in_bwd", "kda_gdn_block_in_bwd",
            "kda_block_in_bwd_workspace_size", "kda_block_out", "kda_block_out_bwd",
-           "kda_block_out_bwd_workspace_size"]
+           "kda_block_out_bwd_workspace_size",
+           "kda_scan", "kda_scan_workspace_size", "kda_scan_states_rows", "kda_scan_bwd", "kda_scan_bwd_workspace_size",
+           "kda_scan_recurrent", "kda_add_norm", "kda_add_norm_q8", "kda_add_norm_bwd",
+           "kda_add_norm_bwd_workspace_size", "kda_beam_select", "kda_beam_workspace_size", "kda_beam_reorder"]
 
 
 class Desc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("K", ctypes.c_int32), ("V", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
                 ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class ScanDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("C", ctypes.c_int32), ("num_seqs", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("leaky", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("C", ctypes.c_int32), ("dtype", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class BeamDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("W", ctypes.c_int32), ("V", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eos", ctypes.c_int32),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
@@ -110,6 +130,19 @@ def lib():
             fn = getattr(L, name + "_workspace_size")
             fn.argtypes = [D]
             fn.restype = ctypes.c_size_t
+        S, M, E, Z = ctypes.POINTER(ScanDesc), ctypes.POINTER(NormDesc), ctypes.POINTER(BeamDesc), ctypes.c_size_t
+        for name, types, result in (
+                ("scan", [P] * 7 + [S, P], ctypes.c_int), ("scan_workspace_size", [S], Z),
+                ("scan_states_rows", [S, I], ctypes.c_int64), ("scan_bwd", [P] * 10 + [S, P], ctypes.c_int),
+                ("scan_bwd_workspace_size", [S, I], Z),
+                ("scan_recurrent", [P] * 6 + [I, I, P, S, P], ctypes.c_int),
+                ("add_norm", [P, P, P, R, P, P, M, P], ctypes.c_int),
+                ("add_norm_q8", [P, P, P, R, I, P, P, P, M, P], ctypes.c_int),
+                ("add_norm_bwd", [P, P, R] + [P] * 5 + [M, P], ctypes.c_int), ("add_norm_bwd_workspace_size", [M], Z),
+                ("beam_select", [P] * 6 + [E, P], ctypes.c_int), ("beam_workspace_size", [E], Z),
+                ("beam_reorder", [P, I, Z, P, P, P, I, I, P], ctypes.c_int)):
+            fn = getattr(L, "kda_" + name)
+            fn.argtypes, fn.restype = types, result
         _lib = L
     return _lib
 

@@ -1,0 +1,56 @@
+// kda_scan.h -- host/device interface of the rule with a vector state (kda_scan.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int kScanChunk = 128;   // tokens between kept states
+constexpr int kScanStrip = 64;    // channels of a workgroup
+
+struct ScanArgs {
+    const void* x;
+    const float* g;
+    const int32_t* cu;            // nullptr: N rows of T tokens
+    const float* h0;              // [N, C], nullptr: zero
+    void* y;
+    float* hT;                    // [N, C], nullptr: not written
+    float* states;                // [scan_slots(), C]; the forward writes them if there, the gradient reads them
+    // gradient
+    const void* dy;
+    const float* dhT;             // [N, C], nullptr: zero
+    void* dx;
+    float* dg;
+    float* dh0;                   // [N, C], nullptr: not written
+    // workspace, [scan_slots(), C] each: a chunk's decay and what it adds (split form), and the gradient of
+    // the state that leaves each chunk
+    float2* sums;
+    float* grads;
+    int T, C, N, slots;
+    bool f32, leaky, split;
+};
+
+struct ScanPoolArgs {
+    const void* x;
+    const float* g;
+    const int32_t* cu;
+    const int32_t* slots;
+    const int32_t* out_slots;
+    void* pool;                   // [num_slots, C]
+    void* y;
+    int T, C, N, num_slots;
+    bool f32, leaky, pool_bf16;
+};
+
+// Rows of `states`: one for each chunk of each sequence; packed, sequence n's begin at row cu[n] / 128 + n.
+long long scan_slots(int B, int T, int N, bool packed);
+// Whether the chunks of these chains run side by side (three kernels) instead of one after the other.
+bool scan_split(int T, int C, int N, int cus);
+
+hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
+// known: `states` holds the forward's; else it is formed first.
+hipError_t launch_scan_bwd(const ScanArgs& a, bool known, hipStream_t s);
+hipError_t launch_scan_recurrent(const ScanPoolArgs& a, hipStream_t s);
+
+}  // namespace kda

@@ -477,6 +477,142 @@ kda_status_t kda_block_out_bwd(const float* o, const void* z, const float* weigh
                                const kda_desc_t* desc, void* stream);
 size_t kda_block_out_bwd_workspace_size(const kda_desc_t* desc);
 
+/* ---------------------------------------------------------------------------
+ * The rule with a vector state: per sequence and channel,
+ *     h_t = a_t h_{t-1} + b_t,  a = exp(g),  b = x, or leaky: b = (1 - a) x,  y = h
+ *     x, y    [B, T, C] dtype (bf16 or fp32);  g [B, T, C] fp32, a log-decay
+ *     cu_seqlens as for kda_fwd;  h0, hT [N, C] fp32 (NULL: zero, not written)
+ *     states  fp32, NULL or kda_scan_states_rows(desc) rows of C: the state that
+ *             enters each chunk of 128 tokens, for kda_scan_bwd. Row n ceil(T / 128) + j
+ *             holds chunk j of sequence n; packed, row cu[n] / 128 + n + j. Rows
+ *             without a chunk are left as they were.
+ * C is any number of channels (heads times head size, say); nothing needs more
+ * alignment than its type. g is usually <= 0; -inf is a reset (nothing of the
+ * state before it remains), and finite g > 0 a growing state. The state is fp32.
+ * y == x is allowed; rows of tokens outside [cu[0], cu[N]) are left as they were;
+ * a zero-length sequence has hT = h0. T is at most 2^30, B T C 2^40, C 2^20 and
+ * N ceil(C / 64) 2^22 (KDA_ERR_SHAPE). Needs desc->workspace of
+ * kda_scan_workspace_size(desc) bytes (0 for most shapes; KDA_ERR_WORKSPACE),
+ * 16-byte aligned, used by one call at a time. Nothing is allocated; results do
+ * not depend on the order of execution. Other errors as kda_fwd. */
+typedef struct kda_scan_desc {
+    int32_t B, T, C;
+    int32_t num_seqs;          /* N: B without cu_seqlens                     */
+    int32_t dtype;             /* of x, y, dy, dx                             */
+    int32_t leaky;             /* 0: b = x; 1: b = (1 - a) x                  */
+    void* workspace;
+    size_t workspace_bytes;
+} kda_scan_desc_t;
+
+kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, const float* h0, void* y,
+                      float* hT, float* states, const kda_scan_desc_t* desc, void* stream);
+size_t kda_scan_workspace_size(const kda_scan_desc_t* desc);   /* with or without cu_seqlens; 0 when invalid */
+/* Rows of `states`, for cu_seqlens (packed != 0) or without; 0 when invalid. */
+int64_t kda_scan_states_rows(const kda_scan_desc_t* desc, int32_t packed);
+
+/* Its gradient. x .. h0 are the forward's inputs, dy [B, T, C] (dtype) and dhT
+ * [N, C] (fp32, NULL: zero) the gradients with respect to its outputs; dx (dtype),
+ * dg (fp32) and dh0 (fp32, NULL: not written) the results. states: what the
+ * forward wrote, or NULL: recomputed from x and g in the workspace. dg is zero
+ * where the decay is. dx == dy is allowed; no other output may overlap an input.
+ * Needs desc->workspace of kda_scan_bwd_workspace_size(desc, states != NULL) bytes. */
+kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqlens, const float* h0,
+                          const float* states, const void* dy, const float* dhT, void* dx, float* dg, float* dh0,
+                          const kda_scan_desc_t* desc, void* stream);
+size_t kda_scan_bwd_workspace_size(const kda_scan_desc_t* desc, int32_t with_states);
+
+/* The same rule token by token over a pool of states [num_slots, C] (KDA_F32 or
+ * KDA_BF16): slots, out_slots, empty places and what a call may do with a slot as
+ * for kda_recurrent. desc->workspace is ignored. y == x is allowed. */
+kda_status_t kda_scan_recurrent(const void* x, const float* g, const int32_t* cu_seqlens, const int32_t* slots,
+                                const int32_t* out_slots, void* pool, int32_t num_slots, int32_t pool_dtype,
+                                void* y, const kda_scan_desc_t* desc, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * What joins two layers: the residual's addition and an RMS norm over C channels,
+ *     r = x + residual (rounded to res_dtype),  y = r / sqrt(mean(r^2) + eps) * weight
+ *     x, y [rows, C] dtype;  residual, r [rows, C] res_dtype: dtype, or fp32;
+ *     weight [C] fp32
+ * The norm is of r as it is stored. residual == NULL: r = x, and r_out is not
+ * written. y == x and r_out == residual are allowed. C is 1 to 32,768, rows times C at
+ * most 2^40 and rows at most 2^31 - 1 (KDA_ERR_SHAPE); a negative or non-finite
+ * eps or another res_dtype is KDA_ERR_UNSUPPORTED. Rows of a multiple of eight
+ * channels, in tensors that are all 16-byte aligned, are the fast ones.
+ *
+ * kda_add_norm_q8 gives y in 8 bits: with amax over a row (group == 0) or over
+ * groups of 128 channels (group == 128, C a multiple of 128, every pointer
+ * 16-byte aligned; other groups: KDA_ERR_UNSUPPORTED),
+ *     scale = max(amax |y|, 2^-40) / 448,  q = y / scale in e4m3 (OCP, nearest even)
+ *     q [rows, C] one byte a value;  scales [rows, C / group] fp32 (group 0: [rows])
+ * y is not rounded in between. A row that holds infinities or NaN has scales and
+ * values that are not numbers to use. */
+typedef struct kda_norm_desc {
+    int64_t rows;
+    int32_t C;
+    int32_t dtype, res_dtype;
+    void* workspace;           /* the gradient's */
+    size_t workspace_bytes;
+} kda_norm_desc_t;
+
+kda_status_t kda_add_norm(const void* x, const void* residual, const float* weight, float eps, void* y, void* r_out,
+                          const kda_norm_desc_t* desc, void* stream);
+kda_status_t kda_add_norm_q8(const void* x, const void* residual, const float* weight, float eps, int32_t group,
+                             void* q, float* scales, void* r_out, const kda_norm_desc_t* desc, void* stream);
+
+/* Gradient of kda_add_norm: r [rows, C] (res_dtype) as the forward stored it (x
+ * without a residual, and res_dtype then its dtype), dy (dtype) the gradient of y,
+ * dr (res_dtype, NULL: zero) that of r from where else it is used. The gradient of
+ * x and of residual is the same sum: dx in dtype and d_residual in res_dtype
+ * (NULL: not written). dweight [C] fp32, over every row, in a fixed order (0 rows:
+ * zero). dx == dy and d_residual == dr are allowed. Needs desc->workspace of
+ * kda_add_norm_bwd_workspace_size(desc) bytes, 16-byte aligned, used by one call
+ * at a time. */
+kda_status_t kda_add_norm_bwd(const void* r, const float* weight, float eps, const void* dy, const void* dr,
+                              void* dx, void* d_residual, float* dweight, const kda_norm_desc_t* desc, void* stream);
+size_t kda_add_norm_bwd_workspace_size(const kda_norm_desc_t* desc);
+
+/* ---------------------------------------------------------------------------
+ * One step of beam search. For each of B entries with W beams, over all beams w
+ * and tokens v,
+ *     total = scores[w] + logits[w, v] - log(sum_u exp(logits[w, u]))
+ * the K largest totals, descending, ties to the lowest w V + v:
+ *     logits [B, W, V] dtype (bf16 or fp32);  scores [B, W] fp32 (-inf or NaN: a dead beam)
+ *     done   bytes [B, W], NULL: none. A beam whose byte is not 0 has one candidate,
+ *            token `eos` with its score as it is; its logits are not read.
+ *     out_scores fp32, parents int32 (the beam), tokens int32, each [B, K]
+ * A logit of -inf or NaN is no candidate and adds nothing to the sum; +inf counts
+ * as the largest finite value. Places beyond the last candidate hold -inf, -1, -1.
+ * Totals are compared in fp64, formed from sums of fp32 exponentials (an error of
+ * about 1e-8). W and K are 1 to 64, V 1 to 2^25, B W at most 2^20 (KDA_ERR_SHAPE);
+ * with done, eos lies in [0, V) (KDA_ERR_SHAPE). Needs desc->workspace of
+ * kda_beam_workspace_size(desc) bytes, 16-byte aligned, used by one call at a time. */
+typedef struct kda_beam_desc {
+    int32_t B, W, V, K;
+    int32_t dtype;
+    int32_t eos;
+    void* workspace;
+    size_t workspace_bytes;
+} kda_beam_desc_t;
+
+kda_status_t kda_beam_select(const void* logits, const float* scores, const uint8_t* done, float* out_scores,
+                             int32_t* parents, int32_t* tokens, const kda_beam_desc_t* desc, void* stream);
+size_t kda_beam_workspace_size(const kda_beam_desc_t* desc);
+
+/* Reorders the states of a pool (of kda_recurrent, kda_scan_recurrent or any other
+ * with equal slots) after a selection: slots int32 [B, W] names the slot of each
+ * beam, parents int32 [B, W] the beam that each new beam continues, new_slots int32
+ * [B, W] receives the slot of each new beam. A beam's first child keeps its slot,
+ * so that only further children are copied: into the slots of beams that have no
+ * children, in turn. new_slots is the same set as slots in each entry, and the same for
+ * every pool that is reordered by the same slots and parents. A parent outside
+ * [0, W) is an empty place: it gets a free slot, whose state is left as it is.
+ * A slot outside [0, num_slots) is never read or written. slots of one call are
+ * distinct. new_slots may not overlap slots or parents. W is 1 to 64, B W at
+ * most 2^20, num_slots >= 0 (KDA_ERR_SHAPE). Nothing else needs alignment; slots of a
+ * multiple of 16 bytes in a 16-byte aligned pool are the fast ones. */
+kda_status_t kda_beam_reorder(void* pool, int32_t num_slots, size_t slot_bytes, const int32_t* slots,
+                              const int32_t* parents, int32_t* new_slots, int32_t B, int32_t W, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
