@@ -40,7 +40,8 @@ struct ReorderArgs {
     int unit;                          // bytes of a copied piece: 16, 4 or 1
 };
 
-int beam_splits(int B, int W, int V, int cus);
+// Parts that a row is cut into, each a workgroup's.
+int beam_splits(int B, int W, int V, bool f32, int cus);
 
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s);
 hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s);

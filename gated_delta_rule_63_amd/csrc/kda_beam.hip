@@ -16,8 +16,8 @@ namespace kda {
 namespace beam {
 
 constexpr int kThreads = 256;
-constexpr int kPer = 32;                            // logits of a thread in a tile
-constexpr int kTile = kThreads * kPer;
+constexpr int kPieces = 4;                          // 16-byte pieces of a thread in a tile
+constexpr int kPer = 8 * kPieces;                   // its logits, at most (bf16)
 constexpr float kHuge = 3.4028234663852886e38f;
 constexpr uint32_t kNone = 0xffffffffu;
 
@@ -29,8 +29,9 @@ __device__ __forceinline__ uint64_t ascending(double x) {
     const uint64_t u = __double_as_longlong(x);
     return u >> 63 ? ~u : u | 1ull << 63;
 }
-// 0 for what is no candidate; every float above -inf comes out above 0x007fffff.
-__device__ __forceinline__ uint32_t order_of(float x) { return x > -INFINITY ? ascending(fminf(x, kHuge)) : 0u; }
+// 0 for what is no candidate; every float above -inf comes out above 0x007fffff. (The
+// zero added makes a zero of -0, which ties with it.)
+__device__ __forceinline__ uint32_t order_of(float x) { return x > -INFINITY ? ascending(fminf(x, kHuge) + 0.f) : 0u; }
 __device__ __forceinline__ float value_of(uint32_t u) { return __uint_as_float(u & 0x80000000u ? u & 0x7fffffffu : ~u); }
 __device__ __forceinline__ uint32_t index_of(uint64_t key) { return ~(uint32_t)key; }
 
@@ -40,6 +41,25 @@ __device__ __forceinline__ T wave_all(T x, F f) {
     for (int o = 1; o < 64; o <<= 1) x = f(x, __shfl_xor(x, o));
     return x;
 }
+
+// The largest of a wave's values, in every lane.
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+#define KDA_STEP(ctrl, rows) x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xf, false))
+    KDA_STEP(0x111, 0xf);      // from 1, 2, 4 and 8 lanes below within 16 ...
+    KDA_STEP(0x112, 0xf);
+    KDA_STEP(0x114, 0xf);
+    KDA_STEP(0x118, 0xf);
+    KDA_STEP(0x142, 0xa);      // ... and from the last lane of the 16 and of the 32 below
+    KDA_STEP(0x143, 0xc);
+#undef KDA_STEP
+    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+__device__ __forceinline__ uint32_t high(uint32_t x) { return x; }
+__device__ __forceinline__ uint32_t high(uint64_t x) { return (uint32_t)(x >> 32); }
+__device__ __forceinline__ uint32_t lowest(uint32_t h, uint32_t) { return h; }
+__device__ __forceinline__ uint64_t lowest(uint32_t h, uint64_t) { return (uint64_t)h << 32; }
+__device__ __forceinline__ uint32_t highest(uint32_t h, uint32_t) { return h; }
+__device__ __forceinline__ uint64_t highest(uint32_t h, uint64_t) { return (uint64_t)h << 32 | 0xffffffffu; }
 
 // Of the 256 values in LDS (each a thread's best; 0: none) a bound that at least
 // `want` and, unless they tie, at most `most` of those above `floor` reach; with
@@ -65,12 +85,15 @@ __device__ __forceinline__ Bound<T> bound_of(const T* best, T floor, int want, i
     T lo = floor + 1;
     int n = reach(u, lo);
     if (n <= want) return Bound<T>{lo, n};
-    T hi = u[0] > u[1] ? u[0] : u[1], hi2 = u[2] > u[3] ? u[2] : u[3];
-    hi = wave_all(hi > hi2 ? hi : hi2, [](T x, T y) { return x > y ? x : y; });     // fewer than `want` reach hi + 1
-    T least = hi;
+    uint32_t top = 0, low = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) least = u[j] > floor && u[j] < least ? u[j] : least;
-    lo = wave_all(least, [](T x, T y) { return x < y ? x : y; });
+    for (int j = 0; j < 4; ++j) {
+        top = max(top, high(u[j]));
+        if (u[j] > floor) low = max(low, ~high(u[j]));
+    }
+    T hi = highest(wave_max(top), T());             // fewer than `want` reach hi + 1
+    const T least = lowest(~wave_max(low), T());
+    lo = least > lo ? least : lo;                   // all n reach it
     while (n > most && lo < hi) {
         const T mid = lo + (hi - lo) / 2 + 1;
         const int c = reach(u, mid);
@@ -101,10 +124,19 @@ __device__ __forceinline__ uint32_t index_bound(const uint32_t* first, int above
 // The place of key i among n unique ones, from the largest down.
 template <typename T>
 __device__ __forceinline__ int rank_of(const T* keys, int n, T key) {
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += keys[j] > key;
+    int r = 0, j = 0;
+    for (; j + 4 <= n; j += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r += keys[j + i] > key;
+    for (; j < n; ++j) r += keys[j] > key;
     return r;
 }
+
+template <bool F32> struct Raw { typedef uint16_t type; };
+template <> struct Raw<true> { typedef float type; };
+template <bool F32> using raw_t = typename Raw<F32>::type;
+__device__ __forceinline__ float up(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
+__device__ __forceinline__ float up(float x) { return x; }
 
 // Row pieces of 16 bytes at multiples of 16 bytes: piece j holds the row's logits
 // from VE j - off on, the first and the last of them only in part.
@@ -118,6 +150,8 @@ struct Piece {
         else return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
     }
 };
+template <bool F32> constexpr int kTile = kThreads * kPieces * Piece<F32>::VE;
+
 template <bool F32>
 __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long long j, int V) {
     constexpr int VE = Piece<F32>::VE, E = 16 / VE;
@@ -144,6 +178,27 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
     return p;
 }
 
+template <bool F32>
+__device__ __forceinline__ void ld_tile(Piece<F32> (&x)[kPieces], const char* row, int off, int t, int V) {
+    constexpr int VE = Piece<F32>::VE;
+    const long long j0 = (long long)t * (kThreads * kPieces);
+    if (j0 * VE >= off && (j0 + kThreads * kPieces) * VE - off <= V) {
+        const uint4* p = reinterpret_cast<const uint4*>(row - off * (16 / VE)) + j0 + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) x[i].raw = p[i * kThreads];
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, off, j0 + i * kThreads + threadIdx.x, V);
+    }
+}
+
+// A workgroup barrier for what passes through LDS: loads stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // One workgroup a part of a row, tile by tile. A tile's candidates are found by its
 // threads' largest logits: at least K threads reach a bound, so no logit below it
 // is among the row's K best, and those that reach it belong to the few threads
@@ -151,27 +206,33 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
 // From then on only logits above the bound count; one that equals it comes
 // too late.
 template <bool F32>
-__global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
-    extern __shared__ uint64_t keys[];              // up to 2 K from earlier tiles, 64 K of one; K sorted
+__global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
+    extern __shared__ uint4 shown[];                // 2 K threads' logits
+    uint64_t* const keys = reinterpret_cast<uint64_t*>(shown + 2 * kPieces * a.K);   // up to 2 K from earlier tiles, 64 K of one; K sorted
+    __shared__ int owner[2 * kBeamMax], rows[2];    // whose they are; how many, in turn
     __shared__ uint32_t best[2][kThreads], first[kThreads];
     __shared__ int held;
     __shared__ float sm[4];
     __shared__ double ss[4];
-    constexpr int VE = Piece<F32>::VE, NV = kPer / VE;
+    constexpr int VE = Piece<F32>::VE, NV = kPieces, TILE = kTile<F32>, PER = NV * VE;
     const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
     if (a.done && a.done[row]) return;
     const char* const base = static_cast<const char*>(a.logits) + (long long)row * a.V * (16 / VE);
     const int off = (int)(reinterpret_cast<uintptr_t>(base) & 15) / (16 / VE);
-    const int tiles = (int)(((long long)a.V + off + kTile - 1) / kTile);
+    const int tiles = (int)(((long long)a.V + off + TILE - 1) / TILE);
     const int t0 = (int)((long long)tiles * part / a.splits), t1 = (int)((long long)tiles * (part + 1) / a.splits);
     const int tid = threadIdx.x;
-    if (tid == 0) held = 0;
+    if (tid == 0) held = rows[0] = rows[1] = 0;
     float m = -kHuge, sum = 0.f;
     uint32_t floor = 0;
+    int turn = 0;
+    Piece<F32> next[NV];
+    if (t0 < t1) ld_tile<F32>(next, base, off, t0, a.V);
     for (int t = t0; t < t1; ++t) {
         Piece<F32> x[NV];
 #pragma unroll
-        for (int i = 0; i < NV; ++i) x[i] = ld_piece<F32>(base, off, (long long)t * (kTile / VE) + i * kThreads + tid, a.V);
+        for (int i = 0; i < NV; ++i) x[i] = next[i];
+        if (t + 1 < t1) ld_tile<F32>(next, base, off, t + 1, a.V);
         float top[NV], tm = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -201,10 +262,10 @@ __global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
         const uint32_t mine = order_of(tm);
         uint32_t* const bests = best[(t - t0) & 1];
         bests[tid] = mine;
-        __syncthreads();
+        lds_barrier();
         const Bound<uint32_t> bd = bound_of(bests, floor, a.K, 2 * a.K);
         if (bd.count == 0) continue;
-        uint32_t last = kNone;
+        uint32_t last = kNone, mine_first = 0;
         if (bd.count > 2 * a.K) {
             uint32_t f = kNone;
             int above = 0;
@@ -213,9 +274,9 @@ __global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
                 for (int i = NV - 1; i >= 0; --i)
 #pragma unroll
                     for (int e = VE - 1; e >= 0; --e)
-                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (kTile / VE) + i * kThreads + tid) * VE + e - off);
-            first[tid] = f;
-            __syncthreads();
+                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (TILE / VE) + i * kThreads + tid) * VE + e - off);
+            first[tid] = mine_first = f;
+            lds_barrier();
             {
                 uint32_t u[4];
 #pragma unroll
@@ -224,20 +285,26 @@ __global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
             }
             last = index_bound(first, above, a.K);
         }
-        if (mine >= bd.value) {
+        // The few threads that reach it leave their logits in LDS, where all look through them.
+        if (mine > bd.value || (mine == bd.value && mine_first <= last)) {
+            const int r = atomicAdd(&rows[turn & 1], 1);
+            owner[r] = tid;
 #pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                if (order_of(top[i]) < bd.value) continue;
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    const uint32_t o = order_of(x[i][e]);
-                    const uint32_t at = (uint32_t)((t * (kTile / VE) + i * kThreads + tid) * VE + e - off);
-                    if (o > bd.value || (o == bd.value && at <= last)) keys[atomicAdd(&held, 1)] = (uint64_t)o << 32 | ~at;
-                }
-            }
+            for (int i = 0; i < NV; ++i) shown[r * NV + i] = x[i].raw;
         }
+        lds_barrier();
+        if (tid == 0) rows[~turn & 1] = 0;
+        const float least = bd.value > 0x007fffffu ? value_of(bd.value) : -kHuge;
+        const bool finite = least < kHuge;          // +inf ties with the largest finite value
+        for (int j = tid; j < rows[turn & 1] * PER; j += kThreads) {
+            const int r = j / PER, e = j % PER;
+            const float v = up(reinterpret_cast<const raw_t<F32>*>(shown)[j]);
+            const uint32_t at = (uint32_t)((t * (TILE / VE) + e / VE * kThreads + owner[r]) * VE + e % VE - off);
+            if ((v >= least && at <= last) || (v > least && finite)) keys[atomicAdd(&held, 1)] = (uint64_t)order_of(v) << 32 | ~at;
+        }
+        ++turn;
         if (bd.count >= a.K) floor = bd.value;
-        __syncthreads();
+        lds_barrier();
         const int n = held;
         if (n > 2 * a.K && t + 1 < t1) {            // keep the K best of them
             uint64_t* const sorted = keys + (2 + 2 * kPer) * a.K;
@@ -245,11 +312,11 @@ __global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
                 const int r = rank_of(keys, n, keys[i]);
                 if (r < a.K) sorted[r] = keys[i];
             }
-            __syncthreads();
+            lds_barrier();
             if (tid < a.K) keys[tid] = sorted[tid];
             if (tid == 0) held = a.K;
             floor = (uint32_t)(sorted[a.K - 1] >> 32);
-            __syncthreads();
+            lds_barrier();
         }
     }
     const float M = wave_all(m, [](float x, float y) { return fmaxf(x, y); });
@@ -269,8 +336,10 @@ __global__ __launch_bounds__(kThreads) void kda_beam_rows(BeamArgs a) {
     for (int i = n + tid; i < a.K; i += kThreads) out[i] = 0;
 }
 
-// One workgroup a batch entry, one list of K keys (a part of a row) a thread. The K
-// best lie in lists whose first total reaches a bound, found as above.
+// One workgroup a batch entry. Its items are the keys of its L lists (parts of rows),
+// the lists' heads first, then their second keys, and so on: thread t's first item is
+// t. At least K of those reach a bound, found as above, and so every one of the K
+// best does; of the later items a list has only what follows K items that do.
 struct Total {
     uint64_t value;                                 // ascending
     uint32_t at;                                    // w V + v
@@ -280,48 +349,71 @@ __device__ __forceinline__ bool before(const Total& x, const Total& y) {
 }
 
 __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
-    extern __shared__ uint64_t raw[];
-    __shared__ double largest[kBeamMax], logs[kBeamMax];   // their sum may swallow the second
+    extern __shared__ uint64_t values[];            // K of 2 K lists; their indices behind them
+    __shared__ double score[kBeamMax], largest[kBeamMax], logs[kBeamMax];
+    __shared__ int state[kBeamMax];                 // 0 dead, 1 alive, 2 done
     __shared__ uint64_t best[kThreads];
     __shared__ uint32_t first[kThreads];
     __shared__ int held;
-    const int b = blockIdx.x, tid = threadIdx.x;
+    constexpr int AHEAD = 4;
+    const int b = blockIdx.x, tid = threadIdx.x, L = a.W * a.splits, n = L * a.K;
+    const uint64_t* const keys = a.keys + (long long)b * n;
+    uint64_t key[AHEAD];                            // asked for before anything waits
+    int list[AHEAD];
+    {
+        const int q = kThreads / L, r = kThreads % L;
+        int l = tid % L, k = tid / L;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) {
+            list[j] = l;
+            key[j] = k < a.K ? keys[l * a.K + k] : 0;
+            l += r;
+            k += q;
+            if (l >= L) l -= L, ++k;
+        }
+    }
     // sums of a row's parts, 16 lanes a row
     for (int w = tid >> 4; w < a.W; w += kThreads / 16) {
-        const BeamPart* p = a.parts + ((long long)b * a.W + w) * a.splits;
-        float M = -kHuge;
+        const int row = b * a.W + w, l = tid & 15;
+        const BeamPart* p = a.parts + (long long)row * a.splits;
+        const float s = a.scores[row];
+        const bool ended = a.done && a.done[row], mine = l < a.splits;
+        const BeamPart p0 = p[mine ? l : 0];
+        float M = mine ? p0.max : -kHuge;
         double S = 0.0;
-        if (!(a.done && a.done[b * a.W + w])) {
-            for (int i = tid & 15; i < a.splits; i += 16) M = fmaxf(M, p[i].max);
+        if (!ended) {
+            for (int i = l + 16; i < a.splits; i += 16) M = fmaxf(M, p[i].max);
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) M = fmaxf(M, __shfl_xor(M, o));
-            for (int i = tid & 15; i < a.splits; i += 16) S += p[i].sum * exp((double)p[i].max - (double)M);
+            if (mine) S = p0.sum * exp((double)p0.max - (double)M);
+            for (int i = l + 16; i < a.splits; i += 16) S += p[i].sum * exp((double)p[i].max - (double)M);
 #pragma unroll
             for (int o = 1; o < 16; o <<= 1) S += __shfl_xor(S, o);
         }
-        if ((tid & 15) == 0) largest[w] = M, logs[w] = log(S);
+        if (l == 0) {
+            score[w] = s;
+            largest[w] = M;                         // not added up: the log may be lost beside a large logit
+            logs[w] = log(S);
+            state[w] = s > -INFINITY ? ended ? 2 : 1 : 0;
+        }
     }
     if (tid == 0) held = 0;
     __syncthreads();
-    const int w = tid / a.splits, row = b * a.W + w;
-    const bool on = w < a.W && a.scores[min(row, a.B * a.W - 1)] > -INFINITY;
-    const bool done = on && a.done && a.done[row];
-    const double score = on ? (double)a.scores[row] : 0.0;
-    const uint64_t* const list = a.keys + ((long long)b * a.W * a.splits + tid) * a.K;
-    const auto total = [&](uint64_t key) {
-        return Total{ascending(score + ((double)value_of((uint32_t)(key >> 32)) - largest[w] - logs[w])), (uint32_t)w * (uint32_t)a.V + index_of(key)};
+    const auto total = [&](int i, int l, uint64_t key) {
+        const int w = l / a.splits;
+        if (i >= n || state[w] == 0) return Total{0, kNone};
+        if (state[w] == 2)                          // one candidate
+            return i == w * a.splits ? Total{ascending(score[w]), (uint32_t)w * (uint32_t)a.V + (uint32_t)a.eos} : Total{0, kNone};
+        if (!key) return Total{0, kNone};
+        return Total{ascending(score[w] + ((double)value_of((uint32_t)(key >> 32)) - largest[w] - logs[w])),
+                     (uint32_t)w * (uint32_t)a.V + index_of(key)};
     };
-    Total head{0, kNone};
-    if (done) {
-        if (tid % a.splits == 0) head = Total{ascending(score), (uint32_t)w * (uint32_t)a.V + (uint32_t)a.eos};
-    } else if (on && list[0]) {
-        head = total(list[0]);
-    }
+    const Total head = total(tid, list[0], key[0]);
     best[tid] = head.value;
     __syncthreads();
-    const Bound<uint64_t> bd = bound_of(best, (uint64_t)0, a.K, a.K);
+    const Bound<uint64_t> bd = bound_of(best, (uint64_t)0, a.K, 2 * a.K);
     uint32_t last = kNone;
-    if (bd.count > a.K) {
+    if (bd.count > 2 * a.K) {
         first[tid] = head.value == bd.value ? head.at : kNone;
         __syncthreads();
         uint64_t u[4];
@@ -329,45 +421,36 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
         for (int j = 0; j < 4; ++j) u[j] = best[4 * (tid & 63) + j];
         last = index_bound(first, reach(u, bd.value + 1), a.K);
     }
-    // room for the lists that reach the bound: K of K
-    uint64_t* const values = raw;
-    uint32_t* const ats = reinterpret_cast<uint32_t*>(raw + a.K * a.K);
+    uint32_t* const ats = reinterpret_cast<uint32_t*>(values + 2 * a.K * a.K);
     const Total limit{bd.value, last};
     const auto put = [&](const Total& x) {
+        if (!x.value || before(limit, x)) return;
         const int i = atomicAdd(&held, 1);
         values[i] = x.value;
         ats[i] = x.at;
     };
-    if (head.value && !before(limit, head)) {
-        put(head);
-        bool more = !done;
-        for (int k = 1; more && k < a.K; k += 4) {
-            uint64_t key[4];
+    put(head);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) key[j] = k + j < a.K ? list[k + j] : 0;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                if (!more) break;
-                const Total x = key[j] ? total(key[j]) : Total{0, kNone};
-                more = x.value && !before(limit, x);
-                if (more) put(x);
-            }
-        }
-    }
+    for (int j = 1; j < AHEAD; ++j)
+        if (j * kThreads < n) put(total(tid + j * kThreads, list[j], key[j]));
+    for (int i = tid + AHEAD * kThreads; i < n; i += kThreads) put(total(i, i % L, keys[(i % L) * a.K + i / L]));
     __syncthreads();
-    const int n = held;
+    const int c = held;
     const long long to = (long long)b * a.K;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < c; i += kThreads) {
         const Total x{values[i], ats[i]};
-        int r = 0;
-        for (int j = 0; j < n; ++j) r += before(Total{values[j], ats[j]}, x);
+        int r = 0, j = 0;
+        for (; j + 4 <= c; j += 4)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) r += before(Total{values[j + u], ats[j + u]}, x);
+        for (; j < c; ++j) r += before(Total{values[j], ats[j]}, x);
         if (r >= a.K) continue;
         const uint64_t v = x.value >> 63 ? x.value & ~(1ull << 63) : ~x.value;
         a.out_scores[to + r] = (float)__longlong_as_double(v);
         a.parents[to + r] = (int)(x.at / (uint32_t)a.V);
         a.tokens[to + r] = (int)(x.at % (uint32_t)a.V);
     }
-    for (int i = n + tid; i < a.K; i += kThreads) {
+    for (int i = c + tid; i < a.K; i += kThreads) {
         a.out_scores[to + i] = -INFINITY;
         a.parents[to + i] = a.tokens[to + i] = -1;
     }
@@ -418,8 +501,9 @@ __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, in
 
 }  // namespace beam
 
-int beam_splits(int B, int W, int V, int cus) {
-    const long long rows = (long long)B * W, tiles = ((long long)V + 7 + beam::kTile - 1) / beam::kTile;
+int beam_splits(int B, int W, int V, bool f32, int cus) {
+    const int tile = f32 ? beam::kTile<true> : beam::kTile<false>;
+    const long long rows = (long long)B * W, tiles = ((long long)V + 7 + tile - 1) / tile;
     long long n = (8LL * cus + rows - 1) / (rows > 0 ? rows : 1);
     if (n > tiles) n = tiles;
     if (n > beam::kThreads / W) n = beam::kThreads / W;
@@ -429,10 +513,10 @@ int beam_splits(int B, int W, int V, int cus) {
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     using namespace beam;
     if (a.B == 0) return hipSuccess;
-    const unsigned n = (unsigned)(a.B * a.W * a.splits), lds = (unsigned)((3 + 2 * kPer) * a.K * sizeof(uint64_t));
+    const unsigned n = (unsigned)(a.B * a.W * a.splits), lds = (unsigned)(2 * kPieces * a.K * 16 + (3 + 2 * kPer) * a.K * sizeof(uint64_t));
     if (a.f32) hipLaunchKernelGGL(kda_beam_rows<true>, dim3(n), dim3(kThreads), lds, s, a);
     else hipLaunchKernelGGL(kda_beam_rows<false>, dim3(n), dim3(kThreads), lds, s, a);
-    hipLaunchKernelGGL(kda_beam_merge, dim3(a.B), dim3(kThreads), (unsigned)(a.K * a.K * 12), s, a);
+    hipLaunchKernelGGL(kda_beam_merge, dim3(a.B), dim3(kThreads), (unsigned)(2 * a.K * a.K * 12), s, a);
     return hipGetLastError();
 }
 

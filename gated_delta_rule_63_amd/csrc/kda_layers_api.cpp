@@ -237,7 +237,7 @@ kda_status_t kda_beam_select(const void* logits, const float* scores, const uint
     a.logits = logits; a.scores = scores; a.done = done;
     a.out_scores = out_scores; a.parents = parents; a.tokens = tokens;
     a.B = desc->B; a.W = desc->W; a.V = desc->V; a.K = desc->K; a.eos = desc->eos;
-    a.splits = kda::beam_splits(desc->B, desc->W, desc->V, compute_units());
+    a.splits = kda::beam_splits(desc->B, desc->W, desc->V, desc->dtype == KDA_F32, compute_units());
     a.f32 = desc->dtype == KDA_F32;
     char* w = static_cast<char*>(desc->workspace);
     a.parts = reinterpret_cast<kda::BeamPart*>(w);
@@ -247,7 +247,7 @@ kda_status_t kda_beam_select(const void* logits, const float* scores, const uint
 
 size_t kda_beam_workspace_size(const kda_beam_desc_t* desc) {
     if (check_beam(desc) != KDA_OK) return 0;
-    const int splits = kda::beam_splits(desc->B, desc->W, desc->V, compute_units());
+    const int splits = kda::beam_splits(desc->B, desc->W, desc->V, desc->dtype == KDA_F32, compute_units());
     return beam_parts_bytes(desc, splits) + sizeof(uint64_t) * desc->B * desc->W * splits * desc->K;
 }
 

@@ -139,6 +139,11 @@ def test_ties_and_masked_places(kda, V, dtype):
     x, _ = draw(1, 3, V, dtype, 5)
     x[0, 0, V - 1] = x[0, 0, 1] = inf
     check(kda, x, scores, 4)
+    x[0, 1] = inf
+    check(kda, x, scores, 8)
+    x[:] = torch.where(torch.arange(V) % 2 == 0, -0.0, 0.0)       # zeros of either sign tie
+    check(kda, x, scores, 8)
+    x, _ = draw(1, 3, V, dtype, 5)
     lowest = torch.finfo(dt).min
     x[0, 0] = lowest
     x[0, 2, : V - 1] = lowest
