@@ -504,7 +504,7 @@ __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, in
 int beam_splits(int B, int W, int V, bool f32, int cus) {
     const int tile = f32 ? beam::kTile<true> : beam::kTile<false>;
     const long long rows = (long long)B * W, tiles = ((long long)V + 7 + tile - 1) / tile;
-    long long n = (8LL * cus + rows - 1) / (rows > 0 ? rows : 1);
+    long long n = (4LL * cus + rows - 1) / (rows > 0 ? rows : 1);
     if (n > tiles) n = tiles;
     if (n > beam::kThreads / W) n = beam::kThreads / W;
     return (int)(n < 1 ? 1 : n);

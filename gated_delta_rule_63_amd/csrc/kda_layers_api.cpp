@@ -57,7 +57,7 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     a->slots = (int)kda::scan_slots(d->B, d->T, d->num_seqs, cu != nullptr);
     a->f32 = d->dtype == KDA_F32;
     a->leaky = d->leaky != 0;
-    a->split = kda::scan_split(d->T, d->C, d->num_seqs, compute_units());
+    a->width = kda::scan_width(d->T, d->C, d->num_seqs, compute_units());
     return KDA_OK;
 }
 
@@ -72,20 +72,23 @@ size_t scan_bytes(const kda_scan_desc_t* d, bool back, bool with_states) {
     if (check_scan(d) != KDA_OK) return 0;
     const size_t row = up16(4 * (size_t)most_slots(d) * d->C);
     size_t n = back && !with_states ? row : 0;
-    if (kda::scan_split(d->T, d->C, d->num_seqs, compute_units())) n += 3 * row;
+    if (kda::scan_width(d->T, d->C, d->num_seqs, compute_units()) == 0) n += 3 * row;
     return n;
 }
 
-void cut_scan(kda::ScanArgs* a, const kda_scan_desc_t* d, bool own_states) {
+void cut_scan(kda::ScanArgs* a, const kda_scan_desc_t* d, bool back) {
+    const bool own_states = back && !a->states;
     const size_t row = up16(4 * (size_t)most_slots(d) * d->C);
     char* w = static_cast<char*>(d->workspace);
     if (own_states) {
         a->states = reinterpret_cast<float*>(w);
         w += row;
     }
-    if (a->split) {
-        a->sums = reinterpret_cast<float2*>(w);
+    if (a->width == 0) {
+        a->decays = reinterpret_cast<float*>(w);
+        a->adds = reinterpret_cast<float*>(w + row);
         a->grads = reinterpret_cast<float*>(w + 2 * row);
+        if (!back && !a->states) a->states = a->grads;   // which the forward does not have
     }
 }
 
@@ -145,8 +148,8 @@ kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, 
     st = workspace(desc->workspace, desc->workspace_bytes, kda_scan_workspace_size(desc));
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
-    cut_scan(&a, desc, false);
     a.h0 = h0; a.y = y; a.hT = hT; a.states = states;
+    cut_scan(&a, desc, false);
     return status(kda::launch_scan(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -167,11 +170,10 @@ kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqle
     st = workspace(desc->workspace, desc->workspace_bytes, kda_scan_bwd_workspace_size(desc, states != nullptr));
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
-    cut_scan(&a, desc, !states);
-    const bool known = states != nullptr;
-    if (known) a.states = const_cast<float*>(states);
+    a.states = const_cast<float*>(states);
+    cut_scan(&a, desc, true);
     a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dg = dg; a.dh0 = dh0;
-    return status(kda::launch_scan_bwd(a, known, static_cast<hipStream_t>(stream)));
+    return status(kda::launch_scan_bwd(a, states != nullptr, static_cast<hipStream_t>(stream)));
 }
 
 size_t kda_scan_bwd_workspace_size(const kda_scan_desc_t* desc, int32_t with_states) {

@@ -23,12 +23,14 @@ struct ScanArgs {
     void* dx;
     float* dg;
     float* dh0;                   // [N, C], nullptr: not written
-    // workspace, [scan_slots(), C] each: a chunk's decay and what it adds (split form), and the gradient of
-    // the state that leaves each chunk
-    float2* sums;
+    // workspace of the split form, [scan_slots(), C] each: a chunk's decay, what it adds to the state, and
+    // what it adds to the gradient, in whose place the gradient that leaves it is put
+    float* decays;
+    float* adds;
     float* grads;
     int T, C, N, slots;
-    bool f32, leaky, split;
+    bool f32, leaky;
+    int width;                    // scan_width()
 };
 
 struct ScanPoolArgs {
@@ -45,8 +47,9 @@ struct ScanPoolArgs {
 
 // Rows of `states`: one for each chunk of each sequence; packed, sequence n's begin at row cu[n] / 128 + n.
 long long scan_slots(int B, int T, int N, bool packed);
-// Whether the chunks of these chains run side by side (three kernels) instead of one after the other.
-bool scan_split(int T, int C, int N, int cus);
+// How a call runs: channels of a workgroup that goes through a sequence (64, 32, 16), or 0:
+// its chunks side by side, in three kernels.
+int scan_width(int T, int C, int N, int cus);
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 // known: `states` holds the forward's; else it is formed first.

@@ -12,12 +12,14 @@
 // decay, so g = -inf (a reset) is an ordinary value.
 #include "kda_device.h"
 #include "kda_scan.h"
+#include <stdlib.h>
 
 namespace kda {
 namespace scan {
 
 constexpr int L = 16;             // tokens of a wave
 constexpr int S = kScanStrip;
+constexpr int W = 8;              // waves of a workgroup
 
 // A workgroup barrier for what passes through LDS: loads and stores of device
 // memory stay in flight across it.
@@ -39,11 +41,20 @@ __device__ __forceinline__ raw_t<F32> down(float x) {
     else return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
-// A token's decay and the factor of its input, 1 - a: by its series where that
-// would cancel (to g^8 / 8!, 1e-8 of it at -1/2), where a then is 1 + (a - 1).
+// e^g to 1.5 ulp: 2^t by the instruction, times what rounding t = g log2(e) took away.
+// The clamp gives that part a value where t is -inf (e^g = 0).
+__device__ __forceinline__ float decay_of(float g) {
+    const float t = g * 0x1.715476p+0f;
+    const float r = __builtin_amdgcn_fmed3f(fmaf(g, 0x1.4ae0c0p-26f, fmaf(g, 0x1.715476p+0f, -t)), -1.f, 1.f);
+    const float e = __builtin_amdgcn_exp2f(t);
+    return fmaf(e, r * 0x1.62e430p-1f, e);
+}
+
+// A token's decay and the factor of its input: 1, or leaky 1 - a, by its series where
+// the difference would cancel (to g^8 / 8!, 1e-8 of it at -1/2).
 template <bool LEAKY>
 __device__ __forceinline__ void decay(float g, float& a, float& in) {
-    a = expf(g);
+    a = decay_of(g);
     in = 1.f;
     if constexpr (LEAKY) {
         float e = 1.f / 40320.f;
@@ -71,140 +82,408 @@ __device__ __forceinline__ Run sequence(const ScanArgs& a, int n) {
     return Run{t0, (long long)(t0 / kScanChunk) + n, t1 - t0};
 }
 
-// This wave's next L rows of a tensor, zeros behind the run's end (a decay of one that adds nothing).
-template <typename T>
-__device__ __forceinline__ void load(T (&v)[L], const void* p, long long tok, int C, int c, int row, int len) {
-    const T* base = static_cast<const T*>(p) + (tok + row) * C;
-    if (row + L <= len) {
-#pragma unroll
-        for (int i = 0; i < L; ++i) v[i] = (base + (long long)i * C)[c];
-    } else {
-#pragma unroll
-        for (int i = 0; i < L; ++i) v[i] = row + i < len ? (base + (long long)i * C)[c] : T(0);
+// The sequence whose chunks begin at or before this row of the states; 64 of them are looked at a time.
+__device__ __forceinline__ int sequence_of(const ScanArgs& a, long long slot) {
+    if (!a.cu) return (int)(slot / ((a.T + kScanChunk - 1) / kScanChunk));
+    int lo = 0, span = a.N;
+    while (span > 1) {
+        const int step = (span + 63) / 64, off = (threadIdx.x & 63) * step;
+        const bool at = off < span && min(max(a.cu[lo + off], 0), a.T) / kScanChunk + (long long)(lo + off) <= slot;
+        const int k = max(__popcll(__ballot(at)) - 1, 0) * step;
+        lo += k;
+        span = min(step, span - k);
     }
-}
-template <typename T>
-__device__ __forceinline__ void store(const T (&v)[L], void* p, long long tok, int C, int c, int row, int len) {
-    T* base = static_cast<T*>(p) + (tok + row) * C;
-    if (c >= C) return;
-#pragma unroll
-    for (int i = 0; i < L; ++i)
-        if (row + i < len) (base + (long long)i * C)[c] = v[i];
+    return __builtin_amdgcn_readfirstlane(lo);
 }
 
-// One workgroup a (sequence, strip): tiles of W * L tokens one after the other.
-template <bool F32, bool LEAKY, int W>
-__global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
-    __shared__ float2 sh[2][W][S];
-    const int strips = (a.C + S - 1) / S, n = blockIdx.x / strips;
-    const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = (blockIdx.x % strips) * S + l, cc = min(c, a.C - 1);
-    const Run run = sequence(a, n);
-    float h = a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f;
-    raw_t<F32> xr[L];
-    float gr[L];
-    int row = w * L;
-    load(xr, a.x, run.tok, a.C, cc, row, run.len);
-    load(gr, a.g, run.tok, a.C, cc, row, run.len);
-    for (int t = 0; t < run.len; t += W * L, row += W * L) {
+// The place of a thread in a tile of 64 W / SW runs of L tokens by SW channels.
+template <int SW>
+struct Lane {
+    int c;                 // its channel: on where it is below C
+    bool on;
+    int l, sub;            // the channel within the strip, the run
+    int first, off;        // its wave's first row of a tile; elements from there to its own first row and channel
+    __device__ __forceinline__ Lane(const ScanArgs& a, int strip) {
+        l = threadIdx.x % SW;
+        sub = SW == 64 ? __builtin_amdgcn_readfirstlane(threadIdx.x / SW) : threadIdx.x / SW;
+        c = strip * SW + l;
+        on = c < a.C;
+        first = __builtin_amdgcn_readfirstlane(threadIdx.x / 64) * (64 / SW) * L;
+        off = (sub * L - first) * a.C + min(c, a.C - 1);
+    }
+    __device__ __forceinline__ int row(int t) const { return t + sub * L; }
+};
+
+// A thread's L rows of a tensor in the tile from token t on, by offsets from the wave's
+// first row. ALL: they are all there. Else the resource ends with the run, behind which
+// zeros are read (a decay of one that adds nothing) and nothing is written; the
+// bounds are checked on the lane's own offset, so the row's is added there.
+template <bool ALL, typename T, int SW>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* p, const Run& run, int C, const Lane<SW>& q, int t) {
+    const T* base = static_cast<const T*>(p) + (run.tok + t + q.first) * C;
+    const int left = ALL ? 0 : max(run.len - t - q.first, 0);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, ALL ? -1 : (int)(left * (uint32_t)C * sizeof(T)), 0x00020000);
+}
+template <bool ALL, typename T, int SW>
+__device__ __forceinline__ void load(T (&v)[L], const void* p, const Run& run, int C, const Lane<SW>& q, int t) {
+    const __amdgpu_buffer_rsrc_t r = rows<ALL, T>(p, run, C, q, t);
+    const int at = q.off * (int)sizeof(T), step = C * (int)sizeof(T);
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if constexpr (sizeof(T) == 2) v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
+        else v[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, ALL ? at : at + i * step, ALL ? i * step : 0, 0));
+    }
+}
+template <bool ALL, typename T, int SW>
+__device__ __forceinline__ void store(const T (&v)[L], void* p, const Run& run, int C, const Lane<SW>& q, int t) {
+    const __amdgpu_buffer_rsrc_t r = rows<ALL, T>(p, run, C, q, t);
+    const int at = q.off * (int)sizeof(T), step = C * (int)sizeof(T);
+    if (!q.on) return;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(v[i], r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
+    }
+}
+
+// Strips next to each other share lines of memory where they are narrow: workgroups go to
+// the eight dies in turn, so each die takes a run of strips.
+__device__ __forceinline__ int strip_of(int i, int strips) {
+    const int per = strips / 8;
+    return i < per * 8 ? (i % 8) * per + i / 8 : i;
+}
+
+// One tile forwards, from the state h that enters it to the one that leaves it.
+template <bool ALL, bool F32, bool LEAKY, int SW>
+struct Tile {
+    static constexpr int NS = 64 * W / SW;
+    raw_t<F32> x[L];
+    float g[L];
+    __device__ __forceinline__ void get(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t) {
+        load<ALL>(x, a.x, run, a.C, p, t);
+        load<ALL>(g, a.g, run, a.C, p, t);
+    }
+    // what becomes of x and g; `next` is fetched meanwhile
+    template <typename N>
+    __device__ __forceinline__ float run(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t, float h, float2 (*s)[SW], const N& next) {
         float d[L], b[L];
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             float in;
-            decay<LEAKY>(gr[i], d[i], in);
-            b[i] = up(xr[i]) * in;
+            decay<LEAKY>(g[i], d[i], in);
+            b[i] = up(x[i]) * in;
         }
-        load(xr, a.x, run.tok, a.C, cc, row + W * L, run.len);
-        load(gr, a.g, run.tok, a.C, cc, row + W * L, run.len);
+        next();
         float A = 1.f, B = 0.f;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             A *= d[i];
             B = fmaf(d[i], B, b[i]);
         }
-        float2(&s)[W][S] = sh[(t / (W * L)) & 1];
-        s[w][l] = make_float2(A, B);
+        s[p.sub][p.l] = make_float2(A, B);
         lds_barrier();
         float in = h;
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-            const float2 p = s[j][l];
-            if (j == w) in = h;
-            h = fmaf(p.x, h, p.y);
+        for (int j = 0; j < NS; ++j) {
+            const float2 m = s[j][p.l];
+            if (j == p.sub) in = h;
+            h = fmaf(m.x, h, m.y);
         }
-        if (a.states && row % kScanChunk == 0 && row < run.len && c < a.C)
-            a.states[(run.slot + row / kScanChunk) * a.C + c] = in;
-        raw_t<F32> yr[L];
+        const int row = p.row(t);
+        if (a.states && row % kScanChunk == 0 && row < run.len && p.on)
+            a.states[(run.slot + row / kScanChunk) * a.C + p.c] = in;
+        if (a.y) {
+            raw_t<F32> y[L];
 #pragma unroll
-        for (int i = 0; i < L; ++i) {
-            in = fmaf(d[i], in, b[i]);
-            yr[i] = down<F32>(in);
+            for (int i = 0; i < L; ++i) {
+                in = fmaf(d[i], in, b[i]);
+                y[i] = down<F32>(in);
+            }
+            store<ALL>(y, a.y, run, a.C, p, t);
         }
-        if (a.y) store(yr, a.y, run.tok, a.C, c, row, run.len);
+        return h;
     }
-    if (a.hT && w == 0 && c < a.C) a.hT[(long long)n * a.C + c] = h;
+};
+
+// One workgroup a (sequence, strip): tiles of W * L tokens one after the other, the next
+// one's rows fetched while one is worked on.
+template <bool F32, bool LEAKY, int SW>
+__global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
+    constexpr int NS = 64 * W / SW, TILE = NS * L;
+    __shared__ float2 sh[2][NS][SW];
+    const int strips = (a.C + SW - 1) / SW, n = blockIdx.x / strips;
+    const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
+    const int cc = min(p.c, a.C - 1);
+    const Run run = sequence(a, n);
+    float h = a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f;
+    const int whole = run.len / TILE;
+    int t = 0;
+    if (whole > 0) {
+        Tile<true, F32, LEAKY, SW> tile;
+        tile.get(a, run, p, 0);
+        for (int k = 0; k < whole; ++k, t += TILE)
+            h = tile.run(a, run, p, t, h, sh[k & 1], [&] {
+                if (k + 1 < whole) tile.get(a, run, p, t + TILE);
+            });
+    }
+    if (t < run.len) {
+        Tile<false, F32, LEAKY, SW> tile;
+        tile.get(a, run, p, t);
+        h = tile.run(a, run, p, t, h, sh[whole & 1], [] {});
+    }
+    if (a.hT && p.sub == 0 && p.on) a.hT[(long long)n * a.C + p.c] = h;
 }
 
-// The gradient, tiles from the last to the first, each from the kept state that enters it.
-template <bool F32, bool LEAKY, int W>
-__global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
-    __shared__ float2 sh[2][W][S];
-    __shared__ float sd[2][W][S];
-    const int strips = (a.C + S - 1) / S, n = blockIdx.x / strips;
-    const int l = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = (blockIdx.x % strips) * S + l, cc = min(c, a.C - 1);
-    const Run run = sequence(a, n);
-    float D = a.dhT ? a.dhT[(long long)n * a.C + cc] : 0.f;
-    raw_t<F32> xr[L], dyr[L];
-    float gr[L];
-    constexpr int TILE = W * L;
-    int t = (run.len - 1) / TILE * TILE;
-    for (int k = 0; run.len > 0 && t >= 0; t -= TILE, ++k) {
-        const int row = t + w * L;
-        load(xr, a.x, run.tok, a.C, cc, row, run.len);
-        load(gr, a.g, run.tok, a.C, cc, row, run.len);
-        load(dyr, a.dy, run.tok, a.C, cc, row, run.len);
-        float h = a.states[(run.slot + t / kScanChunk) * a.C + cc];
-        float d[L], in[L], A = 1.f, B = 0.f, E = 0.f;
+// One tile backwards, from the gradient D that enters it from behind and the state h
+// that entered it to the gradient that leaves it.
+template <bool ALL, bool F32, bool LEAKY, int SW>
+struct TileBwd {
+    static constexpr int NS = 64 * W / SW;
+    raw_t<F32> x[L], dy[L];
+    float g[L];
+    __device__ __forceinline__ void get(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t) {
+        load<ALL>(x, a.x, run, a.C, p, t);
+        load<ALL>(g, a.g, run, a.C, p, t);
+        load<ALL>(dy, a.dy, run, a.C, p, t);
+    }
+    template <typename N>
+    __device__ __forceinline__ float run(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t, float h, float D,
+                                         float2 (*s)[SW], float (*sd)[SW], const N& next) {
+        float d[L], in[L], v[L], u[L], A = 1.f, B = 0.f, E = 0.f;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            decay<LEAKY>(gr[i], d[i], in[i]);
+            decay<LEAKY>(g[i], d[i], in[i]);
+            v[i] = up(x[i]);
+            u[i] = up(dy[i]);
+        }
+        next();
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
             A *= d[i];
-            B = fmaf(d[i], B, up(xr[i]) * in[i]);
+            B = fmaf(d[i], B, v[i] * in[i]);
         }
 #pragma unroll
-        for (int i = L - 1; i >= 0; --i) E = d[i] * (up(dyr[i]) + E);
-        sh[k & 1][w][l] = make_float2(A, B);
-        sd[k & 1][w][l] = E;
+        for (int i = L - 1; i >= 0; --i) E = d[i] * (u[i] + E);
+        s[p.sub][p.l] = make_float2(A, B);
+        sd[p.sub][p.l] = E;
         lds_barrier();
-        float Din = D;
+        float into = D;
 #pragma unroll
-        for (int j = W - 1; j >= 0; --j) {
-            if (j == w) Din = D;
-            D = fmaf(sh[k & 1][j][l].x, D, sd[k & 1][j][l]);
+        for (int j = NS - 1; j >= 0; --j) {
+            const float2 m = s[j][p.l];
+            if (j == p.sub) into = D;
+            D = fmaf(m.x, D, sd[j][p.l]);
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j)
-            if (j < w) h = fmaf(sh[k & 1][j][l].x, h, sh[k & 1][j][l].y);
-        float p[L];
-        raw_t<F32> dxr[L];
+        for (int j = 0; j < NS; ++j)
+            if (j < p.sub) {
+                const float2 m = s[j][p.l];
+                h = fmaf(m.x, h, m.y);
+            }
 #pragma unroll
         for (int i = 0; i < L; ++i) {
-            const float x = up(xr[i]);
-            p[i] = d[i] * (LEAKY ? h - x : h);
-            h = fmaf(d[i], h, x * in[i]);
+            const float b = v[i] * in[i];
+            v[i] = d[i] * (LEAKY ? h - v[i] : h);
+            h = fmaf(d[i], h, b);
         }
+        raw_t<F32> dx[L];
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) {
-            const float dd = up(dyr[i]) + Din;
-            dxr[i] = down<F32>(dd * in[i]);
-            p[i] *= dd;
-            Din = d[i] * dd;
+            const float dd = u[i] + into;
+            dx[i] = down<F32>(dd * in[i]);
+            v[i] *= dd;
+            into = d[i] * dd;
         }
-        store(dxr, a.dx, run.tok, a.C, c, row, run.len);
-        store(p, a.dg, run.tok, a.C, c, row, run.len);
+        store<ALL>(dx, a.dx, run, a.C, p, t);
+        store<ALL>(v, a.dg, run, a.C, p, t);
+        return D;
     }
-    if (a.dh0 && w == 0 && c < a.C) a.dh0[(long long)n * a.C + c] = D;
+};
+
+// The gradient, tiles from the last to the first, each from the kept state that enters it.
+template <bool F32, bool LEAKY, int SW>
+__global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
+    constexpr int NS = 64 * W / SW, TILE = NS * L;
+    __shared__ float2 sh[2][NS][SW];
+    __shared__ float sd[2][NS][SW];
+    const int strips = (a.C + SW - 1) / SW, n = blockIdx.x / strips;
+    const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
+    const int cc = min(p.c, a.C - 1);
+    const Run run = sequence(a, n);
+    const auto state = [&](int t) { return a.states[(run.slot + t / kScanChunk) * a.C + cc]; };
+    float D = a.dhT ? a.dhT[(long long)n * a.C + cc] : 0.f;
+    const int whole = run.len / TILE;
+    if (whole * TILE < run.len) {
+        TileBwd<false, F32, LEAKY, SW> tile;
+        tile.get(a, run, p, whole * TILE);
+        D = tile.run(a, run, p, whole * TILE, state(whole * TILE), D, sh[whole & 1], sd[whole & 1], [] {});
+    }
+    if (whole > 0) {
+        TileBwd<true, F32, LEAKY, SW> tile;
+        tile.get(a, run, p, (whole - 1) * TILE);
+        float next = state((whole - 1) * TILE);
+        for (int k = whole - 1; k >= 0; --k) {
+            const float h = next;
+            D = tile.run(a, run, p, k * TILE, h, D, sh[k & 1], sd[k & 1], [&] {
+                if (k == 0) return;
+                tile.get(a, run, p, (k - 1) * TILE);
+                next = state((k - 1) * TILE);
+            });
+        }
+    }
+    if (a.dh0 && p.sub == 0 && p.on) a.dh0[(long long)n * a.C + p.c] = D;
+}
+
+// ------------------------------------------------------------- chunks side by side
+static_assert(W * L == kScanChunk, "a tile of 64 channels is a chunk");
+
+// A chunk's decay and what it adds to the state (FWD) and to the gradient (BWD).
+template <bool F32, bool LEAKY, bool FWD, bool BWD>
+__global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
+    __shared__ float2 sh[W][S];
+    __shared__ float sd[W][S];
+    const int strips = (a.C + S - 1) / S;
+    const long long slot = blockIdx.x / strips;
+    const Lane<S> p(a, blockIdx.x % strips);
+    const Run run = sequence(a, sequence_of(a, slot));
+    const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
+    if (slot < run.slot || t >= run.len) return;   // no chunk
+    raw_t<F32> x[L], dy[L];
+    float g[L];
+    load<false>(g, a.g, run, a.C, p, t);
+    if constexpr (FWD) load<false>(x, a.x, run, a.C, p, t);
+    if constexpr (BWD) load<false>(dy, a.dy, run, a.C, p, t);
+    float d[L], A = 1.f, B = 0.f, E = 0.f;
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+        float in;
+        decay<LEAKY>(g[i], d[i], in);
+        A *= d[i];
+        if constexpr (FWD) B = fmaf(d[i], B, up(x[i]) * in);
+    }
+    if constexpr (BWD)
+#pragma unroll
+        for (int i = L - 1; i >= 0; --i) E = d[i] * (up(dy[i]) + E);
+    sh[p.sub][p.l] = make_float2(A, B);
+    sd[p.sub][p.l] = E;
+    lds_barrier();
+    if (p.sub > 0 || !p.on) return;
+    A = 1.f, B = 0.f, E = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        const float2 m = sh[j][p.l];
+        A *= m.x;
+        B = fmaf(m.x, B, m.y);
+    }
+#pragma unroll
+    for (int j = W - 1; j >= 0; --j) E = fmaf(sh[j][p.l].x, E, sd[j][p.l]);
+    const long long at = slot * a.C + p.c;
+    a.decays[at] = A;
+    if constexpr (FWD) a.adds[at] = B;
+    if constexpr (BWD) a.grads[at] = E;
+}
+
+// From a sequence's chunks in order to the states that enter them, and in reverse to the
+// gradients that leave them: the same fold, of chunks instead of tokens.
+constexpr int SC = 16, NC = 1024 / SC;   // its channels and runs of L chunks
+template <bool BACK>
+__device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, float2 (*sh)[NC][SC]) {
+    const int l = threadIdx.x % SC, sub = threadIdx.x / SC, c = strip * SC + l, cc = min(c, a.C - 1);
+    const Run run = sequence(a, n);
+    const int chunks = (run.len + kScanChunk - 1) / kScanChunk;
+    const float* from = BACK ? a.grads : a.adds;
+    float* to = BACK ? a.grads : a.states;
+    const float* start = BACK ? a.dhT : a.h0;
+    float* end = BACK ? a.dh0 : a.hT;
+    float h = start ? start[(long long)n * a.C + cc] : 0.f;
+    const auto place = [&](int r) { return (run.slot + (BACK ? chunks - 1 - r : r)) * a.C + cc; };
+    for (int t = 0, k = 0; t < chunks; t += NC * L, ++k) {
+        const int row = t + sub * L;
+        float d[L], b[L], A = 1.f, B = 0.f;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            d[i] = row + i < chunks ? a.decays[place(row + i)] : 1.f;
+            b[i] = row + i < chunks ? from[place(row + i)] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            A *= d[i];
+            B = fmaf(d[i], B, b[i]);
+        }
+        sh[k & 1][sub][l] = make_float2(A, B);
+        lds_barrier();
+        float in = h;
+#pragma unroll 16
+        for (int j = 0; j < NC; ++j) {
+            const float2 m = sh[k & 1][j][l];
+            if (j == sub) in = h;
+            h = fmaf(m.x, h, m.y);
+        }
+        if (c < a.C)
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (row + i < chunks) {
+                    to[place(row + i)] = in;
+                    in = fmaf(d[i], in, b[i]);
+                }
+    }
+    if (end && sub == 0 && c < a.C) end[(long long)n * a.C + c] = h;
+}
+
+template <bool FWD, bool BWD>
+__global__ __launch_bounds__(1024) void kda_scan_combine(ScanArgs a) {
+    __shared__ float2 sh[2][NC][SC];
+    const int strips = (a.C + SC - 1) / SC, both = a.N * strips;
+    const int i = blockIdx.x < both ? blockIdx.x : blockIdx.x - both;
+    if (FWD && (!BWD || blockIdx.x < both)) combine<false>(a, i / strips, i % strips, sh);
+    else combine<true>(a, i / strips, i % strips, sh);
+}
+
+// A chunk from the state that enters it.
+template <bool F32, bool LEAKY>
+__global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
+    __shared__ float2 sh[W][S];
+    const int strips = (a.C + S - 1) / S;
+    const long long slot = blockIdx.x / strips;
+    const Lane<S> p(a, blockIdx.x % strips);
+    const int cc = min(p.c, a.C - 1);
+    const Run run = sequence(a, sequence_of(a, slot));
+    const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
+    if (slot < run.slot || t >= run.len) return;
+    const float h = a.states[slot * a.C + cc];
+    a.states = nullptr;                            // they are there
+    if (t + kScanChunk <= run.len) {
+        Tile<true, F32, LEAKY, S> tile;
+        tile.get(a, run, p, t);
+        tile.run(a, run, p, t, h, sh, [] {});
+    } else {
+        Tile<false, F32, LEAKY, S> tile;
+        tile.get(a, run, p, t);
+        tile.run(a, run, p, t, h, sh, [] {});
+    }
+}
+
+template <bool F32, bool LEAKY>
+__global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a) {
+    __shared__ float2 sh[W][S];
+    __shared__ float sd[W][S];
+    const int strips = (a.C + S - 1) / S;
+    const long long slot = blockIdx.x / strips;
+    const Lane<S> p(a, blockIdx.x % strips);
+    const int cc = min(p.c, a.C - 1);
+    const Run run = sequence(a, sequence_of(a, slot));
+    const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
+    if (slot < run.slot || t >= run.len) return;
+    const float h = a.states[slot * a.C + cc], D = a.grads[slot * a.C + cc];
+    if (t + kScanChunk <= run.len) {
+        TileBwd<true, F32, LEAKY, S> tile;
+        tile.get(a, run, p, t);
+        tile.run(a, run, p, t, h, D, sh, sd, [] {});
+    } else {
+        TileBwd<false, F32, LEAKY, S> tile;
+        tile.get(a, run, p, t);
+        tile.run(a, run, p, t, h, D, sh, sd, [] {});
+    }
 }
 
 // ------------------------------------------------------------ token by token
@@ -241,29 +520,64 @@ long long scan_slots(int B, int T, int N, bool packed) {
     return packed ? (long long)T / kScanChunk + N : (long long)B * ((T + (long long)kScanChunk - 1) / kScanChunk);
 }
 
-bool scan_split(int, int, int, int) { return false; }
+int scan_width(int T, int C, int N, int cus) {
+    const long long strips = (C + scan::S - 1) / scan::S;
+    const char* e = getenv("SPLIT");
+    if (e) return atoi(e);
+    return N * strips * 2 < cus && T > 8 * kScanChunk ? 0 : 64;
+}
+
+#define KDA_SCAN_LAUNCH(kernel, n, threads) hipLaunchKernelGGL((kernel), dim3((unsigned)(n)), dim3(threads), 0, s, a)
 
 template <bool F32, bool LEAKY>
-static hipError_t walk(const ScanArgs& a, hipStream_t s, bool back) {
+static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
     using namespace scan;
-    const unsigned n = (unsigned)((long long)a.N * ((a.C + S - 1) / S));
-    if (back) hipLaunchKernelGGL((kda_scan_walk_bwd<F32, LEAKY, 16>), dim3(n), dim3(1024), 0, s, a);
-    else hipLaunchKernelGGL((kda_scan_walk<F32, LEAKY, 16>), dim3(n), dim3(1024), 0, s, a);
+    const long long strips = (a.C + S - 1) / S, chunks = a.slots * strips;
+    if (a.width > 0) {
+        if (a.width == 64) KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 64>), a.N * strips, 64 * W);
+        else if (a.width == 32) KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 32>), a.N * ((a.C + 31LL) / 32), 64 * W);
+        else KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
+        return hipGetLastError();
+    }
+    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks, 64 * W);
+    KDA_SCAN_LAUNCH((kda_scan_combine<true, false>), a.N * ((a.C + SC - 1) / SC), 1024);
+    if (chunks > 0 && a.y) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY>), chunks, 64 * W);
+    return hipGetLastError();
+}
+
+template <bool F32, bool LEAKY>
+static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
+    using namespace scan;
+    const long long strips = (a.C + S - 1) / S, chunks = a.slots * strips;
+    if (a.width > 0) {
+        if (!known) {
+            const hipError_t e = scan_fwd<F32, LEAKY>(a, s);   // y is not there: states only
+            if (e != hipSuccess) return e;
+        }
+        if (a.width == 64) KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 64>), a.N * strips, 64 * W);
+        else if (a.width == 32) KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 32>), a.N * ((a.C + 31LL) / 32), 64 * W);
+        else KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
+        return hipGetLastError();
+    }
+    if (known) {
+        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, false, true>), chunks, 64 * W);
+        KDA_SCAN_LAUNCH((kda_scan_combine<false, true>), a.N * ((a.C + SC - 1) / SC), 1024);
+    } else {
+        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, true>), chunks, 64 * W);
+        KDA_SCAN_LAUNCH((kda_scan_combine<true, true>), 2 * a.N * ((a.C + SC - 1) / SC), 1024);
+    }
+    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks_bwd<F32, LEAKY>), chunks, 64 * W);
     return hipGetLastError();
 }
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
-    if (a.f32) return a.leaky ? walk<true, true>(a, s, false) : walk<true, false>(a, s, false);
-    return a.leaky ? walk<false, true>(a, s, false) : walk<false, false>(a, s, false);
+    if (a.f32) return a.leaky ? scan_fwd<true, true>(a, s) : scan_fwd<true, false>(a, s);
+    return a.leaky ? scan_fwd<false, true>(a, s) : scan_fwd<false, false>(a, s);
 }
 
 hipError_t launch_scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
-    if (!known) {
-        const hipError_t e = launch_scan(a, s);   // y is not there: states only
-        if (e != hipSuccess) return e;
-    }
-    if (a.f32) return a.leaky ? walk<true, true>(a, s, true) : walk<true, false>(a, s, true);
-    return a.leaky ? walk<false, true>(a, s, true) : walk<false, false>(a, s, true);
+    if (a.f32) return a.leaky ? scan_bwd<true, true>(a, known, s) : scan_bwd<true, false>(a, known, s);
+    return a.leaky ? scan_bwd<false, true>(a, known, s) : scan_bwd<false, false>(a, known, s);
 }
 
 template <bool F32, bool BF16>
