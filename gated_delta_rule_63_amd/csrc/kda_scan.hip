@@ -12,7 +12,6 @@
 // decay, so g = -inf (a reset) is an ordinary value.
 #include "kda_device.h"
 #include "kda_scan.h"
-#include <stdlib.h>
 
 namespace kda {
 namespace scan {
@@ -80,6 +79,20 @@ __device__ __forceinline__ Run sequence(const ScanArgs& a, int n) {
     if (!a.cu) return Run{(long long)n * a.T, (long long)n * ((a.T + kScanChunk - 1) / kScanChunk), a.T};
     const int t0 = min(max(a.cu[n], 0), a.T), t1 = min(max(a.cu[n + 1], t0), a.T);
     return Run{t0, (long long)(t0 / kScanChunk) + n, t1 - t0};
+}
+
+// Packed sequences go longest first, so that the last workgroups to start are short: the
+// one of rank i (up to 64 sequences, one a lane).
+__device__ __forceinline__ int by_length(const ScanArgs& a, int i) {
+    if (!a.cu || a.N > 64 || a.N < 2) return i;
+    const int n = threadIdx.x & 63;
+    const int len = n < a.N ? sequence(a, n).len : -1;
+    int rank = 0;
+    for (int j = 0; j < a.N; ++j) {
+        const int other = __builtin_amdgcn_readlane(len, j);
+        rank += other > len || (other == len && j < n);
+    }
+    return __builtin_ctzll(__ballot(rank == i && n < a.N));
 }
 
 // The sequence whose chunks begin at or before this row of the states; 64 of them are looked at a time.
@@ -211,7 +224,7 @@ template <bool F32, bool LEAKY, int SW>
 __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
     constexpr int NS = 64 * W / SW, TILE = NS * L;
     __shared__ float2 sh[2][NS][SW];
-    const int strips = (a.C + SW - 1) / SW, n = blockIdx.x / strips;
+    const int strips = (a.C + SW - 1) / SW, n = by_length(a, blockIdx.x / strips);
     const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, n);
@@ -306,7 +319,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
     constexpr int NS = 64 * W / SW, TILE = NS * L;
     __shared__ float2 sh[2][NS][SW];
     __shared__ float sd[2][NS][SW];
-    const int strips = (a.C + SW - 1) / SW, n = blockIdx.x / strips;
+    const int strips = (a.C + SW - 1) / SW, n = by_length(a, blockIdx.x / strips);
     const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, n);
@@ -520,11 +533,21 @@ long long scan_slots(int B, int T, int N, bool packed) {
     return packed ? (long long)T / kScanChunk + N : (long long)B * ((T + (long long)kScanChunk - 1) / kScanChunk);
 }
 
-int scan_width(int T, int C, int N, int cus) {
-    const long long strips = (C + scan::S - 1) / scan::S;
-    const char* e = getenv("SPLIT");
-    if (e) return atoi(e);
-    return N * strips * 2 < cus && T > 8 * kScanChunk ? 0 : 64;
+// A workgroup goes through 1000 tokens in 14, 8 or 5 us with 64, 32 or 16 channels (the
+// gradient: 28, 15, 9), as long as memory keeps up; the narrower ones move 90 to 75% as
+// many bytes a second where all are at work (T = 8192, bf16, forwards: C = 12288 163, 207, 217
+// us; C = 8192 142, 113, 141; 131072 x 4096 1990, 1302, 1065, and 1396 with the chunks side
+// by side). So: the widest that occupies five compute units in eight. With fewer chains
+// than that, chunks side by side cost three launches and read their inputs twice, but
+// fill the chip: 131072 x 512 889 us (16 channels) against 192, 8192 x 2048 62 against 46,
+// 4096 x 256 22 against 20; the gradient 1688 against 268 and 38 against 24.
+int scan_width(int T, int C, int N, bool back, int cus) {
+    const auto groups = [&](int width) { return (long long)N * ((C + width - 1) / width); };
+    if (8 * groups(64) >= 5LL * cus) return 64;
+    if (8 * groups(32) >= 5LL * cus) return 32;
+    const long long len = N > 1 ? 2LL * T / N : T;     // (packed sequences: a guess at the longest)
+    if (len <= (back ? 2048 : 4096)) return 16;
+    return 8 * groups(16) >= 6LL * cus && (!back || len <= 16384) ? 16 : 0;
 }
 
 #define KDA_SCAN_LAUNCH(kernel, n, threads) hipLaunchKernelGGL((kernel), dim3((unsigned)(n)), dim3(threads), 0, s, a)
