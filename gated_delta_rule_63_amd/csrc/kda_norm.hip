@@ -15,139 +15,351 @@ namespace norm {
 
 constexpr float kLeast = 0x1p-40f, kE4M3Max = 448.f;
 
-template <bool F32>
-__device__ __forceinline__ float get(const void* p, long long i) { return ld_in<F32>(p, i); }
-template <bool F32>
-__device__ __forceinline__ void put(void* p, long long i, float x) {
-    if constexpr (F32) static_cast<float*>(p)[i] = x;
-    else static_cast<__bf16*>(p)[i] = (__bf16)x;
+// A row on `wpr` waves of a workgroup, E values a lane: as pieces of V neighbours (V = 8,
+// 16 bytes of bf16, or 1 for rows of other sizes and tensors that start elsewhere). It is
+// reached through a buffer resource that ends with it (or holds nothing: a row that is
+// not there), so lanes beyond it read zeros and write nothing.
+template <int E, int V>
+struct Place {
+    int C, lane, lanes;                // of the row
+    long long at;                      // its first value
+    bool on;
+    __device__ __forceinline__ int col(int u) const { return (u * lanes + lane) * V; }
+    __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(const void* p, int size) const {
+        return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p)) + at * size, (short)0, on ? C * size : 0, 0x00020000);
+    }
+};
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <bool F32, int E, int V>
+struct Raw {                           // as it is in memory
+    static constexpr int N = E / V, W = V == 8 ? (F32 ? 8 : 4) : 1;
+    uint32_t w[N][W];
+    __device__ __forceinline__ float operator[](int e) const {
+        const int u = e / V, i = e % V;
+        if constexpr (F32) return __uint_as_float(w[u][i]);
+        else if constexpr (V == 8) return __uint_as_float(i & 1 ? w[u][i / 2] & 0xffff0000u : w[u][i / 2] << 16);
+        else return __uint_as_float(w[u][0] << 16);
+    }
+};
+template <bool F32, int E, int V>
+__device__ __forceinline__ void get(Raw<F32, E, V>& r, const void* p, const Place<E, V>& at) {
+    const __amdgpu_buffer_rsrc_t b = at.row(p, F32 ? 4 : 2);
+#pragma unroll
+    for (int u = 0; u < E / V; ++u) {
+        const int o = at.col(u) * (F32 ? 4 : 2);
+        if constexpr (V == 8) {
+#pragma unroll
+            for (int i = 0; i < (F32 ? 2 : 1); ++i) {
+                const u32x4 q = __builtin_amdgcn_raw_buffer_load_b128(b, o + 16 * i, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r.w[u][4 * i + j] = q[j];
+            }
+        } else if constexpr (F32) {
+            r.w[u][0] = __builtin_amdgcn_raw_buffer_load_b32(b, o, 0, 0);
+        } else {
+            r.w[u][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, o, 0, 0);
+        }
+    }
 }
+template <bool F32, int E, int V>
+__device__ __forceinline__ void put(void* p, const float (&x)[E], const Place<E, V>& at) {
+    const __amdgpu_buffer_rsrc_t b = at.row(p, F32 ? 4 : 2);
+#pragma unroll
+    for (int u = 0; u < E / V; ++u) {
+        const int o = at.col(u) * (F32 ? 4 : 2);
+        const float* v = x + u * V;
+        if constexpr (F32 && V == 8) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                u32x4 q;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) q[j] = __float_as_uint(v[4 * i + j]);
+                __builtin_amdgcn_raw_buffer_store_b128(q, b, o + 16 * i, 0, 0);
+            }
+        } else if constexpr (V == 8) {
+            u32x4 q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) q[j] = __builtin_bit_cast(uint32_t, bf16x2{(__bf16)v[2 * j], (__bf16)v[2 * j + 1]});
+            __builtin_amdgcn_raw_buffer_store_b128(q, b, o, 0, 0);
+        } else if constexpr (F32) {
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[0]), b, o, 0, 0);
+        } else {
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, (__bf16)v[0]), b, o, 0, 0);
+        }
+    }
+}
+
+template <bool MAX>
+__device__ __forceinline__ float join(float x, float y) { return MAX ? fmaxf(x, y) : x + y; }
+// Over 16 lanes, in the last of them; over a wave, in every lane. (Sums and largest values
+// of nothing negative: lanes that a step has nothing for add zero.)
+template <bool MAX>
+__device__ __forceinline__ float to_last16(float x) {
+#define KDA_STEP(ctrl, rows) x = join<MAX>(x, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), ctrl, rows, 0xf, false)))
+    KDA_STEP(0x111, 0xf);      // from 1, 2, 4 and 8 lanes below within 16
+    KDA_STEP(0x112, 0xf);
+    KDA_STEP(0x114, 0xf);
+    KDA_STEP(0x118, 0xf);
+    return x;
+}
+template <bool MAX>
+__device__ __forceinline__ float over_wave(float x) {
+    x = to_last16<MAX>(x);
+    KDA_STEP(0x142, 0xa);      // from the last lane of the 16, and of the 32, below
+    KDA_STEP(0x143, 0xc);
+#undef KDA_STEP
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), 63));
+}
+
+// A workgroup barrier for what passes through LDS: loads and stores of device
+// memory stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// N values over the row's waves, in a fixed order. s: a place for each wave, that is not
+// used again before another barrier.
+template <bool MAX, int N>
+__device__ __forceinline__ void over_row(float (&x)[N], float (*s)[N], int wpr) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = over_wave<MAX>(x[i]);
+    if (wpr == 1) return;
+    const int w = threadIdx.x >> 6, l = threadIdx.x & 63;
+    if (l == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[w][i] = x[i];
+    lds_barrier();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float part = l < wpr ? s[w / wpr * wpr + l][i] : 0.f;
+        x[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(to_last16<MAX>(part)), 15));
+    }
+}
+
 template <bool F32>
 __device__ __forceinline__ float rounded(float x) {
     if constexpr (F32) return x;
     else return (float)(__bf16)x;
 }
 
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x += __shfl_xor(x, o);
-    return x;
-}
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) x = fmaxf(x, __shfl_xor(x, o));
-    return x;
-}
-// over the 256 lanes of a workgroup, the same order for every lane
-template <bool MAX>
-__device__ __forceinline__ float all(float x, float* s) {
-    x = MAX ? wave_max(x) : wave_sum(x);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) s[threadIdx.x >> 6] = x;
-    __syncthreads();
-    return MAX ? fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3])) : (s[0] + s[1]) + (s[2] + s[3]);
-}
-
-__device__ __forceinline__ uint8_t to_e4m3(float x) {
-    return (uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(x, x, 0, false) & 0xff);
-}
-
-// One workgroup a row; the row is read again (from the caches) for each step.
-template <bool F32, bool RF32>
-__global__ __launch_bounds__(256) void kda_add_norm_kernel(NormArgs a) {
-    __shared__ float s[4];
-    const long long at = (long long)blockIdx.x * a.C;
-    const auto sum = [&](int c) {
-        const float x = get<F32>(a.x, at + c);
-        return a.res ? rounded<RF32>(x + get<RF32>(a.res, at + c)) : x;
+// Rows in turn, the next one fetched while one is worked on; the weight stays in registers.
+template <bool F32, bool RF32, int E, int V>
+__global__ __launch_bounds__(1024) void kda_add_norm_kernel(NormArgs a, int wpr) {
+    __shared__ float s[2][2][16][1];
+    const int groups = (blockDim.x >> 6) / wpr, g = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / wpr;
+    Place<E, V> at{a.C, (int)threadIdx.x - g * wpr * 64, wpr * 64, 0, true};
+    Raw<true, E, V> w;
+    get(w, a.weight, at);
+    Raw<F32, E, V> x;
+    Raw<RF32, E, V> res;
+    const auto fetch = [&](long long row) {
+        at.at = row * a.C;
+        at.on = row < a.rows;
+        get(x, a.x, at);
+        if (a.res) get(res, a.res, at);
     };
-    float ss = 0.f;
-    for (int c = threadIdx.x; c < a.C; c += 256) {
-        const float r = sum(c);
-        ss += r * r;
-    }
-    const float k = 1.f / sqrtf(all<false>(ss, s) / a.C + a.eps);
-    if (!a.q8) {
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float r = sum(c);
-            if (a.res) put<RF32>(a.r, at + c, r);
-            put<F32>(a.y, at + c, r * k * a.weight[c]);
+    const long long step = (long long)gridDim.x * groups;
+    long long row = (long long)blockIdx.x * groups + g;
+    fetch(row);
+    int turn = 0;
+    for (long long first = (long long)blockIdx.x * groups; first < a.rows; first += step, row += step, turn ^= 1) {
+        float r[E], ss[1] = {0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            r[e] = a.res ? rounded<RF32>(x[e] + res[e]) : x[e];
+            ss[0] += r[e] * r[e];
         }
-        return;
+        if (first + step < a.rows) fetch(row + step);
+        over_row<false>(ss, s[turn][0], wpr);
+        const float k = 1.f / sqrtf(ss[0] / a.C + a.eps);
+        at.at = row * a.C;
+        at.on = row < a.rows;
+        if (a.res) put<RF32>(a.r, r, at);
+#pragma unroll
+        for (int e = 0; e < E; ++e) r[e] = r[e] * k * w[e];
+        if (!a.q8) {
+            put<F32>(a.y, r, at);
+            continue;
+        }
+        float scale = 0.f;
+        if (a.group == 0) {
+            float m[1] = {0.f};
+#pragma unroll
+            for (int e = 0; e < E; ++e) m[0] = fmaxf(m[0], fabsf(r[e]));
+            over_row<true>(m, s[turn][1], wpr);
+            scale = fmaxf(m[0], kLeast) / kE4M3Max;
+            if (at.on && at.lane == 0) a.scales[row] = scale;
+        }
+        const __amdgpu_buffer_rsrc_t q = at.row(a.y, 1);
+#pragma unroll
+        for (int u = 0; u < E / V; ++u) {
+            const int c = at.col(u);
+            if (V == 8 && a.group) {                // 16 lanes hold a group
+                float m = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) m = fmaxf(m, fabsf(r[u * V + i]));
+                m = __shfl(to_last16<true>(m), (threadIdx.x & 63) | 15);
+                scale = fmaxf(m, kLeast) / kE4M3Max;
+                if (at.on && c < a.C && (threadIdx.x & 15) == 0) a.scales[row * (a.C / 128) + c / 128] = scale;
+            }
+            if constexpr (V == 8) {
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                u32x2 w8;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float* v = r + u * V + 4 * i;
+                    const int low = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] / scale, v[1] / scale, 0, false);
+                    w8[i] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(v[2] / scale, v[3] / scale, low, true);
+                }
+                __builtin_amdgcn_raw_buffer_store_b64(w8, q, c, 0, 0);
+            } else {
+                __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(r[u] / scale, 0.f, 0, false) & 0xff), q, c, 0, 0);
+            }
+        }
     }
-    const int group = a.group ? a.group : a.C, groups = a.C / group;
-    for (int u = 0; u < groups; ++u) {
-        float m = 0.f;
-        for (int c = threadIdx.x; c < group; c += 256) m = fmaxf(m, fabsf(sum(u * group + c) * k * a.weight[u * group + c]));
-        const float scale = fmaxf(all<true>(m, s), kLeast) / kE4M3Max;
-        if (threadIdx.x == 0) a.scales[(long long)blockIdx.x * groups + u] = scale;
-        for (int c = u * group + threadIdx.x; c < (u + 1) * group; c += 256)
-            static_cast<uint8_t*>(a.y)[at + c] = to_e4m3(sum(c) * k * a.weight[c] / scale);
-    }
-    if (a.res)
-        for (int c = threadIdx.x; c < a.C; c += 256) put<RF32>(a.r, at + c, sum(c));
 }
 
-constexpr int kParts = 256;
-
-// Workgroup p takes rows p, p + P, ...; its part of dweight goes to its row of the workspace.
-template <bool F32, bool RF32>
-__global__ __launch_bounds__(256) void kda_add_norm_bwd_kernel(NormArgs a) {
-    __shared__ float s[4];
-    float* part = a.part + (long long)blockIdx.x * a.C;
-    for (int c = threadIdx.x; c < a.C; c += 256) part[c] = 0.f;
-    for (long long row = blockIdx.x; row < a.rows; row += gridDim.x) {
-        const long long at = row * a.C;
-        float ss = 0.f, nd = 0.f;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float r = get<RF32>(a.res, at + c);
-            ss += r * r;
-            nd += r * get<F32>(a.dy, at + c) * a.weight[c];
+// dweight's sum over a workgroup's rows stays in registers, and goes to its row of the
+// workspace (each row of lanes has one of its own).
+template <bool F32, bool RF32, int E, int V>
+__global__ __launch_bounds__(1024) void kda_add_norm_bwd_kernel(NormArgs a, int wpr) {
+    __shared__ float s[2][16][2];
+    const int groups = (blockDim.x >> 6) / wpr, g = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / wpr;
+    Place<E, V> at{a.C, (int)threadIdx.x - g * wpr * 64, wpr * 64, 0, true};
+    Raw<true, E, V> w;
+    get(w, a.weight, at);
+    Raw<RF32, E, V> r, dr;
+    Raw<F32, E, V> dy;
+    const auto fetch = [&](long long row) {
+        at.at = row * a.C;
+        at.on = row < a.rows;
+        get(r, a.res, at);
+        get(dy, a.dy, at);
+        if (a.dr) get(dr, a.dr, at);
+    };
+    float dw[E] = {};
+    const long long step = (long long)gridDim.x * groups;
+    long long row = (long long)blockIdx.x * groups + g;
+    fetch(row);
+    int turn = 0;
+    for (long long first = (long long)blockIdx.x * groups; first < a.rows; first += step, row += step, turn ^= 1) {
+        float n[E], y[E], d[E], sum[2] = {0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            n[e] = r[e];
+            y[e] = dy[e];
+            d[e] = a.dr ? dr[e] : 0.f;
+            sum[0] += n[e] * n[e];
+            sum[1] += n[e] * (y[e] * w[e]);
         }
-        const float k = 1.f / sqrtf(all<false>(ss, s) / a.C + a.eps);
-        const float m = all<false>(nd, s) * k / a.C;
-        for (int c = threadIdx.x; c < a.C; c += 256) {
-            const float n = get<RF32>(a.res, at + c) * k, dy = get<F32>(a.dy, at + c);
-            float d = k * (dy * a.weight[c] - n * m);
-            if (a.dr) d += get<RF32>(a.dr, at + c);
-            part[c] += dy * n;
-            put<F32>(a.dx, at + c, d);
-            if (a.dres) put<RF32>(a.dres, at + c, d);
+        if (first + step < a.rows) fetch(row + step);
+        over_row<false>(sum, s[turn], wpr);
+        const float k = 1.f / sqrtf(sum[0] / a.C + a.eps), m = sum[1] * k / a.C;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            n[e] *= k;
+            dw[e] += y[e] * n[e];             // (nothing of a row that is not there)
+            d[e] += k * (y[e] * w[e] - n[e] * m);
         }
+        at.at = row * a.C;
+        at.on = row < a.rows;
+        put<F32>(a.dx, d, at);
+        if (a.dres) put<RF32>(a.dres, d, at);
     }
+    at.at = ((long long)blockIdx.x * groups + g) * a.C;
+    at.on = true;
+    put<true>(a.part, dw, at);
 }
 
-__global__ __launch_bounds__(256) void kda_add_norm_sum(NormArgs a, int P) {
-    const int c = blockIdx.x * 256 + threadIdx.x;
-    if (c >= a.C) return;
-    float x = 0.f;
-    for (int p = 0; p < P; ++p) x += a.part[(long long)p * a.C + c];
-    a.dweight[c] = x;
+// Column sums of part[P][C]: 32 columns a workgroup, 32 rows at a time, in a fixed order.
+__global__ __launch_bounds__(1024) void kda_add_norm_sum(NormArgs a, int P) {
+    __shared__ float s[32][33];
+    const int x = threadIdx.x & 31, y = threadIdx.x >> 5, c = blockIdx.x * 32 + x;
+    float v[8] = {};                   // eight loads in flight
+    if (c < a.C)
+        for (int p = y; p < P; p += 8 * 32)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += p + 32 * i < P ? a.part[(long long)(p + 32 * i) * a.C + c] : 0.f;
+    s[y][x] = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+    __syncthreads();
+    if (y > 0 || c >= a.C) return;
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum += s[i][x];
+    a.dweight[c] = sum;
 }
+
+// Waves of a row at 8, 16 or 32 values a lane, and rows of a workgroup of at least 256 lanes.
+struct Shape {
+    int E, wpr, threads, groups;
+};
+static Shape shape(int C) {
+    Shape s;
+    s.E = C <= 8192 ? 8 : C <= 16384 ? 16 : 32;
+    s.wpr = 1;
+    while (s.wpr * 64 * s.E < C) s.wpr *= 2;
+    s.threads = s.wpr * 64 > 256 ? s.wpr * 64 : 256;
+    s.groups = s.threads / (s.wpr * 64);
+    return s;
+}
+static unsigned blocks(long long rows, const Shape& s, int most) {
+    const long long n = (rows + s.groups - 1) / s.groups;
+    return (unsigned)(n < most ? n : most);
+}
+constexpr int kThreadsAll = 256 * 2048;    // lanes of the chip
 
 }  // namespace norm
 
-int norm_partials(long long rows, int) { return (int)(rows < norm::kParts ? rows : norm::kParts); }
+using norm::shape;
+
+int norm_partials(long long rows, int C) {
+    const norm::Shape s = shape(C);
+    return (int)norm::blocks(rows, s, norm::kThreadsAll / s.threads) * s.groups;
+}
+
+#define KDA_NORM_LAUNCH(kernel, n, ...) \
+    hipLaunchKernelGGL((kernel<__VA_ARGS__>), dim3(n), dim3(sh.threads), 0, s, a, sh.wpr)
+#define KDA_NORM_SIZES(kernel, n, f32, r32)                                                        \
+    do {                                                                                           \
+        if (a.vec) {                                                                               \
+            if (sh.E == 8) KDA_NORM_LAUNCH(kernel, n, f32, r32, 8, 8);                             \
+            else if (sh.E == 16) KDA_NORM_LAUNCH(kernel, n, f32, r32, 16, 8);                      \
+            else KDA_NORM_LAUNCH(kernel, n, f32, r32, 32, 8);                                      \
+        } else {                                                                                   \
+            if (sh.E == 8) KDA_NORM_LAUNCH(kernel, n, f32, r32, 8, 1);                             \
+            else if (sh.E == 16) KDA_NORM_LAUNCH(kernel, n, f32, r32, 16, 1);                      \
+            else KDA_NORM_LAUNCH(kernel, n, f32, r32, 32, 1);                                      \
+        }                                                                                          \
+    } while (0)
+#define KDA_NORM_TYPES(kernel, n)                                                                  \
+    do {                                                                                           \
+        if (a.f32) KDA_NORM_SIZES(kernel, n, true, true);                                          \
+        else if (a.res_f32) KDA_NORM_SIZES(kernel, n, false, true);                                \
+        else KDA_NORM_SIZES(kernel, n, false, false);                                              \
+    } while (0)
 
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t s) {
     using namespace norm;
     if (a.rows == 0) return hipSuccess;
-    const unsigned n = (unsigned)a.rows;
-    if (a.f32) hipLaunchKernelGGL((kda_add_norm_kernel<true, true>), dim3(n), dim3(256), 0, s, a);
-    else if (a.res_f32) hipLaunchKernelGGL((kda_add_norm_kernel<false, true>), dim3(n), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((kda_add_norm_kernel<false, false>), dim3(n), dim3(256), 0, s, a);
+    const Shape sh = shape(a.C);
+    const unsigned n = blocks(a.rows, sh, kThreadsAll / sh.threads);
+    KDA_NORM_TYPES(kda_add_norm_kernel, n);
     return hipGetLastError();
 }
 
 hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t s) {
     using namespace norm;
+    const Shape sh = shape(a.C);
     const int P = norm_partials(a.rows, a.C);
     if (P > 0) {
-        if (a.f32) hipLaunchKernelGGL((kda_add_norm_bwd_kernel<true, true>), dim3(P), dim3(256), 0, s, a);
-        else if (a.res_f32) hipLaunchKernelGGL((kda_add_norm_bwd_kernel<false, true>), dim3(P), dim3(256), 0, s, a);
-        else hipLaunchKernelGGL((kda_add_norm_bwd_kernel<false, false>), dim3(P), dim3(256), 0, s, a);
+        const unsigned n = (unsigned)(P / sh.groups);
+        KDA_NORM_TYPES(kda_add_norm_bwd_kernel, n);
     }
-    hipLaunchKernelGGL(kda_add_norm_sum, dim3((a.C + 255) / 256), dim3(256), 0, s, a, P);
+    hipLaunchKernelGGL(kda_add_norm_sum, dim3((a.C + 31) / 32), dim3(1024), 0, s, a, P);
     return hipGetLastError();
 }
 
