@@ -6,7 +6,7 @@
 
 namespace kda {
 
-constexpr int kNormMaxC = 32768;
+constexpr int kNormMaxC = 16384;
 
 struct NormArgs {
     const void* x;

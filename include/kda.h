@@ -534,7 +534,7 @@ kda_status_t kda_scan_recurrent(const void* x, const float* g, const int32_t* cu
  *     x, y [rows, C] dtype;  residual, r [rows, C] res_dtype: dtype, or fp32;
  *     weight [C] fp32
  * The norm is of r as it is stored. residual == NULL: r = x, and r_out is not
- * written. y == x and r_out == residual are allowed. C is 1 to 32,768, rows times C at
+ * written. y == x and r_out == residual are allowed. C is 1 to 16,384, rows times C at
  * most 2^40 and rows at most 2^31 - 1 (KDA_ERR_SHAPE); a negative or non-finite
  * eps or another res_dtype is KDA_ERR_UNSUPPORTED. Rows of a multiple of eight
  * channels, in tensors that are all 16-byte aligned, are the fast ones.
