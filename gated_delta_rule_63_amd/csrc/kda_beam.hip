@@ -459,44 +459,55 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
 // --------------------------------------------------------------- reordering
 // A beam's first child keeps its slot; the others take the slots of beams
 // without children, in turn. So a slot that is read is never written, and the
-// slots stay the same set. Every workgroup forms its entry's plan by itself.
-struct Place {
+// slots stay the same set. Every wave forms its entry's plan by itself, one beam a
+// lane: a trip to memory, and no step between the plan and the copies.
+struct Move {
     int from, to;               // slots; equal: nothing to copy
 };
-__device__ __forceinline__ Place place(const ReorderArgs& a, int b, int j) {
-    const int32_t* slots = a.slots + (long long)b * a.W;
-    const int32_t* parents = a.parents + (long long)b * a.W;
-    uint64_t seen = 0;          // beams with a child before j ...
-    int takers = 0, p = 0;      // ... and how many children before it found none to inherit
-    bool first = false;
-    for (int i = 0; i <= j; ++i) {
-        p = parents[i];
-        first = p >= 0 && p < a.W && !(seen >> p & 1);
-        if (first) seen |= 1ull << p;
-        else if (i < j) ++takers;
-    }
+__device__ __forceinline__ Move move_of(const ReorderArgs& a, int b, int j) {
+    const int l = threadIdx.x & 63, at = b * a.W + min(l, a.W - 1);
+    const int slot = a.slots[at], p = l < a.W ? a.parents[at] : -1;
     const bool valid = p >= 0 && p < a.W;
-    if (first) return Place{slots[p], slots[p]};
-    for (int i = j + 1; i < a.W; ++i) {
-        const int q = parents[i];
-        if (q >= 0 && q < a.W) seen |= 1ull << q;
+    bool again = false, childless = true;
+    for (int i = 0; i < a.W; ++i) {
+        const int q = __builtin_amdgcn_readlane(p, i);
+        again |= i < l && q == p;
+        childless &= q != l;
     }
-    int to = 0;
-    for (int w = 0, free = 0; w < a.W; ++w)
-        if (!(seen >> w & 1) && free++ == takers) to = slots[w];
-    return Place{valid ? slots[p] : to, to};
+    const uint64_t all = ~0ull >> (64 - a.W), below = (1ull << j) - 1;
+    const uint64_t keeps = __ballot(valid && !again), free = __ballot(childless) & all;
+    const int parent = __builtin_amdgcn_readlane(p, j);
+    if (keeps >> j & 1) {
+        const int s = __builtin_amdgcn_readlane(slot, parent);
+        return Move{s, s};
+    }
+    // as many children take a slot as slots are free: those of beams without children
+    const int turn = __popcll(~keeps & below);
+    const uint64_t mine = __ballot(childless && l < a.W && __popcll(free & ((1ull << l) - 1)) == turn);
+    const int to = __builtin_amdgcn_readlane(slot, __builtin_ctzll(mine));
+    return Move{parent >= 0 && parent < a.W ? __builtin_amdgcn_readlane(slot, parent) : to, to};
 }
 
+constexpr int kInFlight = 8;    // pieces of a thread
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));   // (an array of uint4 goes through scratch memory)
+
 template <typename T>
-__global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, int pieces) {
-    const int e = blockIdx.x / pieces, piece = blockIdx.x % pieces, b = e / a.W, j = e % a.W;
-    const Place p = place(a, b, j);
-    if (piece == 0 && threadIdx.x == 0) a.new_slots[e] = p.to;
-    if (p.from == p.to || p.from < 0 || p.from >= a.num_slots || p.to < 0 || p.to >= a.num_slots) return;
-    const T* from = reinterpret_cast<const T*>(a.pool + (size_t)p.from * a.slot_bytes);
-    T* to = reinterpret_cast<T*>(a.pool + (size_t)p.to * a.slot_bytes);
+__global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, int parts) {
+    const int e = blockIdx.x / parts, part = blockIdx.x % parts;
+    const Move m = move_of(a, e / a.W, e % a.W);
+    if (part == 0 && threadIdx.x == 0) a.new_slots[e] = m.to;
+    if (m.from == m.to || m.from < 0 || m.from >= a.num_slots || m.to < 0 || m.to >= a.num_slots) return;
+    const T* from = reinterpret_cast<const T*>(a.pool + (size_t)m.from * a.slot_bytes);
+    T* to = reinterpret_cast<T*>(a.pool + (size_t)m.to * a.slot_bytes);
     const size_t n = a.slot_bytes / sizeof(T);
-    for (size_t i = (size_t)piece * 256 + threadIdx.x; i < n; i += (size_t)pieces * 256) to[i] = from[i];
+    for (size_t i = (size_t)part * (256 * kInFlight) + threadIdx.x; i < n; i += (size_t)parts * (256 * kInFlight)) {
+        T x[kInFlight];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u) x[u] = from[min(i + u * 256, n - 1)];
+#pragma unroll
+        for (int u = 0; u < kInFlight; ++u)
+            if (i + u * 256 < n) to[i + u * 256] = x[u];
+    }
 }
 
 }  // namespace beam
@@ -523,11 +534,13 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
 hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
     using namespace beam;
     if (a.B == 0) return hipSuccess;
-    const int pieces = 16;
-    const unsigned n = (unsigned)(a.B * a.W * pieces);
-    if (a.unit == 16) hipLaunchKernelGGL(kda_beam_reorder_kernel<uint4>, dim3(n), dim3(256), 0, s, a, pieces);
-    else if (a.unit == 4) hipLaunchKernelGGL(kda_beam_reorder_kernel<uint32_t>, dim3(n), dim3(256), 0, s, a, pieces);
-    else hipLaunchKernelGGL(kda_beam_reorder_kernel<uint8_t>, dim3(n), dim3(256), 0, s, a, pieces);
+    // up to 64 workgroups a copy, one turn each where that is enough (32 KiB at 16 bytes a piece)
+    const size_t turns = (a.slot_bytes / a.unit + 256 * kInFlight - 1) / (256 * kInFlight);
+    const int parts = (int)(turns < 1 ? 1 : turns > 64 ? 64 : turns);
+    const unsigned n = (unsigned)(a.B * a.W * parts);
+    if (a.unit == 16) hipLaunchKernelGGL(kda_beam_reorder_kernel<u32x4>, dim3(n), dim3(256), 0, s, a, parts);
+    else if (a.unit == 4) hipLaunchKernelGGL(kda_beam_reorder_kernel<uint32_t>, dim3(n), dim3(256), 0, s, a, parts);
+    else hipLaunchKernelGGL(kda_beam_reorder_kernel<uint8_t>, dim3(n), dim3(256), 0, s, a, parts);
     return hipGetLastError();
 }
 
