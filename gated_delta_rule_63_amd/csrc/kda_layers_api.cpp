@@ -45,7 +45,11 @@ kda_status_t check_scan(const kda_scan_desc_t* d) {
     return check_type(d->dtype);
 }
 
-kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const int32_t* cu, bool back,
+kda::ScanForm form(const kda_scan_desc_t* d, bool packed, bool back, bool known) {
+    return {d->B, d->T, d->C, d->num_seqs, packed, d->dtype == KDA_F32, d->leaky != 0, back, known};
+}
+
+kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const int32_t* cu, bool back, bool known,
                        const kda_scan_desc_t* d) {
     const kda_status_t st = check_scan(d);
     if (st != KDA_OK) return st;
@@ -58,7 +62,7 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     a->slots = (int)kda::scan_slots(d->B, d->T, d->num_seqs, cu != nullptr);
     a->f32 = d->dtype == KDA_F32;
     a->leaky = d->leaky != 0;
-    a->width = kda::scan_width(d->T, d->C, d->num_seqs, back, compute_units());
+    a->width = kda::scan_width(form(d, cu != nullptr, back, known), compute_units());
     return KDA_OK;
 }
 
@@ -73,7 +77,8 @@ size_t scan_bytes(const kda_scan_desc_t* d, bool back, bool with_states) {
     if (check_scan(d) != KDA_OK) return 0;
     const size_t row = up16(4 * (size_t)most_slots(d) * d->C);
     size_t n = back && !with_states ? row : 0;
-    if (kda::scan_width(d->T, d->C, d->num_seqs, back, compute_units()) == 0) n += 3 * row;
+    for (const bool packed : {false, true})
+        if (kda::scan_width(form(d, packed, back, with_states), compute_units()) == 0) return n + 3 * row;
     return n;
 }
 
@@ -143,7 +148,7 @@ extern "C" {
 kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, const float* h0, void* y, float* hT,
                       float* states, const kda_scan_desc_t* desc, void* stream) {
     kda::ScanArgs a;
-    kda_status_t st = scan_args(&a, x, g, cu_seqlens, false, desc);
+    kda_status_t st = scan_args(&a, x, g, cu_seqlens, false, true, desc);
     if (st != KDA_OK) return st;
     if (desc->T > 0 && !y) return KDA_ERR_NULL;
     st = workspace(desc->workspace, desc->workspace_bytes, kda_scan_workspace_size(desc));
@@ -165,7 +170,7 @@ kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqle
                           const float* states, const void* dy, const float* dhT, void* dx, float* dg, float* dh0,
                           const kda_scan_desc_t* desc, void* stream) {
     kda::ScanArgs a;
-    kda_status_t st = scan_args(&a, x, g, cu_seqlens, true, desc);
+    kda_status_t st = scan_args(&a, x, g, cu_seqlens, true, states != nullptr, desc);
     if (st != KDA_OK) return st;
     if (desc->T > 0 && !all_there(dy, dx, dg)) return KDA_ERR_NULL;
     st = workspace(desc->workspace, desc->workspace_bytes, kda_scan_bwd_workspace_size(desc, states != nullptr));
@@ -185,7 +190,7 @@ kda_status_t kda_scan_recurrent(const void* x, const float* g, const int32_t* cu
                                 const int32_t* out_slots, void* pool, int32_t num_slots, int32_t pool_dtype, void* y,
                                 const kda_scan_desc_t* desc, void* stream) {
     kda::ScanArgs s;
-    const kda_status_t st = scan_args(&s, x, g, cu_seqlens, false, desc);
+    const kda_status_t st = scan_args(&s, x, g, cu_seqlens, false, true, desc);
     if (st != KDA_OK) return st;
     if (check_type(pool_dtype) != KDA_OK) return KDA_ERR_DTYPE;
     if (num_slots < 0 || (!slots && num_slots < desc->num_seqs)) return KDA_ERR_SHAPE;

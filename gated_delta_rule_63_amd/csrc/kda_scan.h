@@ -49,7 +49,12 @@ struct ScanPoolArgs {
 long long scan_slots(int B, int T, int N, bool packed);
 // How a call runs: channels of a workgroup that goes through a sequence (64, 32, 16), or 0:
 // its chunks side by side, in three kernels.
-int scan_width(int T, int C, int N, bool back, int cus);
+struct ScanForm {
+    int rows, T, C, N;            // rows of T tokens, sequences
+    bool packed, f32, leaky;
+    bool back, known;             // the gradient; with the forward's states
+};
+int scan_width(const ScanForm& f, int cus);
 
 hipError_t launch_scan(const ScanArgs& a, hipStream_t s);
 // known: `states` holds the forward's; else it is formed first.

@@ -13,6 +13,8 @@
 #include "kda_device.h"
 #include "kda_scan.h"
 
+#include <math.h>
+
 namespace kda {
 namespace scan {
 
@@ -398,8 +400,8 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
 
 // From a sequence's chunks in order to the states that enter them, and in reverse to the
 // gradients that leave them: the same fold, of chunks instead of tokens.
-constexpr int SC = 16, NC = 1024 / SC;   // its channels and runs of L chunks
-template <bool BACK>
+// Workgroups of SC channels by NC runs of L chunks: 16 by 64 for long sequences, else 64 by 4.
+template <bool BACK, int SC, int NC>
 __device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, float2 (*sh)[NC][SC]) {
     const int l = threadIdx.x % SC, sub = threadIdx.x / SC, c = strip * SC + l, cc = min(c, a.C - 1);
     const Run run = sequence(a, n);
@@ -426,7 +428,7 @@ __device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, flo
         sh[k & 1][sub][l] = make_float2(A, B);
         lds_barrier();
         float in = h;
-#pragma unroll 16
+#pragma unroll NC < 16 ? NC : 16
         for (int j = 0; j < NC; ++j) {
             const float2 m = sh[k & 1][j][l];
             if (j == sub) in = h;
@@ -443,21 +445,22 @@ __device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, flo
     if (end && sub == 0 && c < a.C) end[(long long)n * a.C + c] = h;
 }
 
-template <bool FWD, bool BWD>
-__global__ __launch_bounds__(1024) void kda_scan_combine(ScanArgs a) {
+template <bool FWD, bool BWD, int SC, int NC>
+__global__ __launch_bounds__(SC * NC) void kda_scan_combine(ScanArgs a) {
     __shared__ float2 sh[2][NC][SC];
     const int strips = (a.C + SC - 1) / SC, both = a.N * strips;
     const int i = blockIdx.x < both ? blockIdx.x : blockIdx.x - both;
-    if (FWD && (!BWD || blockIdx.x < both)) combine<false>(a, i / strips, i % strips, sh);
-    else combine<true>(a, i / strips, i % strips, sh);
+    if (FWD && (!BWD || blockIdx.x < both)) combine<false, SC, NC>(a, i / strips, i % strips, sh);
+    else combine<true, SC, NC>(a, i / strips, i % strips, sh);
 }
 
-// A chunk from the state that enters it.
+// A chunk from the state that enters it; the last ones first, since the last-level cache
+// still holds what the sums read last (T = 131072, C = 512: 192 -> 181 us).
 template <bool F32, bool LEAKY>
 __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
     __shared__ float2 sh[W][S];
     const int strips = (a.C + S - 1) / S;
-    const long long slot = blockIdx.x / strips;
+    const long long slot = a.slots - 1 - blockIdx.x / strips;
     const Lane<S> p(a, blockIdx.x % strips);
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, sequence_of(a, slot));
@@ -481,7 +484,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a) {
     __shared__ float2 sh[W][S];
     __shared__ float sd[W][S];
     const int strips = (a.C + S - 1) / S;
-    const long long slot = blockIdx.x / strips;
+    const long long slot = a.slots - 1 - blockIdx.x / strips;
     const Lane<S> p(a, blockIdx.x % strips);
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, sequence_of(a, slot));
@@ -533,24 +536,41 @@ long long scan_slots(int B, int T, int N, bool packed) {
     return packed ? (long long)T / kScanChunk + N : (long long)B * ((T + (long long)kScanChunk - 1) / kScanChunk);
 }
 
-// A workgroup goes through 1000 tokens in 14, 8 or 5 us with 64, 32 or 16 channels (the
-// gradient: 28, 15, 9), as long as memory keeps up; the narrower ones move 90 to 75% as
-// many bytes a second where all are at work (T = 8192, bf16, forwards: C = 12288 163, 207, 217
-// us; C = 8192 142, 113, 141; 131072 x 4096 1990, 1302, 1065, and 1396 with the chunks side
-// by side). So: the widest that occupies five compute units in eight. With fewer chains
-// than that, chunks side by side cost three launches and read their inputs twice, but
-// fill the chip: 131072 x 512 889 us (16 channels) against 192, 8192 x 2048 62 against 46,
-// 4096 x 256 22 against 20; the gradient 1688 against 268 and 38 against 24.
-int scan_width(int T, int C, int N, bool back, int cus) {
-    const auto groups = [&](int width) { return (long long)N * ((C + width - 1) / width); };
-    if (8 * groups(64) >= 5LL * cus) return 64;
-    if (8 * groups(32) >= 5LL * cus) return 32;
-    const long long len = N > 1 ? 2LL * T / N : T;     // (packed sequences: a guess at the longest)
-    if (len <= (back ? 2048 : 4096)) return 16;
-    return 8 * groups(16) >= 6LL * cus && (!back || len <= 16384) ? 16 : 0;
+// How a call runs is the cheapest of four by this estimate, in ns:
+//   one workgroup a (sequence, strip): the longest sequence at what a workgroup takes a
+//     token (8192 x 2048, 32 to 128 of them: 128, 78, 62 us with 64, 32, 16 channels, the
+//     gradient 229, 150, 120; about 1.45 times that in the leaky form), or all bytes at a
+//     rate that falls with the width of a row's piece (8192 x 12288, which the first fills:
+//     163, 207, 217 us; 8192 x 8192: 142, 113, 141; 131072 x 4096: 1990, 1302, 1065);
+//   chunks side by side: three launches that read the inputs twice (the same four:
+//     45, 280, 192 and 1395 us; 131072 x 512: 889 us with 16 channels against 181, the
+//     gradient 1688 against 263).
+// Packed sequences do not tell the host the longest; twice the average stands for it.
+int scan_width(const ScanForm& f, int cus) {
+    static const struct { int width; double fwd, bwd, rate; } strip[] = {{64, 15.5, 28, 4900}, {32, 9.5, 18, 4600}, {16, 7.5, 14.6, 4000}};
+    const double el = (double)f.rows * f.T * f.C, e = f.f32 ? 4 : 2, len = f.packed && f.N > 1 ? fmin(f.T, 2.0 * f.T / f.N) : f.T;
+    const bool first = f.back && !f.known;             // states to be formed
+    const double bytes = f.back ? 3 * e + 8 : 2 * e + 4;
+    int best = 0;
+    double least = 12000 + el * (bytes + (first ? 2 * e + 4 : e + 4)) / 4.9e3;
+    for (const auto& s : strip) {
+        const double groups = (double)f.N * ((f.C + s.width - 1) / s.width);
+        const double token = (f.back ? s.bwd + (first ? s.fwd : 0) : s.fwd) * (f.leaky ? 1.45 : 1.0);
+        const double turns = fmax(1.0, groups / (2.0 * cus)), at = fmin(1.0, 0.5 + 0.5 * groups / (0.6 * cus));
+        const double t = fmax(len * token * (f.packed ? 1.0 : turns), el * (bytes + (first ? e + 4 : 0)) / (s.rate * at));
+        if (t < least) best = s.width, least = t;
+    }
+    return best;
 }
 
 #define KDA_SCAN_LAUNCH(kernel, n, threads) hipLaunchKernelGGL((kernel), dim3((unsigned)(n)), dim3(threads), 0, s, a)
+
+// (128 chunks a sequence: 64 channels go twice through 64 chunks; 16 channels have four runs in five idle)
+#define KDA_SCAN_COMBINE(fwd, bwd, n)                                                                          \
+    do {                                                                                                       \
+        if (a.slots <= 128LL * a.N) KDA_SCAN_LAUNCH((kda_scan_combine<fwd, bwd, 64, 4>), n * a.N * strips, 256); \
+        else KDA_SCAN_LAUNCH((kda_scan_combine<fwd, bwd, 16, 64>), n * a.N * ((a.C + 15LL) / 16), 1024);       \
+    } while (0)
 
 template <bool F32, bool LEAKY>
 static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
@@ -563,7 +583,7 @@ static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
         return hipGetLastError();
     }
     if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks, 64 * W);
-    KDA_SCAN_LAUNCH((kda_scan_combine<true, false>), a.N * ((a.C + SC - 1) / SC), 1024);
+    KDA_SCAN_COMBINE(true, false, 1);
     if (chunks > 0 && a.y) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY>), chunks, 64 * W);
     return hipGetLastError();
 }
@@ -584,10 +604,10 @@ static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
     }
     if (known) {
         if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, false, true>), chunks, 64 * W);
-        KDA_SCAN_LAUNCH((kda_scan_combine<false, true>), a.N * ((a.C + SC - 1) / SC), 1024);
+        KDA_SCAN_COMBINE(false, true, 1);
     } else {
         if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, true>), chunks, 64 * W);
-        KDA_SCAN_LAUNCH((kda_scan_combine<true, true>), 2 * a.N * ((a.C + SC - 1) / SC), 1024);
+        KDA_SCAN_COMBINE(true, true, 2);
     }
     if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks_bwd<F32, LEAKY>), chunks, 64 * W);
     return hipGetLastError();

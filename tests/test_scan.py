@@ -140,6 +140,13 @@ CASES = [  # lengths (None: rows of T), B, T, C, type, leaky, states both ways
     ((0, 3, 0, 128, 1, 257, 0), 1, 389, 65, "float32", False, True),
     ((130, 5, 300, 0, 64), 1, 499, 64, "bfloat16", True, True),
     ((1, 2, 3, 127, 129, 700), 1, 962, 5, "float32", True, False),
+    # the other forms: 64 and 32 channels a workgroup, and a sequence's chunks side by side
+    (None, 40, 150, 260, "bfloat16", False, True),
+    (None, 40, 300, 130, "float32", True, True),
+    (None, 1, 9000, 40, "bfloat16", False, True),
+    (None, 1, 4300, 67, "float32", True, False),
+    ((3000, 0, 1, 2500, 129), 1, 5630, 34, "bfloat16", True, True),
+    ((900, 0, 70, 1500, 129), 1, 2599, 1000, "float32", False, True),
 ]
 
 
