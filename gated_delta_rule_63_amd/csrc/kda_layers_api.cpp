@@ -201,6 +201,7 @@ kda_status_t kda_scan_recurrent(const void* x, const float* g, const int32_t* cu
     a.pool = pool; a.y = y;
     a.T = s.T; a.C = s.C; a.N = s.N; a.num_slots = num_slots;
     a.f32 = s.f32; a.leaky = s.leaky; a.pool_bf16 = pool_dtype == KDA_BF16;
+    a.vec = s.C % 4 == 0 && aligned16(x, g, pool, y);
     return status(kda::launch_scan_recurrent(a, static_cast<hipStream_t>(stream)));
 }
 

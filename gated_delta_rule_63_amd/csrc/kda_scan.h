@@ -43,6 +43,7 @@ struct ScanPoolArgs {
     void* y;
     int T, C, N, num_slots;
     bool f32, leaky, pool_bf16;
+    bool vec;                     // four neighbouring channels can be read and written at once
 };
 
 // Rows of `states`: one for each chunk of each sequence; packed, sequence n's begin at row cu[n] / 128 + n.

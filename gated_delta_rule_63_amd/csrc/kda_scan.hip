@@ -503,13 +503,28 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a) {
 }
 
 // ------------------------------------------------------------ token by token
-template <bool F32, bool BF16, bool LEAKY>
-__global__ __launch_bounds__(256) void kda_scan_recurrent_kernel(ScanPoolArgs a) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= (long long)a.N * a.C) return;
-    const int n = (int)(i / a.C), c = (int)(i % a.C);
+// A lane owns V neighbouring channels of a sequence over all its tokens, the next token's
+// inputs fetched while one is worked on. Bound by memory, or, few tokens, by a launch
+// and two trips to it (the slot, then the state).
+template <typename T, int V>
+struct Vec {
+    typedef T type __attribute__((ext_vector_type(V)));
+    type x;
+    __device__ __forceinline__ void get(const void* p, long long i) { x = *reinterpret_cast<const type*>(static_cast<const T*>(p) + i); }
+    __device__ __forceinline__ void put(void* p, long long i) const { *reinterpret_cast<type*>(static_cast<T*>(p) + i) = x; }
+};
+template <typename T>
+struct Vec<T, 1> {
+    T x[1];
+    __device__ __forceinline__ void get(const void* p, long long i) { x[0] = static_cast<const T*>(p)[i]; }
+    __device__ __forceinline__ void put(void* p, long long i) const { static_cast<T*>(p)[i] = x[0]; }
+};
+
+template <bool F32, bool BF16, bool LEAKY, int V>
+__global__ __launch_bounds__(256) void kda_scan_recurrent_kernel(ScanPoolArgs a, unsigned per) {
+    const int n = blockIdx.x / per, c = ((blockIdx.x % per) * 256 + threadIdx.x) * V;
     const int slot = a.slots ? a.slots[n] : n;
-    if (slot < 0 || slot >= a.num_slots) return;
+    if (c >= a.C || slot < 0 || slot >= a.num_slots) return;   // (an empty place of the batch)
     long long tok = (long long)n * a.T;
     int len = a.T;
     if (a.cu) {
@@ -518,15 +533,31 @@ __global__ __launch_bounds__(256) void kda_scan_recurrent_kernel(ScanPoolArgs a)
         tok = t0;
     }
     if (len <= 0) return;
-    raw_t<!BF16>* pool = static_cast<raw_t<!BF16>*>(a.pool);
-    float h = up(pool[(long long)slot * a.C + c]);
+    Vec<raw_t<F32>, V> x, y;
+    Vec<float, V> g;
+    Vec<raw_t<!BF16>, V> s;
+    x.get(a.x, tok * a.C + c);
+    g.get(a.g, tok * a.C + c);
+    s.get(a.pool, (long long)slot * a.C + c);
+    float h[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) h[i] = up(s.x[i]);
     for (int t = 0; t < len; ++t, ++tok) {
-        float d, in;
-        decay<LEAKY>(a.g[tok * a.C + c], d, in);
-        h = fmaf(d, h, up(static_cast<const raw_t<F32>*>(a.x)[tok * a.C + c]) * in);
-        static_cast<raw_t<F32>*>(a.y)[tok * a.C + c] = down<F32>(h);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            float d, in;
+            decay<LEAKY>(g.x[i], d, in);
+            h[i] = fmaf(d, h[i], up(x.x[i]) * in);
+            y.x[i] = down<F32>(h[i]);
+            s.x[i] = down<!BF16>(h[i]);
+        }
         const int to = a.out_slots ? a.out_slots[tok] : t + 1 == len ? slot : -1;
-        if (to >= 0 && to < a.num_slots) pool[(long long)to * a.C + c] = down<!BF16>(h);
+        if (t + 1 < len) {
+            x.get(a.x, (tok + 1) * a.C + c);
+            g.get(a.g, (tok + 1) * a.C + c);
+        }
+        y.put(a.y, tok * a.C + c);
+        if (to >= 0 && to < a.num_slots) s.put(a.pool, (long long)to * a.C + c);
     }
 }
 
@@ -623,13 +654,17 @@ hipError_t launch_scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
     return a.leaky ? scan_bwd<false, true>(a, known, s) : scan_bwd<false, false>(a, known, s);
 }
 
-template <bool F32, bool BF16>
+template <bool F32, bool BF16, int V>
 static hipError_t recurrent_scan(const ScanPoolArgs& a, hipStream_t s) {
     using namespace scan;
-    const unsigned n = (unsigned)(((long long)a.N * a.C + 255) / 256);
-    if (a.leaky) hipLaunchKernelGGL((kda_scan_recurrent_kernel<F32, BF16, true>), dim3(n), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((kda_scan_recurrent_kernel<F32, BF16, false>), dim3(n), dim3(256), 0, s, a);
+    const unsigned per = (unsigned)((a.C + 256 * V - 1) / (256 * V)), n = (unsigned)a.N * per;
+    if (a.leaky) hipLaunchKernelGGL((kda_scan_recurrent_kernel<F32, BF16, true, V>), dim3(n), dim3(256), 0, s, a, per);
+    else hipLaunchKernelGGL((kda_scan_recurrent_kernel<F32, BF16, false, V>), dim3(n), dim3(256), 0, s, a, per);
     return hipGetLastError();
+}
+template <bool F32, bool BF16>
+static hipError_t recurrent_scan(const ScanPoolArgs& a, hipStream_t s) {
+    return a.vec ? recurrent_scan<F32, BF16, 4>(a, s) : recurrent_scan<F32, BF16, 1>(a, s);
 }
 
 hipError_t launch_scan_recurrent(const ScanPoolArgs& a, hipStream_t s) {
