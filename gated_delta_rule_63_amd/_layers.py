@@ -13,13 +13,12 @@ from ._lib import BeamDesc, NormDesc, ScanDesc, lib
 from ._ops import _DTYPES, _Tensor, _call, _on, _ptr, _rows
 
 SCAN_CHUNK = 128
-_TYPES = (torch.bfloat16, torch.float32)
 
 
 def _plain(name, t, shape, dtype, device, _device=True):
-    """A tensor the kernels read or write: contiguous, of this shape, type and device."""
+    """A tensor the kernels read or write: contiguous, of this shape (a torch.Size), type and device."""
     if t is not None:
-        _rows(name, t, torch.Size(shape), dtype, device, _device)
+        _rows(name, t, shape, dtype, device, _device)
 
 
 def _bytes(n: int, like: torch.Tensor) -> _Tensor:
@@ -34,30 +33,36 @@ def _with(desc, ws: _Tensor):
 
 # ------------------------------------------------------- the rule with a vector state
 
-def _scan_desc(x, cu_seqlens) -> ScanDesc:
-    N = x.shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    return ScanDesc(x.shape[0], x.shape[1], x.shape[2:].numel(), N, _DTYPES[x.dtype], 0, None, 0)
+def _scan_desc(x, cu_seqlens, leaky=False) -> ScanDesc:
+    shape = x.shape
+    N = shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
+    return ScanDesc(shape[0], shape[1], shape[2] if len(shape) == 3 else shape[2:].numel(), N, _DTYPES[x.dtype], leaky, None, 0)
 
 
-def _check_scan(x, g, cu_seqlens, _device=True) -> ScanDesc:
-    if x.dim() < 3 or x.dtype not in _TYPES:
+def _scan_state(d: ScanDesc, x) -> torch.Size:
+    return torch.Size((d.num_seqs, *x.shape[2:]))
+
+
+def _check_scan(x, g, cu_seqlens, leaky=False, _device=True) -> ScanDesc:
+    shape, device = x.shape, x.device
+    if len(shape) < 3 or x.dtype not in _DTYPES:
         raise ValueError("x must be a bfloat16 or float32 [B, T, ...] tensor")
-    _plain("x", x, x.shape, x.dtype, x.device, _device)
-    _plain("g", g, x.shape, torch.float32, x.device, _device)
+    _rows("x", x, shape, x.dtype, device, _device)
+    _rows("g", g, shape, torch.float32, device, False)
     if cu_seqlens is not None:
         if (cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1
-                or not cu_seqlens.is_contiguous() or cu_seqlens.device != x.device):
+                or not cu_seqlens.is_contiguous() or cu_seqlens.device != device):
             raise ValueError("cu_seqlens must be a contiguous int32 [N + 1] tensor on x's device")
-        if x.shape[0] != 1:
+        if shape[0] != 1:
             raise ValueError("with cu_seqlens the batch dimension must be 1 (sequences packed into one row)")
-    return _scan_desc(x, cu_seqlens)
+    return _scan_desc(x, cu_seqlens, leaky)
 
 
 def _states_shape(d: ScanDesc, x, cu_seqlens):
     """Shape of the states at chunk starts: [B, ceil(T / 128), ...], packed [1, T // 128 + N, ...]."""
     if cu_seqlens is None:
-        return (d.B, (d.T + SCAN_CHUNK - 1) // SCAN_CHUNK, *x.shape[2:])
-    return (1, d.T // SCAN_CHUNK + d.num_seqs, *x.shape[2:])
+        return torch.Size((d.B, (d.T + SCAN_CHUNK - 1) // SCAN_CHUNK, *x.shape[2:]))
+    return torch.Size((1, d.T // SCAN_CHUNK + d.num_seqs, *x.shape[2:]))
 
 
 def _workspace(given: _Tensor, need: int, like: torch.Tensor) -> _Tensor:
@@ -88,16 +93,15 @@ def scan(x: torch.Tensor, g: torch.Tensor, cu_seqlens: _Tensor = None, initial_s
     sequence n's begin at row cu[n] // 128 + n and rows without a chunk are unset), else
     None. out may be x. workspace: an optional device tensor of scan_workspace_size() bytes,
     used by one call at a time; allocated otherwise."""
-    d = _check_scan(x, g, cu_seqlens)
-    state = (d.num_seqs, *x.shape[2:])
+    d = _check_scan(x, g, cu_seqlens, leaky)
+    state = _scan_state(d, x)
     _plain("initial_state", initial_state, state, torch.float32, x.device)
     _plain("final_state", final_state, state, torch.float32, x.device)
     _plain("out", out, x.shape, x.dtype, x.device)
-    d.leaky = int(leaky)
     with _on(x.device, stream) as s:
         y = torch.empty_like(x) if out is None else out
-        hT = x.new_empty(state, dtype=torch.float32) if final_state is None else final_state
-        kept = x.new_empty(_states_shape(d, x, cu_seqlens), dtype=torch.float32) if output_chunk_states else None
+        hT = g.new_empty(state) if final_state is None else final_state
+        kept = g.new_empty(_states_shape(d, x, cu_seqlens)) if output_chunk_states else None
         ws = _workspace(workspace, int(lib().kda_scan_workspace_size(ctypes.byref(d))), x)
         _call("kda_scan", _ptr(x), _ptr(g), _ptr(cu_seqlens), _ptr(initial_state), _ptr(y), _ptr(hT), _ptr(kept),
               _with(d, ws), s)
@@ -114,11 +118,10 @@ def scan_bwd(x: torch.Tensor, g: torch.Tensor, dy: torch.Tensor, cu_seqlens: _Te
     dtype, the others fp32. Rows of tokens that belong to no sequence are unset. workspace:
     an optional device tensor of scan_bwd_workspace_size() bytes, used by one call at a
     time; allocated otherwise."""
-    d = _check_scan_bwd(x, g, dy, cu_seqlens, initial_state, d_final_state, chunk_states)
-    d.leaky = int(leaky)
+    d = _check_scan_bwd(x, g, dy, cu_seqlens, initial_state, d_final_state, chunk_states, leaky)
     with _on(x.device, stream) as s:
         dx, dg = torch.empty_like(x), torch.empty_like(g)
-        dh0 = x.new_empty((d.num_seqs, *x.shape[2:]), dtype=torch.float32)
+        dh0 = g.new_empty(_scan_state(d, x))
         need = int(lib().kda_scan_bwd_workspace_size(ctypes.byref(d), chunk_states is not None))
         ws = _workspace(workspace, need, x)
         _call("kda_scan_bwd", _ptr(x), _ptr(g), _ptr(cu_seqlens), _ptr(initial_state), _ptr(chunk_states), _ptr(dy),
@@ -126,9 +129,9 @@ def scan_bwd(x: torch.Tensor, g: torch.Tensor, dy: torch.Tensor, cu_seqlens: _Te
     return dx, dg, dh0
 
 
-def _check_scan_bwd(x, g, dy, cu_seqlens, initial_state, d_final_state, chunk_states, _device=True) -> ScanDesc:
-    d = _check_scan(x, g, cu_seqlens, _device)
-    state = (d.num_seqs, *x.shape[2:])
+def _check_scan_bwd(x, g, dy, cu_seqlens, initial_state, d_final_state, chunk_states, leaky=False, _device=True) -> ScanDesc:
+    d = _check_scan(x, g, cu_seqlens, leaky, _device)
+    state = _scan_state(d, x)
     _plain("dy", dy, x.shape, x.dtype, x.device, _device)
     _plain("initial_state", initial_state, state, torch.float32, x.device, _device)
     _plain("d_final_state", d_final_state, state, torch.float32, x.device, _device)
@@ -147,8 +150,7 @@ def scan_recurrent(x: torch.Tensor, g: torch.Tensor, pool: torch.Tensor, slots: 
     """scan() token by token for a few tokens per sequence, on states in a pool ([P, ...], fp32 or
     bf16), which is updated in place; slots, out_slots and empty places as for recurrent().
     Returns y in x's dtype; out may be x."""
-    d = _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out)
-    d.leaky = int(leaky)
+    d = _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, leaky)
     with _on(x.device, stream) as s:
         y = torch.empty_like(x) if out is None else out
         _call("kda_scan_recurrent", _ptr(x), _ptr(g), _ptr(cu_seqlens), _ptr(slots), _ptr(out_slots), _ptr(pool),
@@ -156,15 +158,15 @@ def scan_recurrent(x: torch.Tensor, g: torch.Tensor, pool: torch.Tensor, slots: 
     return y
 
 
-def _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, _device=True) -> ScanDesc:
-    d = _check_scan(x, g, cu_seqlens, _device)
-    if (pool.dim() < 1 or pool.shape[1:] != x.shape[2:] or not pool.is_contiguous() or pool.dtype not in _TYPES
-            or pool.device != x.device):
+def _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, leaky=False, _device=True) -> ScanDesc:
+    d = _check_scan(x, g, cu_seqlens, leaky, _device)
+    device = x.device
+    if pool.shape[1:] != x.shape[2:] or not pool.is_contiguous() or pool.dtype not in _DTYPES or pool.device != device:
         raise ValueError(f"pool must be a contiguous float32 or bfloat16 [P, {', '.join(map(str, x.shape[2:]))}] tensor on x's device")
     if slots is None and pool.shape[0] < d.num_seqs:
         raise ValueError("pool has fewer slots than there are sequences")
-    for name, t, n in (("slots", slots, d.num_seqs), ("out_slots", out_slots, x.shape[0] * x.shape[1])):
-        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != x.device):
+    for name, t, n in (("slots", slots, d.num_seqs), ("out_slots", out_slots, d.B * d.T)):
+        if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device):
             raise ValueError(f"{name} must be a contiguous int32 tensor of {n} elements on x's device")
     _plain("out", out, x.shape, x.dtype, x.device, _device)
     return d
@@ -172,21 +174,19 @@ def _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, _device
 
 # ------------------------------------------------------- the residual's addition and a norm
 
-def _check_norm(x, residual, weight, _device=True, outs=()) -> NormDesc:
-    if x.dim() < 1 or x.shape[-1] < 1 or x.dtype not in _TYPES:
+def _check_norm(x, residual, weight, _device=True) -> NormDesc:
+    shape, device, dtype = x.shape, x.device, x.dtype
+    if len(shape) < 1 or shape[-1] < 1 or dtype not in _DTYPES:
         raise ValueError("x must be a bfloat16 or float32 [..., C] tensor")
-    C = x.shape[-1]
-    _plain("x", x, x.shape, x.dtype, x.device, _device)
-    _plain("weight", weight, (C,), torch.float32, x.device, _device)
-    res = x.dtype
+    C, res = shape[-1], dtype
+    _rows("x", x, shape, dtype, device, _device)
+    _rows("weight", weight, shape[-1:], torch.float32, device, False)
     if residual is not None:
-        if residual.dtype not in (x.dtype, torch.float32):
-            raise ValueError("residual must have x's dtype or be float32")
         res = residual.dtype
-        _plain("residual", residual, x.shape, res, x.device, _device)
-    for name, t, dtype in outs:
-        _plain(name, t, x.shape, dtype, x.device, _device)
-    return NormDesc(x.numel() // C, C, _DTYPES[x.dtype], _DTYPES[res], None, 0)
+        if res != dtype and res != torch.float32:
+            raise ValueError("residual must have x's dtype or be float32")
+        _rows("residual", residual, shape, res, device, False)
+    return NormDesc(x.numel() // C, C, _DTYPES[dtype], _DTYPES[res], None, 0)
 
 
 def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: float = 1e-5, out: _Tensor = None,
@@ -195,8 +195,8 @@ def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: floa
     weight. x [..., C] bf16 or fp32; residual of the same shape, in x's dtype or fp32, or None
     (r is x then); weight fp32 [C]. Returns (y in x's dtype, r in residual's). out may be x,
     residual_out may be residual (the stream updated in place)."""
-    d = _check_norm(x, residual, weight, outs=(("out", out, x.dtype), ("residual_out", residual_out,
-                                                                        x.dtype if residual is None else residual.dtype)))
+    d = _check_norm(x, residual, weight)
+    _plain("out", out, x.shape, x.dtype, x.device)
     with _on(x.device, stream) as s:
         y = torch.empty_like(x) if out is None else out
         r = _sum_out(x, residual, residual_out)
@@ -210,7 +210,10 @@ def _sum_out(x, residual, residual_out):
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
         return x
-    return torch.empty_like(residual) if residual_out is None else residual_out
+    if residual_out is None:
+        return torch.empty_like(residual)
+    _rows("residual_out", residual_out, residual.shape, residual.dtype, residual.device, False)
+    return residual_out
 
 
 def add_norm_q8(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, group: int = 0, eps: float = 1e-5,
@@ -218,12 +221,12 @@ def add_norm_q8(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, group:
     """add_norm() with y in 8 bits: scale = max(amax |y|, 2^-40) / 448 over a row (group=0) or over
     each 128 channels (group=128, C a multiple of it), and y / scale rounded to
     float8_e4m3fn. Returns (q [..., C], scales fp32 [...] or [..., C / 128], r)."""
-    d = _check_norm(x, residual, weight, outs=(("residual_out", residual_out, x.dtype if residual is None else residual.dtype),))
+    d = _check_norm(x, residual, weight)
     if group not in (0, 128) or (group and d.C % group):
         raise ValueError("group must be 0 (a row) or 128, with a multiple of 128 channels")
     with _on(x.device, stream) as s:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-        scales = x.new_empty((*x.shape[:-1], d.C // group) if group else x.shape[:-1], dtype=torch.float32)
+        scales = weight.new_empty((*x.shape[:-1], d.C // group) if group else x.shape[:-1])
         r = _sum_out(x, residual, residual_out)
         _call("kda_add_norm_q8", _ptr(x), _ptr(residual), _ptr(weight), eps, group, _ptr(q), _ptr(scales),
               _ptr(r) if residual is not None else None, ctypes.byref(d), s)
@@ -256,15 +259,16 @@ def _check_norm_bwd(r, weight, dy, dr, _device=True) -> NormDesc:
 # ------------------------------------------------------- beam search
 
 def _check_beam(logits, scores, k, done, eos, _device=True) -> BeamDesc:
-    if logits.dim() != 3 or logits.dtype not in _TYPES:
+    shape, device = logits.shape, logits.device
+    if len(shape) != 3 or logits.dtype not in _DTYPES:
         raise ValueError("logits must be a bfloat16 or float32 [B, W, V] tensor")
-    B, W, V = logits.shape
-    _plain("logits", logits, logits.shape, logits.dtype, logits.device, _device)
-    _plain("scores", scores, (B, W), torch.float32, logits.device, _device)
+    B, W, V = shape
+    _rows("logits", logits, shape, logits.dtype, device, _device)
+    _rows("scores", scores, shape[:2], torch.float32, device, False)
     if done is not None:
         if done.dtype not in (torch.bool, torch.uint8):
             raise ValueError("done must be a bool or uint8 [B, W] tensor")
-        _plain("done", done, (B, W), done.dtype, logits.device, _device)
+        _rows("done", done, shape[:2], done.dtype, device, False)
         if not 0 <= eos < V:
             raise ValueError("with done, eos must be a token")
     k = W if k is None else k
@@ -285,7 +289,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     with _on(logits.device, stream) as s:
         ws = _workspace(workspace, int(lib().kda_beam_workspace_size(ctypes.byref(d))), logits)
         best = scores.new_empty(d.B, d.K)
-        parents, tokens = scores.new_empty((2, d.B, d.K), dtype=torch.int32)
+        parents = torch.empty_like(best, dtype=torch.int32)
+        tokens = torch.empty_like(parents)
         _call("kda_beam_select", _ptr(logits), _ptr(scores), _ptr(done), _ptr(best), _ptr(parents), _ptr(tokens), _with(d, ws), s)
     return best, parents, tokens
 

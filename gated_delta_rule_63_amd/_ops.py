@@ -29,6 +29,10 @@ def _f32(t: torch.Tensor) -> torch.Tensor:
     return torch.empty_like(t, dtype=torch.float32)   # 1.2 us; torch.empty with shape and device 3.0
 
 
+# the stream's handle without a torch.cuda.Stream around it: 0.1 us against 1.1
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
 class _Here:
     """The call's stream where its device and stream are current already."""
 
@@ -48,7 +52,7 @@ def _on(device: torch.device, stream: Optional[torch.cuda.Stream]):
     contexts costs more than a small kernel: where they would change nothing they are
     left out.)"""
     if stream is None and torch.cuda.current_device() == device.index:
-        return _Here(torch.cuda.current_stream(device.index).cuda_stream)
+        return _Here(_raw_stream(device.index))
     return _there(device, stream)
 
 
