@@ -132,6 +132,8 @@ __device__ __forceinline__ int rank_of(const T* keys, int n, T key) {
     return r;
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));   // (an array of uint4 goes through scratch memory)
+
 template <bool F32> struct Raw { typedef uint16_t type; };
 template <> struct Raw<true> { typedef float type; };
 template <bool F32> using raw_t = typename Raw<F32>::type;
@@ -143,11 +145,10 @@ __device__ __forceinline__ float up(float x) { return x; }
 template <bool F32>
 struct Piece {
     static constexpr int VE = F32 ? 4 : 8;
-    uint4 raw;
+    u32x4 raw;
     __device__ __forceinline__ float operator[](int e) const {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        if constexpr (F32) return __uint_as_float(w[e]);
-        else return __uint_as_float(e & 1 ? w[e / 2] & 0xffff0000u : w[e / 2] << 16);
+        if constexpr (F32) return __uint_as_float(raw[e]);
+        else return __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
     }
 };
 template <bool F32> constexpr int kTile = kThreads * kPieces * Piece<F32>::VE;
@@ -158,7 +159,7 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
     Piece<F32> p;
     const long long at = VE * j - off;
     if (at >= 0 && at + VE <= V) {
-        p.raw = *reinterpret_cast<const uint4*>(row + at * E);
+        p.raw = *reinterpret_cast<const u32x4*>(row + at * E);
     } else {
         uint32_t w[4];
 #pragma unroll
@@ -173,7 +174,7 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
                     w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | h << 16 : (w[e / 2] & 0xffff0000u) | h;
                 }
             }
-        p.raw = make_uint4(w[0], w[1], w[2], w[3]);
+        p.raw = u32x4{w[0], w[1], w[2], w[3]};
     }
     return p;
 }
@@ -183,9 +184,10 @@ __device__ __forceinline__ void ld_tile(Piece<F32> (&x)[kPieces], const char* ro
     constexpr int VE = Piece<F32>::VE;
     const long long j0 = (long long)t * (kThreads * kPieces);
     if (j0 * VE >= off && (j0 + kThreads * kPieces) * VE - off <= V) {
-        const uint4* p = reinterpret_cast<const uint4*>(row - off * (16 / VE)) + j0 + threadIdx.x;
+        // (each is read once: past the caches, 34.6 -> 32.4 us)
+        const u32x4* p = reinterpret_cast<const u32x4*>(row - off * (16 / VE)) + j0 + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[i].raw = p[i * kThreads];
+        for (int i = 0; i < kPieces; ++i) x[i].raw = __builtin_nontemporal_load(p + i * kThreads);
     } else {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, off, j0 + i * kThreads + threadIdx.x, V);
@@ -207,7 +209,7 @@ __device__ __forceinline__ void lds_barrier() {
 // too late.
 template <bool F32>
 __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
-    extern __shared__ uint4 shown[];                // 2 K threads' logits
+    extern __shared__ u32x4 shown[];                // 2 K threads' logits
     uint64_t* const keys = reinterpret_cast<uint64_t*>(shown + 2 * kPieces * a.K);   // up to 2 K from earlier tiles, 64 K of one; K sorted
     __shared__ int owner[2 * kBeamMax], rows[2];    // whose they are; how many, in turn
     __shared__ uint32_t best[2][kThreads], first[kThreads];
@@ -489,7 +491,6 @@ __device__ __forceinline__ Move move_of(const ReorderArgs& a, int b, int j) {
 }
 
 constexpr int kInFlight = 8;    // pieces of a thread
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));   // (an array of uint4 goes through scratch memory)
 
 template <typename T>
 __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, int parts) {
@@ -536,7 +537,9 @@ hipError_t launch_beam_reorder(const ReorderArgs& a, hipStream_t s) {
     if (a.B == 0) return hipSuccess;
     // up to 64 workgroups a copy, one turn each where that is enough (32 KiB at 16 bytes a piece)
     const size_t turns = (a.slot_bytes / a.unit + 256 * kInFlight - 1) / (256 * kInFlight);
-    const int parts = (int)(turns < 1 ? 1 : turns > 64 ? 64 : turns);
+    const size_t most = (size_t)(1 << 22) / ((size_t)a.B * a.W);       // of a launch
+    const size_t cap = most < 1 ? 1 : most < 64 ? most : 64;
+    const int parts = (int)(turns < 1 ? 1 : turns > cap ? cap : turns);
     const unsigned n = (unsigned)(a.B * a.W * parts);
     if (a.unit == 16) hipLaunchKernelGGL(kda_beam_reorder_kernel<u32x4>, dim3(n), dim3(256), 0, s, a, parts);
     else if (a.unit == 4) hipLaunchKernelGGL(kda_beam_reorder_kernel<uint32_t>, dim3(n), dim3(256), 0, s, a, parts);

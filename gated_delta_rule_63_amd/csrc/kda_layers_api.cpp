@@ -63,6 +63,7 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     a->f32 = d->dtype == KDA_F32;
     a->leaky = d->leaky != 0;
     a->width = kda::scan_width(form(d, cu != nullptr, back, known), compute_units());
+    a->fold = (long long)d->T <= 64LL * kda::kScanChunk;
     return KDA_OK;
 }
 
@@ -94,7 +95,7 @@ void cut_scan(kda::ScanArgs* a, const kda_scan_desc_t* d, bool back) {
         a->decays = reinterpret_cast<float*>(w);
         a->adds = reinterpret_cast<float*>(w + row);
         a->grads = reinterpret_cast<float*>(w + 2 * row);
-        if (!back && !a->states) a->states = a->grads;   // which the forward does not have
+        if (!back && !a->states && !a->fold) a->states = a->grads;   // which the forward does not have
     }
 }
 

@@ -31,6 +31,7 @@ struct ScanArgs {
     int T, C, N, slots;
     bool f32, leaky;
     int width;                    // scan_width()
+    bool fold;                    // side by side: a chunk's workgroup folds those before it itself
 };
 
 struct ScanPoolArgs {

@@ -360,6 +360,14 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
     const int strips = (a.C + S - 1) / S;
     const long long slot = blockIdx.x / strips;
     const Lane<S> p(a, blockIdx.x % strips);
+    if (slot >= a.slots) {                         // behind the chunks: sequences without any
+        const int n = (int)(slot - a.slots);
+        const long long at = (long long)n * a.C + p.c;
+        if (p.sub > 0 || !p.on || sequence(a, n).len > 0) return;
+        if (FWD && a.hT) a.hT[at] = a.h0 ? a.h0[at] : 0.f;
+        if (BWD && a.dh0) a.dh0[at] = a.dhT ? a.dhT[at] : 0.f;
+        return;
+    }
     const Run run = sequence(a, sequence_of(a, slot));
     const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
     if (slot < run.slot || t >= run.len) return;   // no chunk
@@ -454,52 +462,100 @@ __global__ __launch_bounds__(SC * NC) void kda_scan_combine(ScanArgs a) {
     else combine<true, SC, NC>(a, i / strips, i % strips, sh);
 }
 
-// A chunk from the state that enters it; the last ones first, since the last-level cache
-// still holds what the sums read last (T = 131072, C = 512: 192 -> 181 us).
-template <bool F32, bool LEAKY>
+// The fold of a sequence's first `count` chunks (BACK: its last), by the workgroup that
+// works on the next one: each wave one run of them, then the runs.
+template <bool BACK>
+__device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chunks, int count, float h, int cc, const Lane<S>& p, float2 (*s)[S]) {
+    const float* const from = BACK ? a.grads : a.adds;
+    const int per = (count + W - 1) / W, first = p.sub * per;
+    float A = 1.f, B = 0.f;
+    for (int i = 0; i < per; i += 8) {             // eight in flight
+        float d[8], b[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int j = first + i + u;
+            const bool on = i + u < per && j < count;
+            const long long at = (run.slot + (BACK ? chunks - 1 - j : j)) * a.C + cc;
+            d[u] = on ? a.decays[at] : 1.f;
+            b[u] = on ? from[at] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            A *= d[u];
+            B = fmaf(d[u], B, b[u]);
+        }
+    }
+    s[p.sub][p.l] = make_float2(A, B);
+    lds_barrier();
+#pragma unroll
+    for (int j = 0; j < W; ++j) h = fmaf(s[j][p.l].x, h, s[j][p.l].y);
+    return h;
+}
+
+// A chunk from the state that enters it (FOLD: which it forms itself); the last ones
+// first, since the last-level cache still holds what the sums read last (T = 131072, C = 512: 192
+// -> 181 us).
+template <bool F32, bool LEAKY, bool FOLD>
 __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
-    __shared__ float2 sh[W][S];
+    __shared__ float2 sh[2][W][S];
     const int strips = (a.C + S - 1) / S;
     const long long slot = a.slots - 1 - blockIdx.x / strips;
     const Lane<S> p(a, blockIdx.x % strips);
-    const int cc = min(p.c, a.C - 1);
-    const Run run = sequence(a, sequence_of(a, slot));
+    const int cc = min(p.c, a.C - 1), n = sequence_of(a, slot);
+    const Run run = sequence(a, n);
     const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
     if (slot < run.slot || t >= run.len) return;
-    const float h = a.states[slot * a.C + cc];
-    a.states = nullptr;                            // they are there
+    float h;
+    if constexpr (FOLD) {
+        h = fold<false>(a, run, 0, t / kScanChunk, a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f, cc, p, sh[1]);
+    } else {
+        h = a.states[slot * a.C + cc];
+        a.states = nullptr;                        // they are there
+    }
     if (t + kScanChunk <= run.len) {
         Tile<true, F32, LEAKY, S> tile;
         tile.get(a, run, p, t);
-        tile.run(a, run, p, t, h, sh, [] {});
+        h = tile.run(a, run, p, t, h, sh[0], [] {});
     } else {
         Tile<false, F32, LEAKY, S> tile;
         tile.get(a, run, p, t);
-        tile.run(a, run, p, t, h, sh, [] {});
+        h = tile.run(a, run, p, t, h, sh[0], [] {});
     }
+    if (FOLD && a.hT && t + kScanChunk >= run.len && p.sub == 0 && p.on) a.hT[(long long)n * a.C + p.c] = h;
 }
 
-template <bool F32, bool LEAKY>
-__global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a) {
-    __shared__ float2 sh[W][S];
+template <bool F32, bool LEAKY, bool FOLD>
+__global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a, bool known) {
+    __shared__ float2 sh[3][W][S];
     __shared__ float sd[W][S];
     const int strips = (a.C + S - 1) / S;
     const long long slot = a.slots - 1 - blockIdx.x / strips;
     const Lane<S> p(a, blockIdx.x % strips);
-    const int cc = min(p.c, a.C - 1);
-    const Run run = sequence(a, sequence_of(a, slot));
+    const int cc = min(p.c, a.C - 1), n = sequence_of(a, slot);
+    const Run run = sequence(a, n);
     const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
     if (slot < run.slot || t >= run.len) return;
-    const float h = a.states[slot * a.C + cc], D = a.grads[slot * a.C + cc];
+    float h, D;
+    if constexpr (FOLD) {
+        const int chunks = (run.len + kScanChunk - 1) / kScanChunk, j = t / kScanChunk;
+        const long long at = (long long)n * a.C + cc;
+        D = fold<true>(a, run, chunks, chunks - 1 - j, a.dhT ? a.dhT[at] : 0.f, cc, p, sh[1]);
+        if (known) h = a.states[slot * a.C + cc];
+        else h = fold<false>(a, run, chunks, j, a.h0 ? a.h0[at] : 0.f, cc, p, sh[2]);
+    } else {
+        h = a.states[slot * a.C + cc];
+        D = a.grads[slot * a.C + cc];
+    }
     if (t + kScanChunk <= run.len) {
         TileBwd<true, F32, LEAKY, S> tile;
         tile.get(a, run, p, t);
-        tile.run(a, run, p, t, h, D, sh, sd, [] {});
+        D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
     } else {
         TileBwd<false, F32, LEAKY, S> tile;
         tile.get(a, run, p, t);
-        tile.run(a, run, p, t, h, D, sh, sd, [] {});
+        D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
     }
+    if (FOLD && a.dh0 && t == 0 && p.sub == 0 && p.on) a.dh0[(long long)n * a.C + p.c] = D;
 }
 
 // ------------------------------------------------------------ token by token
@@ -582,10 +638,13 @@ int scan_width(const ScanForm& f, int cus) {
     const double el = (double)f.rows * f.T * f.C, e = f.f32 ? 4 : 2, len = f.packed && f.N > 1 ? fmin(f.T, 2.0 * f.T / f.N) : f.T;
     const bool first = f.back && !f.known;             // states to be formed
     const double bytes = f.back ? 3 * e + 8 : 2 * e + 4;
-    int best = 0;
-    double least = 12000 + el * (bytes + (first ? 2 * e + 4 : e + 4)) / 4.9e3;
+    // (a launch takes up to 2^22 workgroups; 64 channels a workgroup always fit: N ceil(C / 64) is at most that)
+    const double most = 1 << 22, chunks = ((double)f.rows * f.T / kScanChunk + 2.0 * f.N) * ((f.C + scan::S - 1) / scan::S);
+    int best = chunks > most ? 64 : 0;
+    double least = chunks > most ? HUGE_VAL : 12000 + el * (bytes + (first ? 2 * e + 4 : e + 4)) / 4.9e3;
     for (const auto& s : strip) {
         const double groups = (double)f.N * ((f.C + s.width - 1) / s.width);
+        if (groups > most) continue;
         const double token = (f.back ? s.bwd + (first ? s.fwd : 0) : s.fwd) * (f.leaky ? 1.45 : 1.0);
         const double turns = fmax(1.0, groups / (2.0 * cus)), at = fmin(1.0, 0.5 + 0.5 * groups / (0.6 * cus));
         const double t = fmax(len * token * (f.packed ? 1.0 : turns), el * (bytes + (first ? e + 4 : 0)) / (s.rate * at));
@@ -613,9 +672,14 @@ static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
         else KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
         return hipGetLastError();
     }
+    if (a.fold) {
+        KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks + a.N * strips, 64 * W);
+        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY, true>), chunks, 64 * W);
+        return hipGetLastError();
+    }
     if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks, 64 * W);
     KDA_SCAN_COMBINE(true, false, 1);
-    if (chunks > 0 && a.y) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY>), chunks, 64 * W);
+    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY, false>), chunks, 64 * W);
     return hipGetLastError();
 }
 
@@ -633,14 +697,19 @@ static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
         else KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
         return hipGetLastError();
     }
-    if (known) {
-        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, false, true>), chunks, 64 * W);
-        KDA_SCAN_COMBINE(false, true, 1);
-    } else {
-        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, true>), chunks, 64 * W);
-        KDA_SCAN_COMBINE(true, true, 2);
+    const long long more = a.fold ? a.N * strips : 0;
+    if (chunks + more > 0) {
+        if (known) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, false, true>), chunks + more, 64 * W);
+        else KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, true>), chunks + more, 64 * W);
     }
-    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks_bwd<F32, LEAKY>), chunks, 64 * W);
+    if (!a.fold) {
+        if (known) KDA_SCAN_COMBINE(false, true, 1);
+        else KDA_SCAN_COMBINE(true, true, 2);
+    }
+    if (chunks > 0) {
+        if (a.fold) hipLaunchKernelGGL((kda_scan_chunks_bwd<F32, LEAKY, true>), dim3((unsigned)chunks), dim3(64 * W), 0, s, a, known);
+        else hipLaunchKernelGGL((kda_scan_chunks_bwd<F32, LEAKY, false>), dim3((unsigned)chunks), dim3(64 * W), 0, s, a, known);
+    }
     return hipGetLastError();
 }
 
