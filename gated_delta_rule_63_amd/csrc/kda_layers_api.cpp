@@ -59,7 +59,7 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     *a = kda::ScanArgs{};
     a->x = x; a->g = g; a->cu = cu;
     a->T = d->T; a->C = d->C; a->N = d->num_seqs;
-    a->slots = (int)kda::scan_slots(d->B, d->T, d->num_seqs, cu != nullptr);
+    a->slots = kda::scan_slots(d->B, d->T, d->num_seqs, cu != nullptr);
     a->f32 = d->dtype == KDA_F32;
     a->leaky = d->leaky != 0;
     a->width = kda::scan_width(form(d, cu != nullptr, back, known), compute_units());

@@ -28,7 +28,8 @@ struct ScanArgs {
     float* decays;
     float* adds;
     float* grads;
-    int T, C, N, slots;
+    int T, C, N;
+    long long slots;
     bool f32, leaky;
     int width;                    // scan_width()
     bool fold;                    // side by side: a chunk's workgroup folds those before it itself

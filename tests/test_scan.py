@@ -325,6 +325,22 @@ def test_scan_recurrent(kda, lens, T, N, C, dtype, pool_dtype, leaky, keep):
 
 
 @pytest.mark.gpu
+def test_unaligned_tensors(kda):
+    """Tensors that start on no 16 bytes give the same bits."""
+    s = make(5, 3, 128, "bfloat16", None, False, 12)
+    x, g, dy, pool = on(s["x"]), on(s["g"]), on(s["dy"]), torch.randn(5, 128, device="cuda")
+    flat = lambda t: torch.cat([t.new_zeros(1), t.reshape(-1)])[1:].reshape(t.shape)
+    ux, ug, udy, up = flat(x), flat(g), flat(dy), flat(pool)
+    assert ux.data_ptr() % 16 and up.data_ptr() % 16
+    assert torch.equal(kda.scan_recurrent(x, g, pool), kda.scan_recurrent(ux, ug, up)) and torch.equal(pool, up)
+    y, hT, kept = kda.scan(x, g, initial_state=pool, output_chunk_states=True)
+    uy, uhT, ukept = kda.scan(ux, ug, initial_state=up, output_chunk_states=True)
+    assert torch.equal(y, uy) and torch.equal(hT, uhT) and torch.equal(kept, ukept)
+    for a, b in zip(kda.scan_bwd(x, g, dy, initial_state=pool, d_final_state=hT), kda.scan_bwd(ux, ug, udy, initial_state=up, d_final_state=flat(hT))):
+        assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
 def test_prompt_then_tokens(kda):
     """A prompt by scan() into a slot of the pool, then token by token, against the whole."""
     s = make(1, 150, 4 * 32, "float32", None, False, 10)
