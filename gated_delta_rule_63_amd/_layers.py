@@ -91,7 +91,7 @@ def scan(x: torch.Tensor, g: torch.Tensor, cu_seqlens: _Tensor = None, initial_s
     in fp32, and with output_chunk_states the states that enter each chunk of 128 tokens,
     which scan_bwd() takes ([B, ceil(T / 128), ...]; packed [1, T // 128 + N, ...], where
     sequence n's begin at row cu[n] // 128 + n and rows without a chunk are unset), else
-    None. out may be x. workspace: an optional device tensor of scan_workspace_size() bytes,
+    None. out may be x, final_state initial_state. workspace: an optional device tensor of scan_workspace_size() bytes,
     used by one call at a time; allocated otherwise."""
     d = _check_scan(x, g, cu_seqlens, leaky)
     state = _scan_state(d, x)
@@ -302,6 +302,8 @@ def _check_reorder(pool, slots, parents, out, _device=True):
         raise ValueError("slots must be [B, W] with 1 to 64 beams")
     for name, t in (("slots", slots), ("parents", parents), ("out", out)):
         _plain(name, t, slots.shape, torch.int32, pool.device, _device)
+    if out is not None and out.data_ptr() in (slots.data_ptr(), parents.data_ptr()) and out.numel():
+        raise ValueError("out may not be slots or parents")
 
 
 def beam_reorder(pool: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor, out: _Tensor = None,

@@ -63,9 +63,12 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     a->f32 = d->dtype == KDA_F32;
     a->leaky = d->leaky != 0;
     a->width = kda::scan_width(form(d, cu != nullptr, back, known), compute_units());
-    a->fold = (long long)d->T <= 64LL * kda::kScanChunk;
     return KDA_OK;
 }
+
+// Whether a chunk's workgroup folds the chunks before it itself. (Each then reads the start
+// state, so that the last one may not be written in its place.)
+bool short_enough(const kda_scan_desc_t* d) { return (long long)d->T <= 64LL * kda::kScanChunk; }
 
 // Rows for either use of the descriptor (it does not say whether cu_seqlens comes with it).
 long long most_slots(const kda_scan_desc_t* d) {
@@ -156,6 +159,7 @@ kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, 
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.h0 = h0; a.y = y; a.hT = hT; a.states = states;
+    a.fold = short_enough(desc) && h0 != hT;
     cut_scan(&a, desc, false);
     return status(kda::launch_scan(a, static_cast<hipStream_t>(stream)));
 }
@@ -178,6 +182,7 @@ kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqle
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.states = const_cast<float*>(states);
+    a.fold = short_enough(desc) && dhT != dh0;
     cut_scan(&a, desc, true);
     a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dg = dg; a.dh0 = dh0;
     return status(kda::launch_scan_bwd(a, states != nullptr, static_cast<hipStream_t>(stream)));

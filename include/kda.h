@@ -488,8 +488,8 @@ size_t kda_block_out_bwd_workspace_size(const kda_desc_t* desc);
  *             without a chunk are left as they were.
  * C is any number of channels (heads times head size, say); nothing needs more
  * alignment than its type. g is usually <= 0; -inf is a reset (nothing of the
- * state before it remains), and finite g > 0 a growing state. The state is fp32.
- * y == x is allowed; rows of tokens outside [cu[0], cu[N]) are left as they were;
+ * state before it remains), and g > 0 a growing state (above 88 its decay is not a number).
+ * The state is fp32. y == x and hT == h0 are allowed; rows of tokens outside [cu[0], cu[N]) are left as they were;
  * a zero-length sequence has hT = h0. T is at most 2^30, B T C 2^40, C 2^20 and
  * N ceil(C / 64) 2^22 (KDA_ERR_SHAPE). Needs desc->workspace of
  * kda_scan_workspace_size(desc) bytes (0 for most shapes; KDA_ERR_WORKSPACE),
@@ -514,7 +514,7 @@ int64_t kda_scan_states_rows(const kda_scan_desc_t* desc, int32_t packed);
  * [N, C] (fp32, NULL: zero) the gradients with respect to its outputs; dx (dtype),
  * dg (fp32) and dh0 (fp32, NULL: not written) the results. states: what the
  * forward wrote, or NULL: recomputed from x and g in the workspace. dg is zero
- * where the decay is. dx == dy is allowed; no other output may overlap an input.
+ * where the decay is. dx == dy and dh0 == dhT are allowed; no other output may overlap an input.
  * Needs desc->workspace of kda_scan_bwd_workspace_size(desc, states != NULL) bytes. */
 kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqlens, const float* h0,
                           const float* states, const void* dy, const float* dhT, void* dx, float* dg, float* dh0,

@@ -64,7 +64,8 @@ def test_binding_refusals():
             ok(**kw)
     re = lambda pool=z(9, 4), s=i(2, 3), p=i(2, 3), out=None: M._check_reorder(pool, s, p, out, _device=False)
     re()
-    for kw in (dict(pool=z(4, 9).T), dict(s=i(6)), dict(p=i(2, 4)), dict(p=z(2, 3)), dict(out=i(3, 2)), dict(s=i(2, 65), p=i(2, 65))):
+    same = i(2, 3)
+    for kw in (dict(s=same, out=same), dict(p=same, out=same), dict(pool=z(4, 9).T), dict(s=i(6)), dict(p=i(2, 4)), dict(p=z(2, 3)), dict(out=i(3, 2)), dict(s=i(2, 65), p=i(2, 65))):
         with pytest.raises(ValueError):
             re(**kw)
 

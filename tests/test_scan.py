@@ -243,6 +243,32 @@ def test_rows_outside_the_sequences_and_in_place(kda):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,C", [(300, 40), (8000, 40), (9000, 40), (150, 10400)])
+def test_states_in_place(kda, T, C):
+    """The last state written over the first one, and the gradients' alike, in each form."""
+    s = make(1, T, C, "bfloat16", None, True, 13)
+    x, g, dy, h0, dhT = (on(s[n]) for n in ("x", "g", "dy", "h0", "dhT"))
+    y, hT, kept = kda.scan(x, g, initial_state=h0, output_chunk_states=True)
+    h = h0.clone()
+    y2, out, _ = kda.scan(x, g, initial_state=h, final_state=h)
+    bound = 2 * 500 * 6 * R.U                      # (the folds may be grouped otherwise: two results within one bound)
+    assert out is h and float((h - hT).abs().max()) <= bound * float(hT.abs().max())
+    assert float((y2.float() - y.float()).abs().max()) <= (2.0 ** -7 + bound) * float(y.float().abs().max())
+    desc = kda._lib.ScanDesc(1, T, C, 1, 0, 0, None, 0)
+    need = kda.lib().kda_scan_bwd_workspace_size(ctypes.byref(desc), 1)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    desc.workspace, desc.workspace_bytes = ws.data_ptr(), need
+    dx, dg, dh0 = kda.scan_bwd(x, g, dy, initial_state=h0, d_final_state=dhT, chunk_states=kept)
+    d, dx2, dg2, p = dhT.clone(), torch.empty_like(dx), torch.empty_like(dg), lambda t: ctypes.c_void_p(t.data_ptr())
+    assert kda.lib().kda_scan_bwd(p(x), p(g), None, p(h0), p(kept), p(dy), p(d), p(dx2), p(dg2), p(d), ctypes.byref(desc),
+                                  torch.cuda.current_stream().cuda_stream) == 0
+    torch.cuda.synchronize()
+    assert float((d - dh0).abs().max()) <= bound * float(dh0.abs().max())
+    assert float((dg2 - dg).abs().max()) <= bound * float(dg.abs().max())
+    assert float((dx2.float() - dx.float()).abs().max()) <= (2.0 ** -7 + bound) * float(dx.float().abs().max())
+
+
+@pytest.mark.gpu
 def test_empty_calls(kda):
     z = lambda *s: torch.zeros(*s, device="cuda")
     h0 = torch.ones(2, 5, device="cuda")
