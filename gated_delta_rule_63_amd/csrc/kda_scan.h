@@ -33,6 +33,7 @@ struct ScanArgs {
     bool f32, leaky;
     int width;                    // scan_width()
     bool fold;                    // side by side: a chunk's workgroup folds those before it itself
+    bool stream;                  // more bytes than the last-level cache holds
 };
 
 struct ScanPoolArgs {

@@ -21,6 +21,12 @@ namespace scan {
 constexpr int L = 16;             // tokens of a wave
 constexpr int S = kScanStrip;
 constexpr int W = 8;              // waves of a workgroup
+// Calls that move more than the last-level cache holds send what they write past it, and what
+// they read once in whole lines (the cache then keeps what is read again): 8192 x 12288
+// 166 -> 156 us, 8192 x 8192 its gradient 203 -> 195 and without states 286 -> 259,
+// 131072 x 512 183 -> 166; strips of 16 channels lose by it (131072 x 4096: 1059 -> 1199).
+constexpr int kPast = 2;          // the buffer instructions' streaming bit
+constexpr double kCache = 256.0 * (1 << 20);
 
 // A workgroup barrier for what passes through LDS: loads and stores of device
 // memory stay in flight across it.
@@ -139,25 +145,25 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* p, const Run&
     const int left = ALL ? 0 : max(run.len - t - q.first, 0);
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, ALL ? -1 : (int)(left * (uint32_t)C * sizeof(T)), 0x00020000);
 }
-template <bool ALL, typename T, int SW>
+template <bool ALL, int AUX, typename T, int SW>
 __device__ __forceinline__ void load(T (&v)[L], const void* p, const Run& run, int C, const Lane<SW>& q, int t) {
     const __amdgpu_buffer_rsrc_t r = rows<ALL, T>(p, run, C, q, t);
     const int at = q.off * (int)sizeof(T), step = C * (int)sizeof(T);
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-        if constexpr (sizeof(T) == 2) v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
-        else v[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, ALL ? at : at + i * step, ALL ? i * step : 0, 0));
+        if constexpr (sizeof(T) == 2) v[i] = __builtin_amdgcn_raw_buffer_load_b16(r, ALL ? at : at + i * step, ALL ? i * step : 0, AUX);
+        else v[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, ALL ? at : at + i * step, ALL ? i * step : 0, AUX));
     }
 }
-template <bool ALL, typename T, int SW>
+template <bool ALL, int AUX, typename T, int SW>
 __device__ __forceinline__ void store(const T (&v)[L], void* p, const Run& run, int C, const Lane<SW>& q, int t) {
     const __amdgpu_buffer_rsrc_t r = rows<ALL, T>(p, run, C, q, t);
     const int at = q.off * (int)sizeof(T), step = C * (int)sizeof(T);
     if (!q.on) return;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
-        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(v[i], r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, ALL ? at : at + i * step, ALL ? i * step : 0, 0);
+        if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16(v[i], r, ALL ? at : at + i * step, ALL ? i * step : 0, AUX);
+        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[i]), r, ALL ? at : at + i * step, ALL ? i * step : 0, AUX);
     }
 }
 
@@ -169,14 +175,14 @@ __device__ __forceinline__ int strip_of(int i, int strips) {
 }
 
 // One tile forwards, from the state h that enters it to the one that leaves it.
-template <bool ALL, bool F32, bool LEAKY, int SW>
+template <bool ALL, bool F32, bool LEAKY, int SW, int LD, int ST>
 struct Tile {
     static constexpr int NS = 64 * W / SW;
     raw_t<F32> x[L];
     float g[L];
     __device__ __forceinline__ void get(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t) {
-        load<ALL>(x, a.x, run, a.C, p, t);
-        load<ALL>(g, a.g, run, a.C, p, t);
+        load<ALL, LD>(x, a.x, run, a.C, p, t);
+        load<ALL, LD>(g, a.g, run, a.C, p, t);
     }
     // what becomes of x and g; `next` is fetched meanwhile
     template <typename N>
@@ -214,7 +220,7 @@ struct Tile {
                 in = fmaf(d[i], in, b[i]);
                 y[i] = down<F32>(in);
             }
-            store<ALL>(y, a.y, run, a.C, p, t);
+            store<ALL, ST>(y, a.y, run, a.C, p, t);
         }
         return h;
     }
@@ -222,8 +228,9 @@ struct Tile {
 
 // One workgroup a (sequence, strip): tiles of W * L tokens one after the other, the next
 // one's rows fetched while one is worked on.
-template <bool F32, bool LEAKY, int SW>
+template <bool F32, bool LEAKY, int SW, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
+    constexpr int LD = STREAM && SW == 64 ? kPast : 0, ST = STREAM && SW > 16 ? kPast : 0;
     constexpr int NS = 64 * W / SW, TILE = NS * L;
     __shared__ float2 sh[2][NS][SW];
     const int strips = (a.C + SW - 1) / SW, n = by_length(a, blockIdx.x / strips);
@@ -234,7 +241,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
     const int whole = run.len / TILE;
     int t = 0;
     if (whole > 0) {
-        Tile<true, F32, LEAKY, SW> tile;
+        Tile<true, F32, LEAKY, SW, LD, ST> tile;
         tile.get(a, run, p, 0);
         for (int k = 0; k < whole; ++k, t += TILE)
             h = tile.run(a, run, p, t, h, sh[k & 1], [&] {
@@ -242,7 +249,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
             });
     }
     if (t < run.len) {
-        Tile<false, F32, LEAKY, SW> tile;
+        Tile<false, F32, LEAKY, SW, LD, ST> tile;
         tile.get(a, run, p, t);
         h = tile.run(a, run, p, t, h, sh[whole & 1], [] {});
     }
@@ -251,15 +258,15 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
 
 // One tile backwards, from the gradient D that enters it from behind and the state h
 // that entered it to the gradient that leaves it.
-template <bool ALL, bool F32, bool LEAKY, int SW>
+template <bool ALL, bool F32, bool LEAKY, int SW, int LD, int ST>
 struct TileBwd {
     static constexpr int NS = 64 * W / SW;
     raw_t<F32> x[L], dy[L];
     float g[L];
     __device__ __forceinline__ void get(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t) {
-        load<ALL>(x, a.x, run, a.C, p, t);
-        load<ALL>(g, a.g, run, a.C, p, t);
-        load<ALL>(dy, a.dy, run, a.C, p, t);
+        load<ALL, LD>(x, a.x, run, a.C, p, t);
+        load<ALL, LD>(g, a.g, run, a.C, p, t);
+        load<ALL, LD>(dy, a.dy, run, a.C, p, t);
     }
     template <typename N>
     __device__ __forceinline__ float run(const ScanArgs& a, const Run& run, const Lane<SW>& p, int t, float h, float D,
@@ -309,15 +316,16 @@ struct TileBwd {
             v[i] *= dd;
             into = d[i] * dd;
         }
-        store<ALL>(dx, a.dx, run, a.C, p, t);
-        store<ALL>(v, a.dg, run, a.C, p, t);
+        store<ALL, ST>(dx, a.dx, run, a.C, p, t);
+        store<ALL, ST>(v, a.dg, run, a.C, p, t);
         return D;
     }
 };
 
 // The gradient, tiles from the last to the first, each from the kept state that enters it.
-template <bool F32, bool LEAKY, int SW>
+template <bool F32, bool LEAKY, int SW, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
+    constexpr int LD = STREAM && SW == 64 ? kPast : 0, ST = STREAM && SW > 16 ? kPast : 0;
     constexpr int NS = 64 * W / SW, TILE = NS * L;
     __shared__ float2 sh[2][NS][SW];
     __shared__ float sd[2][NS][SW];
@@ -329,12 +337,12 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
     float D = a.dhT ? a.dhT[(long long)n * a.C + cc] : 0.f;
     const int whole = run.len / TILE;
     if (whole * TILE < run.len) {
-        TileBwd<false, F32, LEAKY, SW> tile;
+        TileBwd<false, F32, LEAKY, SW, LD, ST> tile;
         tile.get(a, run, p, whole * TILE);
         D = tile.run(a, run, p, whole * TILE, state(whole * TILE), D, sh[whole & 1], sd[whole & 1], [] {});
     }
     if (whole > 0) {
-        TileBwd<true, F32, LEAKY, SW> tile;
+        TileBwd<true, F32, LEAKY, SW, LD, ST> tile;
         tile.get(a, run, p, (whole - 1) * TILE);
         float next = state((whole - 1) * TILE);
         for (int k = whole - 1; k >= 0; --k) {
@@ -373,9 +381,9 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
     if (slot < run.slot || t >= run.len) return;   // no chunk
     raw_t<F32> x[L], dy[L];
     float g[L];
-    load<false>(g, a.g, run, a.C, p, t);
-    if constexpr (FWD) load<false>(x, a.x, run, a.C, p, t);
-    if constexpr (BWD) load<false>(dy, a.dy, run, a.C, p, t);
+    load<false, 0>(g, a.g, run, a.C, p, t);
+    if constexpr (FWD) load<false, 0>(x, a.x, run, a.C, p, t);
+    if constexpr (BWD) load<false, 0>(dy, a.dy, run, a.C, p, t);
     float d[L], A = 1.f, B = 0.f, E = 0.f;
 #pragma unroll
     for (int i = 0; i < L; ++i) {
@@ -495,8 +503,9 @@ __device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chu
 // A chunk from the state that enters it (FOLD: which it forms itself); the last ones
 // first, since the last-level cache still holds what the sums read last (T = 131072, C = 512: 192
 // -> 181 us).
-template <bool F32, bool LEAKY, bool FOLD>
+template <bool F32, bool LEAKY, bool FOLD, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
+    constexpr int ST = STREAM ? kPast : 0;
     __shared__ float2 sh[2][W][S];
     const int strips = (a.C + S - 1) / S;
     const long long slot = a.slots - 1 - blockIdx.x / strips;
@@ -513,19 +522,20 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
         a.states = nullptr;                        // they are there
     }
     if (t + kScanChunk <= run.len) {
-        Tile<true, F32, LEAKY, S> tile;
+        Tile<true, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
         h = tile.run(a, run, p, t, h, sh[0], [] {});
     } else {
-        Tile<false, F32, LEAKY, S> tile;
+        Tile<false, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
         h = tile.run(a, run, p, t, h, sh[0], [] {});
     }
     if (FOLD && a.hT && t + kScanChunk >= run.len && p.sub == 0 && p.on) a.hT[(long long)n * a.C + p.c] = h;
 }
 
-template <bool F32, bool LEAKY, bool FOLD>
+template <bool F32, bool LEAKY, bool FOLD, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a, bool known) {
+    constexpr int ST = STREAM ? kPast : 0;
     __shared__ float2 sh[3][W][S];
     __shared__ float sd[W][S];
     const int strips = (a.C + S - 1) / S;
@@ -547,11 +557,11 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks_bwd(ScanArgs a, bool k
         D = a.grads[slot * a.C + cc];
     }
     if (t + kScanChunk <= run.len) {
-        TileBwd<true, F32, LEAKY, S> tile;
+        TileBwd<true, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
         D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
     } else {
-        TileBwd<false, F32, LEAKY, S> tile;
+        TileBwd<false, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
         D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
     }
@@ -662,24 +672,37 @@ int scan_width(const ScanForm& f, int cus) {
         else KDA_SCAN_LAUNCH((kda_scan_combine<fwd, bwd, 16, 64>), n * a.N * ((a.C + 15LL) / 16), 1024);       \
     } while (0)
 
+#define KDA_SCAN_WALK(kernel)                                                                                  \
+    do {                                                                                                       \
+        if (a.width == 64 && a.stream) KDA_SCAN_LAUNCH((kernel<F32, LEAKY, 64, true>), a.N * strips, 64 * W);  \
+        else if (a.width == 64) KDA_SCAN_LAUNCH((kernel<F32, LEAKY, 64, false>), a.N * strips, 64 * W);        \
+        else if (a.width == 32 && a.stream)                                                                    \
+            KDA_SCAN_LAUNCH((kernel<F32, LEAKY, 32, true>), a.N * ((a.C + 31LL) / 32), 64 * W);                \
+        else if (a.width == 32) KDA_SCAN_LAUNCH((kernel<F32, LEAKY, 32, false>), a.N * ((a.C + 31LL) / 32), 64 * W); \
+        else KDA_SCAN_LAUNCH((kernel<F32, LEAKY, 16, false>), a.N * ((a.C + 15LL) / 16), 64 * W);              \
+    } while (0)
+#define KDA_SCAN_CHUNKS(kernel, ...)                                                                           \
+    do {                                                                                                       \
+        if (chunks == 0) break;                                                                                \
+        const dim3 n((unsigned)chunks), t(64 * W);                                                             \
+        if (a.fold && a.stream) hipLaunchKernelGGL((kernel<F32, LEAKY, true, true>), n, t, 0, s, __VA_ARGS__); \
+        else if (a.fold) hipLaunchKernelGGL((kernel<F32, LEAKY, true, false>), n, t, 0, s, __VA_ARGS__);       \
+        else if (a.stream) hipLaunchKernelGGL((kernel<F32, LEAKY, false, true>), n, t, 0, s, __VA_ARGS__);     \
+        else hipLaunchKernelGGL((kernel<F32, LEAKY, false, false>), n, t, 0, s, __VA_ARGS__);                  \
+    } while (0)
+
 template <bool F32, bool LEAKY>
 static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
     using namespace scan;
     const long long strips = (a.C + S - 1) / S, chunks = a.slots * strips;
     if (a.width > 0) {
-        if (a.width == 64) KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 64>), a.N * strips, 64 * W);
-        else if (a.width == 32) KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 32>), a.N * ((a.C + 31LL) / 32), 64 * W);
-        else KDA_SCAN_LAUNCH((kda_scan_walk<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
+        KDA_SCAN_WALK(kda_scan_walk);
         return hipGetLastError();
     }
-    if (a.fold) {
-        KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks + a.N * strips, 64 * W);
-        if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY, true>), chunks, 64 * W);
-        return hipGetLastError();
-    }
-    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks, 64 * W);
-    KDA_SCAN_COMBINE(true, false, 1);
-    if (chunks > 0) KDA_SCAN_LAUNCH((kda_scan_chunks<F32, LEAKY, false>), chunks, 64 * W);
+    const long long more = a.fold ? a.N * strips : 0;
+    if (chunks + more > 0) KDA_SCAN_LAUNCH((kda_scan_sums<F32, LEAKY, true, false>), chunks + more, 64 * W);
+    if (!a.fold) KDA_SCAN_COMBINE(true, false, 1);
+    KDA_SCAN_CHUNKS(kda_scan_chunks, a);
     return hipGetLastError();
 }
 
@@ -692,9 +715,7 @@ static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
             const hipError_t e = scan_fwd<F32, LEAKY>(a, s);   // y is not there: states only
             if (e != hipSuccess) return e;
         }
-        if (a.width == 64) KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 64>), a.N * strips, 64 * W);
-        else if (a.width == 32) KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 32>), a.N * ((a.C + 31LL) / 32), 64 * W);
-        else KDA_SCAN_LAUNCH((kda_scan_walk_bwd<F32, LEAKY, 16>), a.N * ((a.C + 15LL) / 16), 64 * W);
+        KDA_SCAN_WALK(kda_scan_walk_bwd);
         return hipGetLastError();
     }
     const long long more = a.fold ? a.N * strips : 0;
@@ -706,19 +727,23 @@ static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
         if (known) KDA_SCAN_COMBINE(false, true, 1);
         else KDA_SCAN_COMBINE(true, true, 2);
     }
-    if (chunks > 0) {
-        if (a.fold) hipLaunchKernelGGL((kda_scan_chunks_bwd<F32, LEAKY, true>), dim3((unsigned)chunks), dim3(64 * W), 0, s, a, known);
-        else hipLaunchKernelGGL((kda_scan_chunks_bwd<F32, LEAKY, false>), dim3((unsigned)chunks), dim3(64 * W), 0, s, a, known);
-    }
+    KDA_SCAN_CHUNKS(kda_scan_chunks_bwd, a, known);
     return hipGetLastError();
 }
 
-hipError_t launch_scan(const ScanArgs& a, hipStream_t s) {
+static ScanArgs with_stream(ScanArgs a, double bytes) {
+    a.stream = (double)(a.cu ? 1 : a.N) * a.T * a.C * bytes > scan::kCache;
+    return a;
+}
+
+hipError_t launch_scan(const ScanArgs& args, hipStream_t s) {
+    const ScanArgs a = with_stream(args, args.f32 ? 12 : 8);
     if (a.f32) return a.leaky ? scan_fwd<true, true>(a, s) : scan_fwd<true, false>(a, s);
     return a.leaky ? scan_fwd<false, true>(a, s) : scan_fwd<false, false>(a, s);
 }
 
-hipError_t launch_scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
+hipError_t launch_scan_bwd(const ScanArgs& args, bool known, hipStream_t s) {
+    const ScanArgs a = with_stream(args, args.f32 ? 20 : 14);
     if (a.f32) return a.leaky ? scan_bwd<true, true>(a, known, s) : scan_bwd<true, false>(a, known, s);
     return a.leaky ? scan_bwd<false, true>(a, known, s) : scan_bwd<false, false>(a, known, s);
 }
