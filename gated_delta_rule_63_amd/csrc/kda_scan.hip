@@ -142,7 +142,7 @@ struct Lane {
 template <bool ALL, typename T, int SW>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows(const void* p, const Run& run, int C, const Lane<SW>& q, int t) {
     const T* base = static_cast<const T*>(p) + (run.tok + t + q.first) * C;
-    const int left = ALL ? 0 : max(run.len - t - q.first, 0);
+    const int left = ALL ? 0 : min(max(run.len - t - q.first, 0), 64 / SW * L);   // of the wave's rows: the size is 32 bits
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<T*>(base), (short)0, ALL ? -1 : (int)(left * (uint32_t)C * sizeof(T)), 0x00020000);
 }
 template <bool ALL, int AUX, typename T, int SW>

@@ -300,6 +300,36 @@ def test_beyond_32_bit_offsets(kda):
     assert float((dg[:, cut:] - sg).abs().max()) <= 4 * 20 * 6 * R.U * float(sg.abs().max())
 
 
+@pytest.mark.gpu
+def test_four_gibibytes_of_a_sequence(kda):
+    """Few channels over so many tokens that the rows left from a token on are 2^32 bytes and some.
+    Decays of one between resets every 100 tokens, inputs of -1, 0 and 1: all sums are exact."""
+    C, every = 64, 100
+    T = (1 << 24) + 64
+    cycle = torch.randint(-1, 2, (every, C), generator=torch.Generator("cuda").manual_seed(2), device="cuda")
+    x = torch.empty(T, C, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(T, C, device="cuda")
+    g[::every] = float("-inf")
+    want = torch.empty_like(x)
+    ahead = torch.empty_like(x)                     # sums to the next reset: of dx with dy = x
+    whole = T // every * every
+    x[:whole].view(-1, every, C)[:] = cycle
+    x[whole:] = cycle[:T - whole]
+    want[:whole].view(-1, every, C)[:] = cycle.cumsum(0)
+    want[whole:] = cycle.cumsum(0)[:T - whole]
+    ahead[:whole].view(-1, every, C)[:] = cycle.flip(0).cumsum(0).flip(0)
+    ahead[whole:] = cycle[:T - whole].flip(0).cumsum(0).flip(0)
+    y, hT, kept = kda.scan(x[None], g[None], output_chunk_states=True)
+    assert torch.equal(y[0], want) and torch.equal(hT[0], want[-1].float())
+    assert torch.equal(kept[0, 1:], want[127::128][:kept.shape[1] - 1].float())
+    for states in (kept, None):
+        dx, dg, _ = kda.scan_bwd(x[None], g[None], x[None], chunk_states=states)
+        assert torch.equal(dx[0], ahead)
+        assert torch.equal(dg[0, 1:every], want[:every - 1].float() * ahead[1:every].float())
+        assert torch.equal(dg[0, 1 - every - T % every:][:every - 1], dg[0, 1:every]) and not dg[0, ::every].any()
+        del dx, dg
+
+
 POOL = [  # lengths, T, N, C, inputs, pool, leaky, out_slots
     (None, 1, 1, 1, "float32", "float32", False, False),
     (None, 1, 70, 128, "bfloat16", "bfloat16", False, False),
