@@ -66,9 +66,16 @@ kda_status_t scan_args(kda::ScanArgs* a, const void* x, const float* g, const in
     return KDA_OK;
 }
 
-// Whether a chunk's workgroup folds the chunks before it itself. (Each then reads the start
-// state, so that the last one may not be written in its place.)
-bool short_enough(const kda_scan_desc_t* d) { return (long long)d->T <= 64LL * kda::kScanChunk; }
+// Whether a chunk's workgroup folds the chunks before it itself: a launch less, for reading
+// half of all chunks' maps once a chunk, from the caches. (8192 x 512: 20.3 -> 17.0 us, 16384 x 512:
+// 26.8 -> 24.8, 12288 x 1024: 34.1 -> 32.5; 8192 x 2048: the same; 24000 x 512: 34.6 -> 35.4,
+// 32768 x 512: 45.4 -> 48.7.) Each reads the start state, so that the last one may not be
+// written in its place.
+bool folds(const kda_scan_desc_t* d, bool packed) {
+    const double T = d->T, N = d->num_seqs, len = packed && N > 1 ? std::min(T, 2 * T / N) : T;
+    const double chunks = len / kda::kScanChunk;
+    return T <= 256.0 * kda::kScanChunk && N * chunks * chunks * d->C <= 12e6;
+}
 
 // Rows for either use of the descriptor (it does not say whether cu_seqlens comes with it).
 long long most_slots(const kda_scan_desc_t* d) {
@@ -129,7 +136,7 @@ kda_status_t add_norm(bool q8, const void* x, const void* res, const float* weig
     if (group != 0 && (group != 128 || d->C % 128 || !aligned16(x, res, weight, y, res ? r : nullptr))) return KDA_ERR_UNSUPPORTED;
     kda::NormArgs a = norm_args(weight, eps, d, res != nullptr);
     a.x = x; a.res = res; a.y = y; a.r = r; a.scales = scales;
-    a.q8 = q8; a.group = group;
+    a.q8 = q8; a.group = d->C == 128 ? 0 : group;      // (then the row is the group)
     a.vec = d->C % 8 == 0 && aligned16(x, res, weight, y, res ? r : nullptr);
     return status(kda::launch_add_norm(a, static_cast<hipStream_t>(stream)));
 }
@@ -159,7 +166,7 @@ kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, 
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.h0 = h0; a.y = y; a.hT = hT; a.states = states;
-    a.fold = short_enough(desc) && h0 != hT;
+    a.fold = folds(desc, cu_seqlens != nullptr) && h0 != hT;
     cut_scan(&a, desc, false);
     return status(kda::launch_scan(a, static_cast<hipStream_t>(stream)));
 }
@@ -182,7 +189,7 @@ kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqle
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.states = const_cast<float*>(states);
-    a.fold = short_enough(desc) && dhT != dh0;
+    a.fold = folds(desc, cu_seqlens != nullptr) && dhT != dh0;
     cut_scan(&a, desc, true);
     a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dg = dg; a.dh0 = dh0;
     return status(kda::launch_scan_bwd(a, states != nullptr, static_cast<hipStream_t>(stream)));

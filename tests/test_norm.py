@@ -137,7 +137,7 @@ def make(rows, C, dtype, res, seed):
 
 
 SHAPES = [(1, 1), (3, 7), (5, 8), (37, 64), (2, 100), (130, 128), (9, 512), (3, 520), (4, 1000), (33, 2048), (3, 2049), (5, 4096),
-          (2, 4104), (3, 8192), (2, 8200), (2, 12288), (1, 16384), (2, 9001), (3, 16383), (700, 136), (301, 100), (67, 250), (9, 256)]
+          (2, 4104), (3, 8192), (2, 8200), (2, 12288), (1, 16384), (2, 9001), (3, 16383), (700, 136), (301, 100), (67, 250), (9, 256), (65, 1024), (130, 600)]
 TYPES = [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "float32"), ("bfloat16", None), ("float32", None)]
 
 
@@ -208,6 +208,43 @@ def test_many_rows(kda):
     d, sums, bd, bw = grad(r64, w.double().numpy(), dy.double().numpy(), dr.double().numpy())
     R.held(as64(dx), d, bd, "dx")
     R.held(as64(dw), sums, bw, "dw", rms=1e-5)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [96, 256, 1000, 2048, 9008])
+@pytest.mark.parametrize("mib", [300, 700])
+@pytest.mark.parametrize("dtype,res", TYPES)
+def test_calls_beyond_the_cache(kda, dtype, res, mib, C):
+    """Rows of large calls have the bits of the same rows in small ones; dweight from the few rows
+    that add to it."""
+    dt, rt = getattr(torch, dtype), getattr(torch, res or dtype)
+    e, re = dt.itemsize, rt.itemsize
+    gen = torch.Generator("cuda").manual_seed(5)
+    many = lambda n, t: torch.empty(n, C, dtype=t, device="cuda").normal_(generator=gen)
+    w = 1 + 0.3 * many(1, torch.float32)[0]
+    for part, size in (("y", e + e + (2 * re if res else 0)), ("q8", e + 1 + (2 * re if res else 0)), ("bwd", 2 * e + 3 * re)):
+        n = (mib << 20) // (size * C)
+        x = many(n, dt)
+        r0 = many(n, rt) if res or part == "bwd" else None
+        places = [slice(0, 70), slice(n // 2 - 35, n // 2 + 35), slice(n - 70, n)]
+        cut = lambda t, at: None if t is None else t[at].clone()
+        if part == "bwd":
+            x[torch.arange(n, device="cuda") % 97 != 5] = 0
+            dr = many(n, rt)
+            dx, dres, dw = kda.add_norm_bwd(r0, w, x, dr=dr, eps=EPS)
+            used = slice(5, None, 97)
+            want, _, bw = grad(as64(r0[used]), as64(w), as64(x[used]), 0.0)[1:]
+            R.held(as64(dw), want, bw, "dw")
+            for at in places:
+                for got, small in zip((dx, dres), kda.add_norm_bwd(cut(r0, at), w, cut(x, at), dr=cut(dr, at), eps=EPS)):
+                    assert torch.equal(got[at], small)
+        else:
+            call = kda.add_norm if part == "y" else kda.add_norm_q8
+            got = call(x, r0, w, eps=EPS)
+            for at in places:
+                for whole, small in zip(got, call(cut(x, at), cut(r0, at), w, eps=EPS)):
+                    view = (lambda t: t.view(torch.uint8)) if whole.dtype.itemsize == 1 else (lambda t: t)
+                    assert torch.equal(view(whole[at]), view(small))
 
 
 @pytest.mark.gpu
