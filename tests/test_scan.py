@@ -147,6 +147,10 @@ CASES = [  # lengths (None: rows of T), B, T, C, type, leaky, states both ways
     (None, 1, 4300, 67, "float32", True, False),
     ((3000, 0, 1, 2500, 129), 1, 5630, 34, "bfloat16", True, True),
     ((900, 0, 70, 1500, 129), 1, 2599, 1000, "float32", False, True),
+    # with the chunks' fold in a launch of its own
+    (None, 1, 33000, 20, "bfloat16", True, True),
+    (None, 1, 12800, 1300, "float32", False, True),
+    ((20000, 0, 13001), 1, 33001, 33, "float32", False, True),
 ]
 
 
@@ -243,7 +247,7 @@ def test_rows_outside_the_sequences_and_in_place(kda):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("T,C", [(300, 40), (8000, 40), (9000, 40), (150, 10400)])
+@pytest.mark.parametrize("T,C", [(300, 40), (8000, 40), (9000, 40), (33000, 40), (150, 10400)])
 def test_states_in_place(kda, T, C):
     """The last state written over the first one, and the gradients' alike, in each form."""
     s = make(1, T, C, "bfloat16", None, True, 13)
