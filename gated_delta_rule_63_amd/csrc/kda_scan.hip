@@ -10,6 +10,13 @@
 // tokens in registers, the waves exchange them through LDS, and each goes over
 // its tokens once more from the state that enters them. Nothing divides by a
 // decay, so g = -inf (a reset) is an ordinary value.
+//
+// Bound by memory where there are enough (sequence, strip) pairs, 5.1 TB/s, a copy's rate
+// (8192 x 12288, bf16 with fp32 gates, 805 MB: 157 us; the gradient of 8192 x 8192, 0.94 GB: 193).
+// Few chains leave most of the chip idle, so their chunks run side by side and the inputs
+// pass twice, the second time in part from the last-level cache (131072 x 512, 0.54 GB:
+// 165 us; packed lengths of 271 to 3063, 8192 x 1000, leaky, fp32, the gradient without states,
+// 164 MB: 55 us, 22 + 33 in its two kernels).
 #include "kda_device.h"
 #include "kda_scan.h"
 
@@ -23,8 +30,9 @@ constexpr int S = kScanStrip;
 constexpr int W = 8;              // waves of a workgroup
 // Calls that move more than the last-level cache holds send what they write past it, and what
 // they read once in whole lines (the cache then keeps what is read again): 8192 x 12288
-// 166 -> 156 us, 8192 x 8192 its gradient 203 -> 195 and without states 286 -> 259,
-// 131072 x 512 183 -> 166; strips of 16 channels lose by it (131072 x 4096: 1059 -> 1199).
+// 166 -> 157 us, 8192 x 8192 its gradient 203 -> 193, 131072 x 512 183 -> 165; strips of 16
+// channels lose by it (131072 x 4096: 1059 -> 1199), and so do rows of no whole lines (8 x 8192 x
+// 1000: 126 -> 160, its gradient 218 -> 318).
 constexpr int kPast = 2;          // the buffer instructions' streaming bit
 constexpr double kCache = 256.0 * (1 << 20);
 
@@ -167,10 +175,12 @@ __device__ __forceinline__ void store(const T (&v)[L], void* p, const Run& run, 
     }
 }
 
-// Strips next to each other share lines of memory where they are narrow: workgroups go to
-// the eight dies in turn, so each die takes a run of strips.
-__device__ __forceinline__ int strip_of(int i, int strips) {
-    const int per = strips / 8;
+// Strips next to each other share lines of memory where they are narrow or rows are no whole
+// lines: workgroups go to the eight dies in turn, so each die takes a run of strips. (Chunks
+// side by side, 20000 x 700: 55 -> 40 us, its gradient 69 -> 53; 30000 x 2040: 211 -> 165. Rows of
+// whole lines share nothing, and lose: 8192 x 2048 43 -> 45, the gradient 57 -> 64.)
+__device__ __forceinline__ int in_runs(int i, int n) {
+    const int per = n / 8;
     return i < per * 8 ? (i % 8) * per + i / 8 : i;
 }
 
@@ -234,7 +244,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk(ScanArgs a) {
     constexpr int NS = 64 * W / SW, TILE = NS * L;
     __shared__ float2 sh[2][NS][SW];
     const int strips = (a.C + SW - 1) / SW, n = by_length(a, blockIdx.x / strips);
-    const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
+    const Lane<SW> p(a, in_runs(blockIdx.x % strips, strips));
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, n);
     float h = a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f;
@@ -330,7 +340,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
     __shared__ float2 sh[2][NS][SW];
     __shared__ float sd[2][NS][SW];
     const int strips = (a.C + SW - 1) / SW, n = by_length(a, blockIdx.x / strips);
-    const Lane<SW> p(a, strip_of(blockIdx.x % strips, strips));
+    const Lane<SW> p(a, in_runs(blockIdx.x % strips, strips));
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, n);
     const auto state = [&](int t) { return a.states[(run.slot + t / kScanChunk) * a.C + cc]; };
@@ -366,8 +376,9 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
     __shared__ float2 sh[W][S];
     __shared__ float sd[W][S];
     const int strips = (a.C + S - 1) / S;
-    const long long slot = blockIdx.x / strips;
-    const Lane<S> p(a, blockIdx.x % strips);
+    const int i = a.C % S ? in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
+    const long long slot = i / strips;
+    const Lane<S> p(a, i % strips);
     if (slot >= a.slots) {                         // behind the chunks: sequences without any
         const int n = (int)(slot - a.slots);
         const long long at = (long long)n * a.C + p.c;
@@ -508,8 +519,9 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
     constexpr int ST = STREAM ? kPast : 0;
     __shared__ float2 sh[2][W][S];
     const int strips = (a.C + S - 1) / S;
-    const long long slot = a.slots - 1 - blockIdx.x / strips;
-    const Lane<S> p(a, blockIdx.x % strips);
+    const int i = a.C % S ? in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
+    const long long slot = a.slots - 1 - i / strips;
+    const Lane<S> p(a, i % strips);
     const int cc = min(p.c, a.C - 1), n = sequence_of(a, slot);
     const Run run = sequence(a, n);
     const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
@@ -541,8 +553,9 @@ __global__ __launch_bounds__(64 * W, 4) void kda_scan_chunks_bwd(ScanArgs a, boo
     __shared__ float2 sh[3][W][S];
     __shared__ float sd[W][S];
     const int strips = (a.C + S - 1) / S;
-    const long long slot = a.slots - 1 - blockIdx.x / strips;
-    const Lane<S> p(a, blockIdx.x % strips);
+    const int i = a.C % S ? in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
+    const long long slot = a.slots - 1 - i / strips;
+    const Lane<S> p(a, i % strips);
     const int cc = min(p.c, a.C - 1), n = sequence_of(a, slot);
     const Run run = sequence(a, n);
     const int t = (int)min((slot - run.slot) * kScanChunk, (long long)run.len);
@@ -635,31 +648,40 @@ long long scan_slots(int B, int T, int N, bool packed) {
     return packed ? (long long)T / kScanChunk + N : (long long)B * ((T + (long long)kScanChunk - 1) / kScanChunk);
 }
 
-// How a call runs is the cheapest of four by this estimate, in ns:
-//   one workgroup a (sequence, strip): the longest sequence at what a workgroup takes a
-//     token (8192 x 2048, 32 to 128 of them: 128, 78, 62 us with 64, 32, 16 channels, the
-//     gradient 229, 150, 120; about 1.45 times that in the leaky form), or all bytes at a
-//     rate that falls with the width of a row's piece (8192 x 12288, which the first fills:
-//     163, 207, 217 us; 8192 x 8192: 142, 113, 141; 131072 x 4096: 1990, 1302, 1065);
-//   chunks side by side: three launches that read the inputs twice (the same four:
-//     45, 280, 192 and 1395 us; 131072 x 512: 889 us with 16 channels against 181, the
-//     gradient 1688 against 263).
+// How a call runs is the cheapest of four by this estimate, in ns, whose constants are fitted to
+// 612 measured calls (51 sizes from 1 x 256 x 256 to 134 M values, both types and forms; fwd, the
+// gradient with states and without): 1.2% above the best of the four on average, 42 calls
+// more than 6%, one 30%.
+//   one workgroup a (sequence, strip): the longest sequence, in whole tiles, at what a
+//     workgroup takes a token, or all bytes at a rate that falls where few workgroups run
+//     (8192 x 2048, bf16, 32 to 128 of them: 116, 66, 49 us with 64, 32, 16 channels, the gradient
+//     220, 140, 108; 8192 x 12288: 157, 207, 224 and 278, 326, 379; 16 x 2048 x 2048 in fp32,
+//     the gradient: 301, 228, 258);
+//   chunks side by side: two or three launches that read the inputs twice, or as many workgroups
+//     where chunks are hardly filled (8192 x 2048: 42 us, the gradient 57; 8192 x 12288: 241,
+//     309 and, without states, 328 against 387; 131072 x 512: 169 against 922 with 16
+//     channels, the gradient 214 against 1600).
 // Packed sequences do not tell the host the longest; twice the average stands for it.
 int scan_width(const ScanForm& f, int cus) {
-    static const struct { int width; double fwd, bwd, rate; } strip[] = {{64, 15.5, 28, 4900}, {32, 9.5, 18, 4600}, {16, 7.5, 14.6, 4000}};
+    static const struct { int width; double token, token_bwd, rate, rate_bwd[2]; } strip[] = {
+        {64, 15.7, 26.6, 5460, {5020, 4900}}, {32, 8.5, 20.6, 4680, {5440, 5590}}, {16, 5.7, 9.4, 3880, {3540, 4130}}};
     const double el = (double)f.rows * f.T * f.C, e = f.f32 ? 4 : 2, len = f.packed && f.N > 1 ? fmin(f.T, 2.0 * f.T / f.N) : f.T;
     const bool first = f.back && !f.known;             // states to be formed
     const double bytes = f.back ? 3 * e + 8 : 2 * e + 4;
     // (a launch takes up to 2^22 workgroups; 64 channels a workgroup always fit: N ceil(C / 64) is at most that)
-    const double most = 1 << 22, chunks = ((double)f.rows * f.T / kScanChunk + 2.0 * f.N) * ((f.C + scan::S - 1) / scan::S);
-    int best = chunks > most ? 64 : 0;
-    double least = chunks > most ? HUGE_VAL : 12000 + el * (bytes + (first ? 2 * e + 4 : e + 4)) / 4.9e3;
+    const double most = 1 << 22, wide = (f.C + scan::S - 1) / scan::S, chunks = ((double)f.rows * f.T / kScanChunk + f.N) * wide;
+    const bool fits = chunks + f.N * wide <= most;
+    const double again = first ? 2 * e + 4 : e + 4, rate = first ? 7710 : f.back ? 7070 : 6490;
+    int best = fits ? 0 : 64;
+    double least = fits ? 14900 + fmax(el * (bytes + again) / rate, chunks / cus * (f.back ? 4400 : 2700)) : HUGE_VAL;
     for (const auto& s : strip) {
         const double groups = (double)f.N * ((f.C + s.width - 1) / s.width);
         if (groups > most) continue;
-        const double token = (f.back ? s.bwd + (first ? s.fwd : 0) : s.fwd) * (f.leaky ? 1.45 : 1.0);
-        const double turns = fmax(1.0, groups / (2.0 * cus)), at = fmin(1.0, 0.5 + 0.5 * groups / (0.6 * cus));
-        const double t = fmax(len * token * (f.packed ? 1.0 : turns), el * (bytes + (first ? e + 4 : 0)) / (s.rate * at));
+        const double tile = 64.0 * kScanChunk / s.width, tokens = ceil(len / tile) * tile;
+        const double turns = f.packed ? 1.0 : fmax(1.0, groups / (0.88 * cus)), at = fmin(1.0, 0.2 + 0.8 * groups / (0.7 * cus));
+        const auto walk = [&](double token, double b, double r) { return fmax(tokens * token * turns, el * b / (r * at)); };
+        double t = 5300 + (f.back ? walk(s.token_bwd, bytes, s.rate_bwd[f.f32]) : walk(s.token, bytes, s.rate));
+        if (first) t += 2600 + walk(s.token, e + 4, s.rate);
         if (t < least) best = s.width, least = t;
     }
     return best;
@@ -734,7 +756,7 @@ static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
 }
 
 static ScanArgs with_stream(ScanArgs a, double bytes) {
-    a.stream = (double)(a.cu ? 1 : a.N) * a.T * a.C * bytes > scan::kCache;
+    a.stream = a.C % scan::S == 0 && (double)(a.cu ? 1 : a.N) * a.T * a.C * bytes > scan::kCache;
     return a;
 }
 
