@@ -9,13 +9,17 @@
 // A logit with its index is one 64-bit key: the float's bits, made to ascend as
 // integers, over the inverted index. Keys of a row are unique, 0 is none.
 // NaN and -inf give no key; +inf counts as the largest finite value.
+//
+// 64 x 8 beams, 131072 tokens in bf16 (134 MB), K = 16: 32 us for the rows, 4.1 TB/s read (a sum
+// by the library reads 4.0), 5 for the merge; 1 x 4 beams, 32000 tokens: 5.4 + 4.0 us,
+// launches and trips to memory. Reordering 16 x 4 beams of 2 MiB, 13 us, moves 5 TB/s.
 #include "kda_beam.h"
 #include "kda_device.h"
 
 namespace kda {
 namespace beam {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;                       // of a workgroup, or one wave where that will do
 constexpr int kPieces = 4;                          // 16-byte pieces of a thread in a tile
 constexpr int kPer = 8 * kPieces;                   // its logits, at most (bf16)
 constexpr float kHuge = 3.4028234663852886e38f;
@@ -61,33 +65,37 @@ __device__ __forceinline__ uint64_t lowest(uint32_t h, uint64_t) { return (uint6
 __device__ __forceinline__ uint32_t highest(uint32_t h, uint32_t) { return h; }
 __device__ __forceinline__ uint64_t highest(uint32_t h, uint64_t) { return (uint64_t)h << 32 | 0xffffffffu; }
 
-// Of the 256 values in LDS (each a thread's best; 0: none) a bound that at least
+// Of the 64 Q values in LDS (each a thread's best; 0: none) a bound that at least
 // `want` and, unless they tie, at most `most` of those above `floor` reach; with
-// fewer than `want` of them, all. Every wave finds it by itself, four values a
+// fewer than `want` of them, all. Every wave finds it by itself, Q values a
 // lane, by bisection with a ballot for each count.
 template <typename T>
 struct Bound {
     T value;
     int count;                                      // how many reach it
 };
-template <typename T>
-__device__ __forceinline__ int reach(const T (&u)[4], T v) {
+template <int Q, typename T>
+__device__ __forceinline__ void values_of(T (&u)[Q], const T* best) {
+#pragma unroll
+    for (int j = 0; j < Q; ++j) u[j] = best[Q * (threadIdx.x & 63) + j];
+}
+template <int Q, typename T>
+__device__ __forceinline__ int reach(const T (&u)[Q], T v) {
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) n += __popcll(__ballot(u[j] >= v));
+    for (int j = 0; j < Q; ++j) n += __popcll(__ballot(u[j] >= v));
     return n;
 }
-template <typename T>
+template <int Q, typename T>
 __device__ __forceinline__ Bound<T> bound_of(const T* best, T floor, int want, int most) {
-    T u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = best[4 * (threadIdx.x & 63) + j];
+    T u[Q];
+    values_of(u, best);
     T lo = floor + 1;
     int n = reach(u, lo);
     if (n <= want) return Bound<T>{lo, n};
     uint32_t top = 0, low = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < Q; ++j) {
         top = max(top, high(u[j]));
         if (u[j] > floor) low = max(low, ~high(u[j]));
     }
@@ -105,16 +113,16 @@ __device__ __forceinline__ Bound<T> bound_of(const T* best, T floor, int want, i
 
 // Where more than `most` reach a bound, many equal it: the index up to which those
 // count, from each thread's first index of that value (kNone: it has none).
+template <int Q>
 __device__ __forceinline__ uint32_t index_bound(const uint32_t* first, int above, int want) {
-    uint32_t u[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) u[j] = first[4 * (threadIdx.x & 63) + j];
+    uint32_t u[Q];
+    values_of(u, first);
     uint32_t lo = 0, hi = kNone - 1;
     while (lo < hi) {
         const uint32_t mid = lo + (hi - lo) / 2;
         int n = above;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) n += __popcll(__ballot(u[j] <= mid));
+        for (int j = 0; j < Q; ++j) n += __popcll(__ballot(u[j] <= mid));
         if (n >= want) hi = mid;
         else lo = mid + 1;
     }
@@ -151,7 +159,7 @@ struct Piece {
         else return __uint_as_float(e & 1 ? raw[e / 2] & 0xffff0000u : raw[e / 2] << 16);
     }
 };
-template <bool F32> constexpr int kTile = kThreads * kPieces * Piece<F32>::VE;
+template <bool F32, int TH> constexpr int kTile = TH * kPieces * Piece<F32>::VE;
 
 template <bool F32>
 __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long long j, int V) {
@@ -179,18 +187,18 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
     return p;
 }
 
-template <bool F32>
+template <bool F32, int TH>
 __device__ __forceinline__ void ld_tile(Piece<F32> (&x)[kPieces], const char* row, int off, int t, int V) {
     constexpr int VE = Piece<F32>::VE;
-    const long long j0 = (long long)t * (kThreads * kPieces);
-    if (j0 * VE >= off && (j0 + kThreads * kPieces) * VE - off <= V) {
+    const long long j0 = (long long)t * (TH * kPieces);
+    if (j0 * VE >= off && (j0 + TH * kPieces) * VE - off <= V) {
         // (each is read once: past the caches, 34.6 -> 32.4 us)
         const u32x4* p = reinterpret_cast<const u32x4*>(row - off * (16 / VE)) + j0 + threadIdx.x;
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[i].raw = __builtin_nontemporal_load(p + i * kThreads);
+        for (int i = 0; i < kPieces; ++i) x[i].raw = __builtin_nontemporal_load(p + i * TH);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, off, j0 + i * kThreads + threadIdx.x, V);
+        for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, off, j0 + i * TH + threadIdx.x, V);
     }
 }
 
@@ -201,22 +209,30 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// How many threads may leave their logits in LDS.
+__host__ __device__ constexpr int shown_threads(int K, int TH) { return 2 * K < TH ? 2 * K : TH; }
+
 // One workgroup a part of a row, tile by tile. A tile's candidates are found by its
 // threads' largest logits: at least K threads reach a bound, so no logit below it
 // is among the row's K best, and those that reach it belong to the few threads
 // that do: at most 2 K of them, or K where the bound is a tie, broken by index.
 // From then on only logits above the bound count; one that equals it comes
-// too late.
-template <bool F32>
-__global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
-    extern __shared__ u32x4 shown[];                // 2 K threads' logits
-    uint64_t* const keys = reinterpret_cast<uint64_t*>(shown + 2 * kPieces * a.K);   // up to 2 K from earlier tiles, 64 K of one; K sorted
+// too late. Half of a tile's time is arithmetic, an exponential a logit; the next tile is
+// on its way meanwhile. (Four workgroups a compute unit, the rows of 64 x 8 x 131072: 38 us; five
+// 38, six 45 and eight 73, where the tiles no longer fit the registers. With loads that
+// pass the caches 32.)
+template <bool F32, int TH>
+__global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
+    extern __shared__ u32x4 shown[];                // of `most` threads, their logits
+    const int most = shown_threads(a.K, TH);
+    uint64_t* const keys = reinterpret_cast<uint64_t*>(shown + kPieces * most);   // up to 2 K from earlier tiles, theirs of one; K sorted
     __shared__ int owner[2 * kBeamMax], rows[2];    // whose they are; how many, in turn
-    __shared__ uint32_t best[2][kThreads], first[kThreads];
+    __shared__ uint32_t best[2][TH], first[TH];
     __shared__ int held;
-    __shared__ float sm[4];
-    __shared__ double ss[4];
-    constexpr int VE = Piece<F32>::VE, NV = kPieces, TILE = kTile<F32>, PER = NV * VE;
+    constexpr int Q = TH / 64;
+    __shared__ float sm[Q];
+    __shared__ double ss[Q];
+    constexpr int VE = Piece<F32>::VE, NV = kPieces, TILE = kTile<F32, TH>, PER = NV * VE;
     const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
     if (a.done && a.done[row]) return;
     const char* const base = static_cast<const char*>(a.logits) + (long long)row * a.V * (16 / VE);
@@ -229,12 +245,12 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
     uint32_t floor = 0;
     int turn = 0;
     Piece<F32> next[NV];
-    if (t0 < t1) ld_tile<F32>(next, base, off, t0, a.V);
+    if (t0 < t1) ld_tile<F32, TH>(next, base, off, t0, a.V);
     for (int t = t0; t < t1; ++t) {
         Piece<F32> x[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[i] = next[i];
-        if (t + 1 < t1) ld_tile<F32>(next, base, off, t + 1, a.V);
+        if (t + 1 < t1) ld_tile<F32, TH>(next, base, off, t + 1, a.V);
         float top[NV], tm = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -265,7 +281,7 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
         uint32_t* const bests = best[(t - t0) & 1];
         bests[tid] = mine;
         lds_barrier();
-        const Bound<uint32_t> bd = bound_of(bests, floor, a.K, 2 * a.K);
+        const Bound<uint32_t> bd = bound_of<Q>(bests, floor, a.K, 2 * a.K);
         if (bd.count == 0) continue;
         uint32_t last = kNone, mine_first = 0;
         if (bd.count > 2 * a.K) {
@@ -276,16 +292,15 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
                 for (int i = NV - 1; i >= 0; --i)
 #pragma unroll
                     for (int e = VE - 1; e >= 0; --e)
-                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (TILE / VE) + i * kThreads + tid) * VE + e - off);
+                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (TILE / VE) + i * TH + tid) * VE + e - off);
             first[tid] = mine_first = f;
             lds_barrier();
             {
-                uint32_t u[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) u[j] = bests[4 * (tid & 63) + j];
+                uint32_t u[Q];
+                values_of(u, bests);
                 above = reach(u, bd.value + 1);
             }
-            last = index_bound(first, above, a.K);
+            last = index_bound<Q>(first, above, a.K);
         }
         // The few threads that reach it leave their logits in LDS, where all look through them.
         if (mine > bd.value || (mine == bd.value && mine_first <= last)) {
@@ -298,10 +313,10 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
         if (tid == 0) rows[~turn & 1] = 0;
         const float least = bd.value > 0x007fffffu ? value_of(bd.value) : -kHuge;
         const bool finite = least < kHuge;          // +inf ties with the largest finite value
-        for (int j = tid; j < rows[turn & 1] * PER; j += kThreads) {
+        for (int j = tid; j < rows[turn & 1] * PER; j += TH) {
             const int r = j / PER, e = j % PER;
             const float v = up(reinterpret_cast<const raw_t<F32>*>(shown)[j]);
-            const uint32_t at = (uint32_t)((t * (TILE / VE) + e / VE * kThreads + owner[r]) * VE + e % VE - off);
+            const uint32_t at = (uint32_t)((t * (TILE / VE) + e / VE * TH + owner[r]) * VE + e % VE - off);
             if ((v >= least && at <= last) || (v > least && finite)) keys[atomicAdd(&held, 1)] = (uint64_t)order_of(v) << 32 | ~at;
         }
         ++turn;
@@ -309,8 +324,8 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
         lds_barrier();
         const int n = held;
         if (n > 2 * a.K && t + 1 < t1) {            // keep the K best of them
-            uint64_t* const sorted = keys + (2 + 2 * kPer) * a.K;
-            for (int i = tid; i < n; i += kThreads) {
+            uint64_t* const sorted = keys + 2 * a.K + kPer * most;
+            for (int i = tid; i < n; i += TH) {
                 const int r = rank_of(keys, n, keys[i]);
                 if (r < a.K) sorted[r] = keys[i];
             }
@@ -324,18 +339,23 @@ __global__ __launch_bounds__(kThreads, 4) void kda_beam_rows(BeamArgs a) {
     const float M = wave_all(m, [](float x, float y) { return fmaxf(x, y); });
     if ((tid & 63) == 0) sm[tid >> 6] = M;
     __syncthreads();
-    const float all = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
+    float all = sm[0];
+#pragma unroll
+    for (int i = 1; i < Q; ++i) all = fmaxf(all, sm[i]);
     const double d = wave_all((double)(sum * expf(m - all)), [](double x, double y) { return x + y; });
     if ((tid & 63) == 0) ss[tid >> 6] = d;
     __syncthreads();
-    if (tid == 0) a.parts[blockIdx.x] = BeamPart{all, 0, (ss[0] + ss[1]) + (ss[2] + ss[3])};
+    double sums = ss[0];
+#pragma unroll
+    for (int i = 1; i < Q; ++i) sums += ss[i];
+    if (tid == 0) a.parts[blockIdx.x] = BeamPart{all, 0, sums};
     uint64_t* const out = a.keys + (long long)blockIdx.x * a.K;
     const int n = held;
-    for (int i = tid; i < n; i += kThreads) {
+    for (int i = tid; i < n; i += TH) {
         const int r = rank_of(keys, n, keys[i]);
         if (r < a.K) out[r] = keys[i];
     }
-    for (int i = n + tid; i < a.K; i += kThreads) out[i] = 0;
+    for (int i = n + tid; i < a.K; i += TH) out[i] = 0;
 }
 
 // One workgroup a batch entry. Its items are the keys of its L lists (parts of rows),
@@ -350,12 +370,13 @@ __device__ __forceinline__ bool before(const Total& x, const Total& y) {
     return x.value > y.value || (x.value == y.value && x.at < y.at);
 }
 
-__global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
+template <int TH>
+__global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
     extern __shared__ uint64_t values[];            // K of 2 K lists; their indices behind them
     __shared__ double score[kBeamMax], largest[kBeamMax], logs[kBeamMax];
     __shared__ int state[kBeamMax];                 // 0 dead, 1 alive, 2 done
-    __shared__ uint64_t best[kThreads];
-    __shared__ uint32_t first[kThreads];
+    __shared__ uint64_t best[TH];
+    __shared__ uint32_t first[TH];
     __shared__ int held;
     constexpr int AHEAD = 4;
     const int b = blockIdx.x, tid = threadIdx.x, L = a.W * a.splits, n = L * a.K;
@@ -363,7 +384,7 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
     uint64_t key[AHEAD];                            // asked for before anything waits
     int list[AHEAD];
     {
-        const int q = kThreads / L, r = kThreads % L;
+        const int q = TH / L, r = TH % L;
         int l = tid % L, k = tid / L;
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
@@ -375,7 +396,7 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
         }
     }
     // sums of a row's parts, 16 lanes a row
-    for (int w = tid >> 4; w < a.W; w += kThreads / 16) {
+    for (int w = tid >> 4; w < a.W; w += TH / 16) {
         const int row = b * a.W + w, l = tid & 15;
         const BeamPart* p = a.parts + (long long)row * a.splits;
         const float s = a.scores[row];
@@ -413,15 +434,14 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
     const Total head = total(tid, list[0], key[0]);
     best[tid] = head.value;
     __syncthreads();
-    const Bound<uint64_t> bd = bound_of(best, (uint64_t)0, a.K, 2 * a.K);
+    const Bound<uint64_t> bd = bound_of<TH / 64>(best, (uint64_t)0, a.K, 2 * a.K);
     uint32_t last = kNone;
     if (bd.count > 2 * a.K) {
         first[tid] = head.value == bd.value ? head.at : kNone;
         __syncthreads();
-        uint64_t u[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) u[j] = best[4 * (tid & 63) + j];
-        last = index_bound(first, reach(u, bd.value + 1), a.K);
+        uint64_t u[TH / 64];
+        values_of(u, best);
+        last = index_bound<TH / 64>(first, reach(u, bd.value + 1), a.K);
     }
     uint32_t* const ats = reinterpret_cast<uint32_t*>(values + 2 * a.K * a.K);
     const Total limit{bd.value, last};
@@ -434,12 +454,12 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
     put(head);
 #pragma unroll
     for (int j = 1; j < AHEAD; ++j)
-        if (j * kThreads < n) put(total(tid + j * kThreads, list[j], key[j]));
-    for (int i = tid + AHEAD * kThreads; i < n; i += kThreads) put(total(i, i % L, keys[(i % L) * a.K + i / L]));
+        if (j * TH < n) put(total(tid + j * TH, list[j], key[j]));
+    for (int i = tid + AHEAD * TH; i < n; i += TH) put(total(i, i % L, keys[(i % L) * a.K + i / L]));
     __syncthreads();
     const int c = held;
     const long long to = (long long)b * a.K;
-    for (int i = tid; i < c; i += kThreads) {
+    for (int i = tid; i < c; i += TH) {
         const Total x{values[i], ats[i]};
         int r = 0, j = 0;
         for (; j + 4 <= c; j += 4)
@@ -452,7 +472,7 @@ __global__ __launch_bounds__(kThreads) void kda_beam_merge(BeamArgs a) {
         a.parents[to + r] = (int)(x.at / (uint32_t)a.V);
         a.tokens[to + r] = (int)(x.at % (uint32_t)a.V);
     }
-    for (int i = c + tid; i < a.K; i += kThreads) {
+    for (int i = c + tid; i < a.K; i += TH) {
         a.out_scores[to + i] = -INFINITY;
         a.parents[to + i] = a.tokens[to + i] = -1;
     }
@@ -490,7 +510,7 @@ __device__ __forceinline__ Move move_of(const ReorderArgs& a, int b, int j) {
     return Move{parent >= 0 && parent < a.W ? __builtin_amdgcn_readlane(slot, parent) : to, to};
 }
 
-constexpr int kInFlight = 8;    // pieces of a thread
+constexpr int kInFlight = 8;    // pieces of a thread (16 x 4 beams of 2 MiB: one in flight 23 us, eight 13)
 
 template <typename T>
 __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, int parts) {
@@ -513,8 +533,11 @@ __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, in
 
 }  // namespace beam
 
+// Parts of a row: four workgroups a compute unit, as many as stay there at once (64 x 8 x 131072:
+// 35 us; 8 a unit 38, 16 a unit 42, 32 a unit 50, since each part finds its first bound anew), of a
+// tile at least, and a list for a thread of the merge at most.
 int beam_splits(int B, int W, int V, bool f32, int cus) {
-    const int tile = f32 ? beam::kTile<true> : beam::kTile<false>;
+    const int tile = f32 ? beam::kTile<true, beam::kThreads> : beam::kTile<false, beam::kThreads>;
     const long long rows = (long long)B * W, tiles = ((long long)V + 7 + tile - 1) / tile;
     long long n = (4LL * cus + rows - 1) / (rows > 0 ? rows : 1);
     if (n > tiles) n = tiles;
@@ -525,10 +548,21 @@ int beam_splits(int B, int W, int V, bool f32, int cus) {
 hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     using namespace beam;
     if (a.B == 0) return hipSuccess;
-    const unsigned n = (unsigned)(a.B * a.W * a.splits), lds = (unsigned)(2 * kPieces * a.K * 16 + (3 + 2 * kPer) * a.K * sizeof(uint64_t));
-    if (a.f32) hipLaunchKernelGGL(kda_beam_rows<true>, dim3(n), dim3(kThreads), lds, s, a);
-    else hipLaunchKernelGGL(kda_beam_rows<false>, dim3(n), dim3(kThreads), lds, s, a);
-    hipLaunchKernelGGL(kda_beam_merge, dim3(a.B), dim3(kThreads), (unsigned)(2 * a.K * a.K * 12), s, a);
+    const unsigned n = (unsigned)(a.B * a.W * a.splits);
+    // A row that fits a wave's tile is one wave's work, and so is an entry with few keys (15386 x 8 x
+    // 156 in fp32, K = 1: 560 -> 146 us; 540 x 16 x 423, K = 16: 49 -> 30), but many keys are ranked by
+    // more threads (53 x 32 x 1882, K = 64: 79 us, on a wave each 1445; 64 x 8 x 131072, K = 16, the
+    // merge of 256 on a wave: 5 us more).
+    const bool wave = a.K <= 16 && a.V + 7 <= (a.f32 ? kTile<true, 64> : kTile<false, 64>);
+    const int most = shown_threads(a.K, wave ? 64 : kThreads);
+    const unsigned lds = (unsigned)(kPieces * most * 16 + (3 * a.K + kPer * most) * sizeof(uint64_t));
+    if (a.f32 && wave) hipLaunchKernelGGL((kda_beam_rows<true, 64>), dim3(n), dim3(64), lds, s, a);
+    else if (a.f32) hipLaunchKernelGGL((kda_beam_rows<true, kThreads>), dim3(n), dim3(kThreads), lds, s, a);
+    else if (wave) hipLaunchKernelGGL((kda_beam_rows<false, 64>), dim3(n), dim3(64), lds, s, a);
+    else hipLaunchKernelGGL((kda_beam_rows<false, kThreads>), dim3(n), dim3(kThreads), lds, s, a);
+    const unsigned more = (unsigned)(2 * a.K * a.K * 12);
+    if (a.W * a.splits * a.K <= 64) hipLaunchKernelGGL(kda_beam_merge<64>, dim3(a.B), dim3(64), more, s, a);
+    else hipLaunchKernelGGL(kda_beam_merge<kThreads>, dim3(a.B), dim3(kThreads), more, s, a);
     return hipGetLastError();
 }
 

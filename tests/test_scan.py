@@ -342,6 +342,8 @@ POOL = [  # lengths, T, N, C, inputs, pool, leaky, out_slots
     ((0, 3, 1, 0, 40, 5), 49, 6, 34, "float32", "float32", True, False),
     ((1, 0, 8, 2), 11, 4, 256, "bfloat16", "bfloat16", True, True),
     (None, 1, 300, 1000, "bfloat16", "float32", False, False),
+    (None, 2, 7, 301, "bfloat16", "float32", True, False),
+    (None, 1, 1027, 6, "float32", "bfloat16", False, False),
 ]
 
 
