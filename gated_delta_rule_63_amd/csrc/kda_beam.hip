@@ -217,8 +217,7 @@ __host__ __device__ constexpr int shown_threads(int K, int TH) { return 2 * K < 
 // is among the row's K best, and those that reach it belong to the few threads
 // that do: at most 2 K of them, or K where the bound is a tie, broken by index.
 // From then on only logits above the bound count; one that equals it comes
-// too late. Half of a tile's time is arithmetic, an exponential a logit; the next tile is
-// on its way meanwhile. (Four workgroups a compute unit, the rows of 64 x 8 x 131072: 38 us; five
+// too late. The next tile is on its way meanwhile. (Four workgroups a compute unit, the rows of 64 x 8 x 131072: 38 us; five
 // 38, six 45 and eight 73, where the tiles no longer fit the registers. With loads that
 // pass the caches 32.)
 template <bool F32, int TH>
