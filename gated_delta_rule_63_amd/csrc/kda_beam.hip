@@ -168,21 +168,23 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
     const long long at = VE * j - off;
     if (at >= 0 && at + VE <= V) {
         p.raw = *reinterpret_cast<const u32x4*>(row + at * E);
-    } else {
-        uint32_t w[4];
+        return p;
+    }
+    p.raw = u32x4(F32 ? 0xff800000u : 0xff80ff80u);  // -inf
+    if (at + VE <= 0 || at >= V) return p;
+    // its logits one by one, all on their way at once
+    uint32_t w[VE];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = F32 ? 0xff800000u : 0xff80ff80u;     // -inf
+    for (int e = 0; e < VE; ++e) {
+        const char* q = row + min(max(at + e, 0LL), V - 1LL) * E;
+        if constexpr (F32) w[e] = *reinterpret_cast<const uint32_t*>(q);
+        else w[e] = *reinterpret_cast<const uint16_t*>(q);
+    }
 #pragma unroll
-        for (int e = 0; e < VE; ++e)
-            if (at + e >= 0 && at + e < V) {
-                if constexpr (F32) {
-                    w[e] = *reinterpret_cast<const uint32_t*>(row + (at + e) * E);
-                } else {
-                    const uint32_t h = *reinterpret_cast<const uint16_t*>(row + (at + e) * E);
-                    w[e / 2] = e & 1 ? (w[e / 2] & 0xffffu) | h << 16 : (w[e / 2] & 0xffff0000u) | h;
-                }
-            }
-        p.raw = u32x4{w[0], w[1], w[2], w[3]};
+    for (int e = 0; e < VE; ++e) {
+        if (at + e < 0 || at + e >= V) w[e] = F32 ? 0xff800000u : 0xff80u;
+        if constexpr (F32) p.raw[e] = w[e];
+        else p.raw[e / 2] = e & 1 ? (p.raw[e / 2] & 0xffffu) | w[e] << 16 : (p.raw[e / 2] & 0xffff0000u) | w[e];
     }
     return p;
 }

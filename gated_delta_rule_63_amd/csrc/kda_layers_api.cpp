@@ -166,7 +166,7 @@ kda_status_t kda_scan(const void* x, const float* g, const int32_t* cu_seqlens, 
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.h0 = h0; a.y = y; a.hT = hT; a.states = states;
-    a.fold = folds(desc, cu_seqlens != nullptr) && h0 != hT;
+    a.fold = folds(desc, cu_seqlens != nullptr) && (!hT || h0 != hT);
     cut_scan(&a, desc, false);
     return status(kda::launch_scan(a, static_cast<hipStream_t>(stream)));
 }
@@ -189,7 +189,7 @@ kda_status_t kda_scan_bwd(const void* x, const float* g, const int32_t* cu_seqle
     if (st != KDA_OK) return st;
     if (desc->num_seqs == 0) return KDA_OK;
     a.states = const_cast<float*>(states);
-    a.fold = folds(desc, cu_seqlens != nullptr) && dhT != dh0;
+    a.fold = folds(desc, cu_seqlens != nullptr) && (!dh0 || dhT != dh0);
     cut_scan(&a, desc, true);
     a.h0 = h0; a.dy = dy; a.dhT = dhT; a.dx = dx; a.dg = dg; a.dh0 = dh0;
     return status(kda::launch_scan_bwd(a, states != nullptr, static_cast<hipStream_t>(stream)));
