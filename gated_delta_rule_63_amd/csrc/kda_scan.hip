@@ -332,7 +332,8 @@ struct TileBwd {
     }
 };
 
-// The gradient, tiles from the last to the first, each from the kept state that enters it.
+// The gradient, tiles from the last to the first, each from the kept state that enters it (no
+// states: sequences of one tile, which the first state enters; 200 x 64 x 640, 51 -> 33 us).
 template <bool F32, bool LEAKY, int SW, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
     constexpr int LD = STREAM && SW == 64 ? kPast : 0, ST = STREAM && SW > 16 ? kPast : 0;
@@ -343,7 +344,10 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
     const Lane<SW> p(a, in_runs(blockIdx.x % strips, strips));
     const int cc = min(p.c, a.C - 1);
     const Run run = sequence(a, n);
-    const auto state = [&](int t) { return a.states[(run.slot + t / kScanChunk) * a.C + cc]; };
+    const auto state = [&](int t) {
+        if (!a.states) return a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f;
+        return a.states[(run.slot + t / kScanChunk) * a.C + cc];
+    };
     float D = a.dhT ? a.dhT[(long long)n * a.C + cc] : 0.f;
     const int whole = run.len / TILE;
     if (whole * TILE < run.len) {
@@ -652,6 +656,9 @@ long long scan_slots(int B, int T, int N, bool packed) {
     return packed ? (long long)T / kScanChunk + N : (long long)B * ((T + (long long)kScanChunk - 1) / kScanChunk);
 }
 
+// Tokens of a walk's tile.
+static int scan_tile(int width) { return 64 * kScanChunk / width; }
+
 // How a call runs is the cheapest of four by this estimate, in ns, whose constants are fitted to
 // 612 measured calls (51 sizes from 1 x 256 x 256 to 134 M values, both types and forms; fwd, the
 // gradient with states and without): 1.2% above the best of the four on average, 42 calls
@@ -681,11 +688,11 @@ int scan_width(const ScanForm& f, int cus) {
     for (const auto& s : strip) {
         const double groups = (double)f.N * ((f.C + s.width - 1) / s.width);
         if (groups > most) continue;
-        const double tile = 64.0 * kScanChunk / s.width, tokens = ceil(len / tile) * tile;
+        const double tile = scan_tile(s.width), tokens = ceil(len / tile) * tile;
         const double turns = f.packed ? 1.0 : fmax(1.0, groups / (0.88 * cus)), at = fmin(1.0, 0.2 + 0.8 * groups / (0.7 * cus));
         const auto walk = [&](double token, double b, double r) { return fmax(tokens * token * turns, el * b / (r * at)); };
         double t = 5300 + (f.back ? walk(s.token_bwd, bytes, s.rate_bwd[f.f32]) : walk(s.token, bytes, s.rate));
-        if (first) t += 2600 + walk(s.token, e + 4, s.rate);
+        if (first && f.T > tile) t += 2600 + walk(s.token, e + 4, s.rate);
         if (t < least) best = s.width, least = t;
     }
     return best;
@@ -735,11 +742,13 @@ static hipError_t scan_fwd(const ScanArgs& a, hipStream_t s) {
 }
 
 template <bool F32, bool LEAKY>
-static hipError_t scan_bwd(const ScanArgs& a, bool known, hipStream_t s) {
+static hipError_t scan_bwd(ScanArgs a, bool known, hipStream_t s) {
     using namespace scan;
     const long long strips = (a.C + S - 1) / S, chunks = a.slots * strips;
     if (a.width > 0) {
-        if (!known) {
+        if (!known && a.T <= scan_tile(a.width)) {
+            a.states = nullptr;
+        } else if (!known) {
             const hipError_t e = scan_fwd<F32, LEAKY>(a, s);   // y is not there: states only
             if (e != hipSuccess) return e;
         }
