@@ -148,8 +148,9 @@ template <bool F32> using raw_t = typename Raw<F32>::type;
 __device__ __forceinline__ float up(uint16_t u) { return __uint_as_float((uint32_t)u << 16); }
 __device__ __forceinline__ float up(float x) { return x; }
 
-// Row pieces of 16 bytes at multiples of 16 bytes: piece j holds the row's logits
-// from VE j - off on, the first and the last of them only in part.
+// Row pieces of 16 bytes, counted from the row's first logit wherever it lies: beams with the
+// same logits then add the same exponentials in the same order, and tie. The last piece
+// may be there in part.
 template <bool F32>
 struct Piece {
     static constexpr int VE = F32 ? 4 : 8;
@@ -161,28 +162,32 @@ struct Piece {
 };
 template <bool F32, int TH> constexpr int kTile = TH * kPieces * Piece<F32>::VE;
 
+// (16 bytes at the alignment of a logit)
+template <bool F32> struct Loose { typedef u32x4 type __attribute__((aligned(2))); };
+template <> struct Loose<true> { typedef u32x4 type __attribute__((aligned(4))); };
+
 template <bool F32>
-__device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long long j, int V) {
+__device__ __forceinline__ Piece<F32> ld_piece(const char* row, long long j, int V) {
     constexpr int VE = Piece<F32>::VE, E = 16 / VE;
     Piece<F32> p;
-    const long long at = VE * j - off;
-    if (at >= 0 && at + VE <= V) {
-        p.raw = *reinterpret_cast<const u32x4*>(row + at * E);
+    const long long at = VE * j;
+    if (at + VE <= V) {
+        p.raw = *reinterpret_cast<const typename Loose<F32>::type*>(row + at * E);
         return p;
     }
     p.raw = u32x4(F32 ? 0xff800000u : 0xff80ff80u);  // -inf
-    if (at + VE <= 0 || at >= V) return p;
+    if (at >= V) return p;
     // its logits one by one, all on their way at once
     uint32_t w[VE];
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-        const char* q = row + min(max(at + e, 0LL), V - 1LL) * E;
+        const char* q = row + min(at + e, V - 1LL) * E;
         if constexpr (F32) w[e] = *reinterpret_cast<const uint32_t*>(q);
         else w[e] = *reinterpret_cast<const uint16_t*>(q);
     }
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-        if (at + e < 0 || at + e >= V) w[e] = F32 ? 0xff800000u : 0xff80u;
+        if (at + e >= V) w[e] = F32 ? 0xff800000u : 0xff80u;
         if constexpr (F32) p.raw[e] = w[e];
         else p.raw[e / 2] = e & 1 ? (p.raw[e / 2] & 0xffffu) | w[e] << 16 : (p.raw[e / 2] & 0xffff0000u) | w[e];
     }
@@ -190,17 +195,17 @@ __device__ __forceinline__ Piece<F32> ld_piece(const char* row, int off, long lo
 }
 
 template <bool F32, int TH>
-__device__ __forceinline__ void ld_tile(Piece<F32> (&x)[kPieces], const char* row, int off, int t, int V) {
+__device__ __forceinline__ void ld_tile(Piece<F32> (&x)[kPieces], const char* row, int t, int V) {
     constexpr int VE = Piece<F32>::VE;
     const long long j0 = (long long)t * (TH * kPieces);
-    if (j0 * VE >= off && (j0 + TH * kPieces) * VE - off <= V) {
+    if ((j0 + TH * kPieces) * VE <= V) {
         // (each is read once: past the caches, 34.6 -> 32.4 us)
-        const u32x4* p = reinterpret_cast<const u32x4*>(row - off * (16 / VE)) + j0 + threadIdx.x;
+        const typename Loose<F32>::type* p = reinterpret_cast<const typename Loose<F32>::type*>(row) + j0 + threadIdx.x;
 #pragma unroll
         for (int i = 0; i < kPieces; ++i) x[i].raw = __builtin_nontemporal_load(p + i * TH);
     } else {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, off, j0 + i * TH + threadIdx.x, V);
+        for (int i = 0; i < kPieces; ++i) x[i] = ld_piece<F32>(row, j0 + i * TH + threadIdx.x, V);
     }
 }
 
@@ -219,9 +224,9 @@ __host__ __device__ constexpr int shown_threads(int K, int TH) { return 2 * K < 
 // is among the row's K best, and those that reach it belong to the few threads
 // that do: at most 2 K of them, or K where the bound is a tie, broken by index.
 // From then on only logits above the bound count; one that equals it comes
-// too late. The next tile is on its way meanwhile. (Four workgroups a compute unit, the rows of 64 x 8 x 131072: 38 us; five
-// 38, six 45 and eight 73, where the tiles no longer fit the registers. With loads that
-// pass the caches 32.)
+// too late. The next tile is on its way meanwhile. (Four workgroups a compute unit, the rows of
+// 64 x 8 x 131072: 38 us; five 38, six 45 and eight 73, where the tiles no longer fit the
+// registers. With loads that pass the caches 32.)
 template <bool F32, int TH>
 __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     extern __shared__ u32x4 shown[];                // of `most` threads, their logits
@@ -229,7 +234,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     uint64_t* const keys = reinterpret_cast<uint64_t*>(shown + kPieces * most);   // up to 2 K from earlier tiles, theirs of one; K sorted
     __shared__ int owner[2 * kBeamMax], rows[2];    // whose they are; how many, in turn
     __shared__ uint32_t best[2][TH], first[TH];
-    __shared__ int held, kept;
+    __shared__ int held;
     constexpr int Q = TH / 64;
     __shared__ float sm[Q];
     __shared__ double ss[Q];
@@ -237,8 +242,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     const int row = blockIdx.x / a.splits, part = blockIdx.x % a.splits;
     if (a.done && a.done[row]) return;
     const char* const base = static_cast<const char*>(a.logits) + (long long)row * a.V * (16 / VE);
-    const int off = (int)(reinterpret_cast<uintptr_t>(base) & 15) / (16 / VE);
-    const int tiles = (int)(((long long)a.V + off + TILE - 1) / TILE);
+    const int tiles = (int)(((long long)a.V + TILE - 1) / TILE);
     const int t0 = (int)((long long)tiles * part / a.splits), t1 = (int)((long long)tiles * (part + 1) / a.splits);
     const int tid = threadIdx.x;
     if (tid == 0) held = rows[0] = rows[1] = 0;
@@ -246,12 +250,12 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     uint32_t floor = 0;
     int turn = 0;
     Piece<F32> next[NV];
-    if (t0 < t1) ld_tile<F32, TH>(next, base, off, t0, a.V);
+    if (t0 < t1) ld_tile<F32, TH>(next, base, t0, a.V);
     for (int t = t0; t < t1; ++t) {
         Piece<F32> x[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) x[i] = next[i];
-        if (t + 1 < t1) ld_tile<F32, TH>(next, base, off, t + 1, a.V);
+        if (t + 1 < t1) ld_tile<F32, TH>(next, base, t + 1, a.V);
         float top[NV], tm = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -293,7 +297,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
                 for (int i = NV - 1; i >= 0; --i)
 #pragma unroll
                     for (int e = VE - 1; e >= 0; --e)
-                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (TILE / VE) + i * TH + tid) * VE + e - off);
+                        if (order_of(x[i][e]) == bd.value) f = (uint32_t)((t * (TILE / VE) + i * TH + tid) * VE + e);
             first[tid] = mine_first = f;
             lds_barrier();
             {
@@ -317,7 +321,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
         for (int j = tid; j < rows[turn & 1] * PER; j += TH) {
             const int r = j / PER, e = j % PER;
             const float v = up(reinterpret_cast<const raw_t<F32>*>(shown)[j]);
-            const uint32_t at = (uint32_t)((t * (TILE / VE) + e / VE * TH + owner[r]) * VE + e % VE - off);
+            const uint32_t at = (uint32_t)((t * (TILE / VE) + e / VE * TH + owner[r]) * VE + e % VE);
             if ((v >= least && at <= last) || (v > least && finite)) keys[atomicAdd(&held, 1)] = (uint64_t)order_of(v) << 32 | ~at;
         }
         ++turn;
@@ -362,7 +366,8 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
 // One workgroup a batch entry. Its items are the keys of its L lists (parts of rows),
 // the lists' heads first, then their second keys, and so on: thread t's first item is
 // t. At least K of those reach a bound, found as above, and so every one of the K
-// best does; of the later items a list has only what follows K items that do.
+// best does; of the later items a list has only what follows items that do, so that the
+// merge ends with the first turn in which none does.
 struct Total {
     uint64_t value;                                 // ascending
     uint32_t at;                                    // w V + v
@@ -371,12 +376,23 @@ __device__ __forceinline__ bool before(const Total& x, const Total& y) {
     return x.value > y.value || (x.value == y.value && x.at < y.at);
 }
 
-// Places for the candidates that a second bound leaves; with smaller K there are few to begin with.
-__host__ __device__ constexpr int spare(int K) { return K > 32 ? 512 : 0; }
+// The last that counts of the threads' best: at least K are not behind it, and at most 2 K.
+template <int TH>
+__device__ __forceinline__ Total limit_of(uint64_t* best, uint32_t* first, const Total& mine, int K) {
+    best[threadIdx.x] = mine.value;
+    __syncthreads();
+    const Bound<uint64_t> bd = bound_of<TH / 64>(best, (uint64_t)0, K, 2 * K);
+    if (bd.count <= 2 * K) return Total{bd.value, kNone};
+    first[threadIdx.x] = mine.value == bd.value ? mine.at : kNone;
+    __syncthreads();
+    uint64_t u[TH / 64];
+    values_of(u, best);
+    return Total{bd.value, index_bound<TH / 64>(first, reach(u, bd.value + 1), K)};
+}
 
 template <int TH>
 __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
-    extern __shared__ uint64_t values[];            // K of 2 K lists; their indices behind them; places for fewer
+    extern __shared__ uint64_t values[];            // K of 2 K lists; their indices behind them
     __shared__ double score[kBeamMax], largest[kBeamMax], logs[kBeamMax];
     __shared__ int state[kBeamMax];                 // 0 dead, 1 alive, 2 done
     __shared__ uint64_t best[TH];
@@ -385,11 +401,10 @@ __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
     constexpr int AHEAD = 4;
     const int b = blockIdx.x, tid = threadIdx.x, L = a.W * a.splits, n = L * a.K;
     const uint64_t* const keys = a.keys + (long long)b * n;
-    uint64_t key[AHEAD];                            // asked for before anything waits
-    int list[AHEAD];
-    {
-        const int q = TH / L, r = TH % L;
-        int l = tid % L, k = tid / L;
+    uint64_t key[AHEAD];
+    int list[AHEAD], l = tid % L, k = tid / L;      // the next item's
+    const int q = TH / L, r = TH % L;
+    const auto fetch = [&] {
 #pragma unroll
         for (int j = 0; j < AHEAD; ++j) {
             list[j] = l;
@@ -398,7 +413,8 @@ __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
             k += q;
             if (l >= L) l -= L, ++k;
         }
-    }
+    };
+    fetch();                                        // before anything waits
     // sums of a row's parts, 16 lanes a row
     for (int w = tid >> 4; w < a.W; w += TH / 16) {
         const int row = b * a.W + w, l = tid & 15;
@@ -436,21 +452,12 @@ __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
                      (uint32_t)w * (uint32_t)a.V + index_of(key)};
     };
     const Total head = total(tid, list[0], key[0]);
-    best[tid] = head.value;
-    __syncthreads();
-    const Bound<uint64_t> bd = bound_of<TH / 64>(best, (uint64_t)0, a.K, 2 * a.K);
-    uint32_t last = kNone;
-    if (bd.count > 2 * a.K) {
-        first[tid] = head.value == bd.value ? head.at : kNone;
-        __syncthreads();
-        uint64_t u[TH / 64];
-        values_of(u, best);
-        last = index_bound<TH / 64>(first, reach(u, bd.value + 1), a.K);
-    }
     uint32_t* const ats = reinterpret_cast<uint32_t*>(values + 2 * a.K * a.K);
-    const Total limit{bd.value, last};
+    const Total limit = limit_of<TH>(best, first, head, a.K);
+    bool any = false;
     const auto put = [&](const Total& x) {
         if (!x.value || before(limit, x)) return;
+        any = true;
         const int i = atomicAdd(&held, 1);
         values[i] = x.value;
         ats[i] = x.at;
@@ -459,36 +466,42 @@ __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
 #pragma unroll
     for (int j = 1; j < AHEAD; ++j)
         if (j * TH < n) put(total(tid + j * TH, list[j], key[j]));
-    for (int i = tid + AHEAD * TH; i < n; i += TH) put(total(i, i % L, keys[(i % L) * a.K + i / L]));
-    __syncthreads();
+    // (a turn holds every list's next item, L <= TH)
+    for (int i = tid + AHEAD * TH; __syncthreads_or(any) && i - tid < n; i += AHEAD * TH) {
+        fetch();
+        any = false;
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) put(total(i + j * TH, list[j], key[j]));
+    }
     int c = held;
-    const uint64_t* value = values;
-    const uint32_t* at = ats;
-    const int room = spare(a.K);
-    if (c > room && room > 0) {                     // fewer to rank (53 x 32, K = 64: 55 -> 41 us)
-        uint64_t* const few = reinterpret_cast<uint64_t*>(ats + 2 * a.K * a.K);
-        uint32_t* const few_ats = reinterpret_cast<uint32_t*>(few + room);
-        uint32_t top = 0;
-        for (int i = tid; i < c; i += TH) top = max(top, high(values[i]));
-        first[tid] = top;
+    if (c > TH && c > 4 * a.K) {
+        // Ranking takes c^2 reads: only those that a second bound leaves, of each thread's best, found
+        // as above (53 x 32 beams, K = 64: 55 -> 15 us; 3 x 16, 198533 tokens in bf16, many equal, K = 32: 201 -> 22)
+        Total top{0, kNone};
+        for (int i = tid; i < c; i += TH) {
+            const Total x{values[i], ats[i]};
+            if (before(x, top)) top = x;
+        }
+        const Total least = limit_of<TH>(best, first, top, a.K);
+        for (int i = tid; i - tid < c; i += TH) {   // to places that have been read
+            const Total x = i < c ? Total{values[i], ats[i]} : Total{0, kNone};
+            __syncthreads();
+            if (i >= c || before(least, x)) continue;
+            const int j = atomicAdd(&kept, 1);
+            values[j] = x.value;
+            ats[j] = x.at;
+        }
         __syncthreads();
-        const uint32_t v = bound_of<TH / 64>(first, 0u, a.K, 2 * a.K).value;
-        for (int i = tid; i < c; i += TH)
-            if (high(values[i]) >= v) {
-                const int j = atomicAdd(&kept, 1);
-                if (j < room) few[j] = values[i], few_ats[j] = ats[i];
-            }
-        __syncthreads();
-        if (kept <= room) c = kept, value = few, at = few_ats;
+        c = kept;
     }
     const long long to = (long long)b * a.K;
     for (int i = tid; i < c; i += TH) {
-        const Total x{value[i], at[i]};
+        const Total x{values[i], ats[i]};
         int r = 0, j = 0;
         for (; j + 4 <= c; j += 4)
 #pragma unroll
-            for (int u = 0; u < 4; ++u) r += before(Total{value[j + u], at[j + u]}, x);
-        for (; j < c; ++j) r += before(Total{value[j], at[j]}, x);
+            for (int u = 0; u < 4; ++u) r += before(Total{values[j + u], ats[j + u]}, x);
+        for (; j < c; ++j) r += before(Total{values[j], ats[j]}, x);
         if (r >= a.K) continue;
         const uint64_t v = x.value >> 63 ? x.value & ~(1ull << 63) : ~x.value;
         a.out_scores[to + r] = (float)__longlong_as_double(v);
@@ -561,7 +574,7 @@ __global__ __launch_bounds__(256) void kda_beam_reorder_kernel(ReorderArgs a, in
 // tile at least, and a list for a thread of the merge at most.
 int beam_splits(int B, int W, int V, bool f32, int cus) {
     const int tile = f32 ? beam::kTile<true, beam::kThreads> : beam::kTile<false, beam::kThreads>;
-    const long long rows = (long long)B * W, tiles = ((long long)V + 7 + tile - 1) / tile;
+    const long long rows = (long long)B * W, tiles = ((long long)V + tile - 1) / tile;
     long long n = (4LL * cus + rows - 1) / (rows > 0 ? rows : 1);
     if (n > tiles) n = tiles;
     if (n > beam::kThreads / W) n = beam::kThreads / W;
@@ -573,17 +586,17 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     if (a.B == 0) return hipSuccess;
     const unsigned n = (unsigned)(a.B * a.W * a.splits);
     // A row that fits a wave's tile is one wave's work, and so is an entry with few keys (15386 x 8 x
-    // 156 in fp32, K = 1: 560 -> 146 us; 540 x 16 x 423, K = 16: 49 -> 30), but many keys are ranked by
-    // more threads (53 x 32 x 1882, K = 64: 79 us, on a wave each 1445; 64 x 8 x 131072, K = 16, the
+    // 156 in fp32, K = 1: 560 -> 119 us; 540 x 16 x 423, K = 16: 49 -> 28), but many keys are ranked by
+    // more threads (53 x 32 x 1882, K = 64: 42 us, on a wave each 1.4 ms; 64 x 8 x 131072, K = 16, the
     // merge of 256 on a wave: 5 us more).
-    const bool wave = a.K <= 16 && a.V + 7 <= (a.f32 ? kTile<true, 64> : kTile<false, 64>);
+    const bool wave = a.K <= 16 && a.V <= (a.f32 ? kTile<true, 64> : kTile<false, 64>);
     const int most = shown_threads(a.K, wave ? 64 : kThreads);
     const unsigned lds = (unsigned)(kPieces * most * 16 + (3 * a.K + kPer * most) * sizeof(uint64_t));
     if (a.f32 && wave) hipLaunchKernelGGL((kda_beam_rows<true, 64>), dim3(n), dim3(64), lds, s, a);
     else if (a.f32) hipLaunchKernelGGL((kda_beam_rows<true, kThreads>), dim3(n), dim3(kThreads), lds, s, a);
     else if (wave) hipLaunchKernelGGL((kda_beam_rows<false, 64>), dim3(n), dim3(64), lds, s, a);
     else hipLaunchKernelGGL((kda_beam_rows<false, kThreads>), dim3(n), dim3(kThreads), lds, s, a);
-    const unsigned more = (unsigned)((2 * a.K * a.K + spare(a.K)) * 12);
+    const unsigned more = (unsigned)(2 * a.K * a.K * 12);
     if (a.W * a.splits * a.K <= 64) hipLaunchKernelGGL(kda_beam_merge<64>, dim3(a.B), dim3(64), more, s, a);
     else hipLaunchKernelGGL(kda_beam_merge<kThreads>, dim3(a.B), dim3(kThreads), more, s, a);
     return hipGetLastError();

@@ -583,7 +583,7 @@ size_t kda_add_norm_bwd_workspace_size(const kda_norm_desc_t* desc);
  * A logit of -inf or NaN is no candidate and adds nothing to the sum; +inf counts
  * as the largest finite value. Places beyond the last candidate hold -inf, -1, -1.
  * Totals are compared in fp64, formed from sums of fp32 exponentials (an error of
- * the order of 1e-7). W and K are 1 to 64, V 1 to 2^25, B W at most 2^20 (KDA_ERR_SHAPE);
+ * the order of 1e-7, the same for beams with the same logits). W and K are 1 to 64, V 1 to 2^25, B W at most 2^20 (KDA_ERR_SHAPE);
  * with done, eos lies in [0, V) (KDA_ERR_SHAPE). Needs desc->workspace of
  * kda_beam_workspace_size(desc) bytes, 16-byte aligned, used by one call at a time. */
 typedef struct kda_beam_desc {

@@ -156,6 +156,22 @@ def test_ties_and_masked_places(kda, V, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("K", [5, 32, 64])
+@pytest.mark.parametrize("W,V", [(16, 70001), (64, 700), (3, 150000)])
+def test_many_keys(kda, W, V, K):
+    """Many lists of keys an entry, with one beam ahead of the others, all alike, few distinct logits
+    or only ordinary ones."""
+    x, scores = draw(2, W, V, "bfloat16", 8)
+    check(kda, x, scores, K)
+    ahead = scores.clone()
+    ahead[:, W // 2] += 30.0
+    check(kda, x, ahead, K)
+    check(kda, x[:1].expand(2, W, V).contiguous(), torch.full((2, W), -2.0), K)
+    check(kda, x[:, :1].expand(2, W, V).contiguous(), torch.full((2, W), -2.0), K)
+    check(kda, (x > 2.5).to(torch.bfloat16), torch.full((2, W), -1.0), K)
+
+
+@pytest.mark.gpu
 def test_logits_of_done_beams_are_not_read(kda):
     x, scores = draw(2, 4, 3000, "float32", 7)
     done = torch.tensor([[True, False, True, False], [False, False, False, True]])
