@@ -400,9 +400,10 @@ static unsigned blocks(long long rows, const Shape& s, int most) {
 constexpr int kThreadsAll = 256 * 2048;    // lanes of the chip
 
 // What goes past the last-level cache, by a call's bytes: nothing, what is read, or all. 67 M values,
-// C = 4096, in us: bf16 (537 MB) 101, 82, 95, its gradient 110, 95, 104; with an fp32 residual (805 MB)
-// 153, 149, 138, its gradient 208, 207, 189; fp32 (1.07 GB) 194, 198, 183. At 268 MB
-// (8192 x 4096) 42, 44, 49.
+// C = 4096, results written over the last ones, in us: bf16 (537 MB) 101, 82, 95, its gradient 110, 95,
+// 104; with an fp32 residual (805 MB) 153, 149, 138, its gradient 208, 207, 189; fp32 (1.07 GB) 194,
+// 198, 183. 12288 x 4096 in bf16 (403 MB) with results elsewhere 77, 76, 72, and read by the next
+// kernel 96, 92, 105. At 268 MB (8192 x 4096) 42, 44, 49; elsewhere 52, 51, 49; read next 63, 64, 71.
 static int beyond(double bytes) {
     constexpr double cache = 256.0 * (1 << 20);
     return bytes > 2.5 * cache ? 2 : bytes > cache ? 1 : 0;
