@@ -172,6 +172,19 @@ def test_many_keys(kda, W, V, K):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("V", [7, 500, 2048, 9001])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_unaligned_logits(kda, dtype, V):
+    """The same bits wherever the logits begin."""
+    x, scores = draw(3, 4, V, dtype, 9)
+    flat = torch.empty(x.numel() + 1, dtype=x.dtype, device="cuda")
+    flat[1:] = x.reshape(-1).cuda()
+    check(kda, x, scores, 6)
+    got = kda.beam_select(flat[1:].view(x.shape), scores.cuda(), k=6)
+    assert all(torch.equal(a, b) for a, b in zip(got, kda.beam_select(x.cuda(), scores.cuda(), k=6)))
+
+
+@pytest.mark.gpu
 def test_logits_of_done_beams_are_not_read(kda):
     x, scores = draw(2, 4, 3000, "float32", 7)
     done = torch.tensor([[True, False, True, False], [False, False, False, True]])
