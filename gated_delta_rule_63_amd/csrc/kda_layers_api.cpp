@@ -119,6 +119,8 @@ kda_status_t check_norm(const kda_norm_desc_t* d, bool residual, float eps) {
     return eps >= 0.f && isfinite(eps) ? KDA_OK : KDA_ERR_UNSUPPORTED;
 }
 
+int pieces(int32_t C) { return C % 8 == 0 ? 8 : C % 4 == 0 ? 4 : C % 2 == 0 ? 2 : 1; }
+
 kda::NormArgs norm_args(const float* weight, float eps, const kda_norm_desc_t* d, bool residual) {
     kda::NormArgs a{};
     a.weight = weight; a.eps = eps;
@@ -137,7 +139,7 @@ kda_status_t add_norm(bool q8, const void* x, const void* res, const float* weig
     kda::NormArgs a = norm_args(weight, eps, d, res != nullptr);
     a.x = x; a.res = res; a.y = y; a.r = r; a.scales = scales;
     a.q8 = q8; a.group = d->C == 128 ? 0 : group;      // (then the row is the group)
-    a.vec = d->C % 8 == 0 && aligned16(x, res, weight, y, res ? r : nullptr);
+    a.vec = aligned16(x, res, weight, y, res ? r : nullptr) ? pieces(d->C) : 1;
     return status(kda::launch_add_norm(a, static_cast<hipStream_t>(stream)));
 }
 
@@ -238,7 +240,7 @@ kda_status_t kda_add_norm_bwd(const void* r, const float* weight, float eps, con
     kda::NormArgs a = norm_args(weight, eps, desc, true);
     a.res = r; a.dy = dy; a.dr = dr; a.dx = dx; a.dres = d_residual; a.dweight = dweight;
     a.part = static_cast<float*>(desc->workspace);
-    a.vec = desc->C % 8 == 0 && aligned16(r, weight, dy, dr, dx, d_residual);
+    a.vec = aligned16(r, weight, dy, dr, dx, d_residual) ? pieces(desc->C) : 1;
     return status(kda::launch_add_norm_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

@@ -27,7 +27,7 @@ struct NormArgs {
     int C;
     int group;                 // 0: a row
     bool f32, res_f32, q8;
-    bool vec;                  // rows of whole 16-byte pieces
+    int vec;                   // neighbours that make up every row: 8, 4, 2 or 1
 };
 
 int norm_partials(long long rows, int C);

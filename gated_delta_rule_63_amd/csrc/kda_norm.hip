@@ -29,10 +29,10 @@ constexpr float kLeast = 0x1p-40f, kE4M3Max = 448.f;
 
 // A row on LANES = 16 or 32 lanes or on `wpr` waves (LANES = 64), E values a lane, as pieces
 // of V neighbours (16 bytes of the widest type: 8 in bf16, 4 where a tensor is fp32, so that every
-// load takes whole lines; or 1 for rows of other sizes and tensors that start elsewhere). A wave reaches its rows (64 / LANES, or its part of one) through
-// a buffer resource that ends with the last one that is there, so that lanes beyond it
-// read zeros and write nothing; what lies beyond a row's end in the next one's place is
-// sent beyond all.
+// load takes whole lines; less for rows of other sizes, 1 for tensors that start elsewhere). A
+// wave reaches its rows (64 / LANES, or its part of one) through a buffer resource that ends
+// with the last one that is there, so that lanes beyond it read zeros and write nothing;
+// what lies beyond a row's end in the next one's place is sent beyond all.
 template <int LANES, int E, int V>
 struct Place {
     static constexpr int R = 64 / LANES;
@@ -92,7 +92,7 @@ __device__ __forceinline__ void get(Raw<F32, E, V>& r, const void* p, const Plac
         } else if constexpr (W == 2) {
             const u32x2 q = __builtin_amdgcn_raw_buffer_load_b64(b, o, 0, AUX);
             r.w[u][0] = q[0], r.w[u][1] = q[1];
-        } else if constexpr (F32) {
+        } else if constexpr (F32 || V == 2) {
             r.w[u][0] = __builtin_amdgcn_raw_buffer_load_b32(b, o, 0, AUX);
         } else {
             r.w[u][0] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(b, o, 0, AUX);
@@ -120,7 +120,7 @@ __device__ __forceinline__ void put(void* p, const float (&x)[E], const Place<LA
                 __builtin_amdgcn_raw_buffer_store_b128(u32x4{w[i], w[i + 1], w[i + 2], w[i + 3]}, b, o + 4 * i, 0, AUX);
         } else if constexpr (W == 2) {
             __builtin_amdgcn_raw_buffer_store_b64(u32x2{w[0], w[1]}, b, o, 0, AUX);
-        } else if constexpr (F32) {
+        } else if constexpr (F32 || V == 2) {
             __builtin_amdgcn_raw_buffer_store_b32(w[0], b, o, 0, AUX);
         } else {
             __builtin_amdgcn_raw_buffer_store_b16((uint16_t)w[0], b, o, 0, AUX);
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(1024) void kda_add_norm_kernel(NormArgs a, int wpr)
 #pragma unroll
         for (int u = 0; u < E / V; ++u) {
             const int c = at.col(u);
-            if (V > 1 && LANES >= 32 && a.group) {  // which 128 / V lanes hold
+            if (V >= 4 && LANES >= 32 && a.group) {  // which 128 / V lanes hold
                 constexpr int last = 128 / V - 1;
                 float m = 0.f;
 #pragma unroll
@@ -264,6 +264,9 @@ __global__ __launch_bounds__(1024) void kda_add_norm_kernel(NormArgs a, int wpr)
             }
             if constexpr (V == 1) {
                 __builtin_amdgcn_raw_buffer_store_b8((uint8_t)(__builtin_amdgcn_cvt_pk_fp8_f32(r[u] / scale, 0.f, 0, false) & 0xff), q, at.off(u, 1), 0, 0);
+            } else if constexpr (V == 2) {
+                const int two = __builtin_amdgcn_cvt_pk_fp8_f32(r[2 * u] / scale, r[2 * u + 1] / scale, 0, false);
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)two, q, at.off(u, 1), 0, 0);
             } else {
                 uint32_t w8[V / 4];
 #pragma unroll
@@ -378,8 +381,11 @@ __global__ __launch_bounds__(1024) void kda_add_norm_sum(NormArgs a, int P) {
 // 104 / 93 / 113, on 64 114 / 126 / 122. A row of up to 1024 stays in one wave at 16 values a lane,
 // with nothing to exchange (C = 600: 114 / 106 / 116 against 116 / 126 / 126 on two waves; 1024:
 // 104 / 93 / 109 against 103 / 94 / 113). Beyond, 8 values a lane (C = 4096: 101 / 93 / 110 against
-// 105 / 96 / 114), until a workgroup has no more waves. Values one by one where pieces do not
-// fit (C = 1001 against 1000: 114 / 101 / 120 against 89 / 83 / 103).
+// 105 / 96 / 114), until a workgroup has no more waves. Smaller pieces where these do
+// not make up a row, which go past the cache in bf16 alone (large calls so; C = 1000: 89 / 83 / 103,
+// 1004: 93 / 84 / 108, 1002: 92 / 88 / 112 against 111 / 100 / 116 through it; in fp32 1002 takes 218 /
+// 182 / 201 against 209 / 172 / 217), or values one by one (1001: 114 / 101 / 120; past it 110 / 103 /
+// 127).
 struct Shape {
     int lanes, E, wpr, threads, rows;
 };
@@ -429,10 +435,14 @@ int norm_partials(long long rows, int C) {
     } while (0)
 #define KDA_NORM_PIECES(kernel, n, f32, r32, V)                                                    \
     do {                                                                                           \
-        if (!a.vec) KDA_NORM_SIZES(kernel, n, f32, r32, 1, 0);                                     \
-        else if (past == 2) KDA_NORM_SIZES(kernel, n, f32, r32, V, 2);                             \
-        else if (past == 1) KDA_NORM_SIZES(kernel, n, f32, r32, V, 1);                             \
-        else KDA_NORM_SIZES(kernel, n, f32, r32, V, 0);                                            \
+        if (a.vec >= V && past == 2) KDA_NORM_SIZES(kernel, n, f32, r32, V, 2);                    \
+        else if (a.vec >= V && past == 1) KDA_NORM_SIZES(kernel, n, f32, r32, V, 1);               \
+        else if (a.vec >= V) KDA_NORM_SIZES(kernel, n, f32, r32, V, 0);                            \
+        else if (V == 8 && a.vec == 4 && past) KDA_NORM_SIZES(kernel, n, f32, r32, 4, 1);          \
+        else if (V == 8 && a.vec == 4) KDA_NORM_SIZES(kernel, n, f32, r32, 4, 0);                  \
+        else if (V == 8 && a.vec == 2 && past) KDA_NORM_SIZES(kernel, n, f32, r32, 2, 1);          \
+        else if (a.vec == 2) KDA_NORM_SIZES(kernel, n, f32, r32, 2, 0);                            \
+        else KDA_NORM_SIZES(kernel, n, f32, r32, 1, 0);                                            \
     } while (0)
 #define KDA_NORM_TYPES(kernel, n)                                                                  \
     do {                                                                                           \

@@ -67,8 +67,8 @@ int norm_partials(long long rows, int) { return (int)(rows < 2048 ? rows : 2048)
 static void norm_ok(const NormArgs& a) {
     ++launches;
     EXPECT(a.rows >= 0 && a.rows <= INT_MAX && a.C >= 1 && a.C <= kNormMaxC && a.rows <= (1LL << 40) / a.C);
-    EXPECT(!a.vec || a.C % 8 == 0);
-    EXPECT(a.group == 0 || (a.group == 128 && a.C % 128 == 0 && a.vec));
+    EXPECT(a.vec >= 1 && a.vec <= 8 && a.C % a.vec == 0);
+    EXPECT(a.group == 0 || (a.group == 128 && a.C % 128 == 0 && a.vec == 8));
 }
 hipError_t launch_add_norm(const NormArgs& a, hipStream_t) { norm_ok(a); return hipSuccess; }
 hipError_t launch_add_norm_bwd(const NormArgs& a, hipStream_t) {

@@ -137,7 +137,7 @@ def make(rows, C, dtype, res, seed):
 
 
 SHAPES = [(1, 1), (3, 7), (5, 8), (37, 64), (2, 100), (130, 128), (9, 512), (3, 520), (4, 1000), (33, 2048), (3, 2049), (5, 4096),
-          (2, 4104), (3, 8192), (2, 8200), (2, 12288), (1, 16384), (2, 9001), (3, 16383), (700, 136), (301, 100), (67, 250), (9, 256), (65, 1024), (130, 600)]
+          (2, 4104), (3, 8192), (2, 8200), (2, 12288), (1, 16384), (2, 9001), (3, 16383), (700, 136), (301, 100), (67, 250), (9, 256), (65, 1024), (130, 600), (3, 1002), (5, 9004), (2, 4098)]
 TYPES = [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "float32"), ("bfloat16", None), ("float32", None)]
 
 
@@ -211,7 +211,7 @@ def test_many_rows(kda):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("C", [96, 256, 1000, 2048, 9008])
+@pytest.mark.parametrize("C", [96, 256, 1000, 1002, 1004, 2048, 9008])
 @pytest.mark.parametrize("mib", [300, 700])
 @pytest.mark.parametrize("dtype,res", TYPES)
 def test_calls_beyond_the_cache(kda, dtype, res, mib, C):
