@@ -322,7 +322,8 @@ __global__ __launch_bounds__(1024) void kda_add_norm_bwd_kernel(NormArgs a, int 
             sum[1] += n[e] * (y[e] * w[e]);
         }
         over_row<false, LANES>(sum, s[turn], wpr);
-        const float k = 1.f / sqrtf(sum[0] / a.C + a.eps), m = sum[1] * k / a.C;
+        // (zero where there is no row: with eps = 0 the zeros read there would make it infinite)
+        const float k = at.sub < at.rows ? 1.f / sqrtf(sum[0] / a.C + a.eps) : 0.f, m = sum[1] * k / a.C;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
             n[e] *= k;

@@ -536,8 +536,10 @@ kda_status_t kda_scan_recurrent(const void* x, const float* g, const int32_t* cu
  * The norm is of r as it is stored. residual == NULL: r = x, and r_out is not
  * written. y == x and r_out == residual are allowed. C is 1 to 16,384, rows times C at
  * most 2^40 and rows at most 2^31 - 1 (KDA_ERR_SHAPE); a negative or non-finite
- * eps or another res_dtype is KDA_ERR_UNSUPPORTED. Rows of a multiple of eight
- * channels, in tensors that are all 16-byte aligned, are the fast ones.
+ * eps or another res_dtype is KDA_ERR_UNSUPPORTED. With eps == 0 a row of zeros has
+ * no norm: its results, and dweight, are NaN. Squares are added in fp32, so a row
+ * whose sum of squares leaves fp32's range has none either. Rows of a multiple of
+ * eight channels, in tensors that are all 16-byte aligned, are the fast ones.
  *
  * kda_add_norm_q8 gives y in 8 bits: with amax over a row (group == 0) or over
  * groups of 128 channels (group == 128, C a multiple of 128, every pointer

@@ -317,3 +317,27 @@ def test_streams_and_graphs(kda):
         other = both()
         torch.cuda.synchronize()
         assert same(held, want) and same(other, want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,res", [("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "float32")])
+@pytest.mark.parametrize("C", [8, 100, 128, 200, 256, 600, 1000, 1024, 1025, 2048])
+def test_eps_of_zero(kda, C, dtype, res, monkeypatch):
+    """eps = 0 over rows that are not zero, at numbers of rows that fill a workgroup or do not."""
+    monkeypatch.setitem(globals(), "EPS", 0.0)              # of the references
+    gen = torch.Generator().manual_seed(8)
+    n = lambda *s: torch.randn(*s, generator=gen)
+    dt, rt = getattr(torch, dtype), getattr(torch, res)
+    for rows in (1, 4, 7, 9, 16, 17):
+        x, r0, w, dy, dr = n(rows, C).to(dt), (3 * n(rows, C)).to(rt), 1 + 0.3 * n(C), n(rows, C).to(dt), n(rows, C).to(rt)
+        r, r64 = stream(x, r0)
+        y, rr = kda.add_norm(x.cuda(), r0.cuda(), w.cuda(), eps=0.0)
+        dx, dres, dw = kda.add_norm_bwd(r.cuda(), w.cuda(), dy.cuda(), dr=dr.cuda(), eps=0.0)
+        torch.cuda.synchronize()
+        want = norm(r64, w.double().numpy())
+        assert torch.equal(rr.cpu(), r)
+        R.held(as64(y), want, rel(C) * np.abs(want), f"y, {rows} rows", dtype)
+        d, sums, bd, bw = grad(r64, w.double().numpy(), dy.double().numpy(), dr.double().numpy())
+        R.held(as64(dx), d, bd, "dx", dtype)
+        R.held(as64(dres), d, bd, "dres", res)
+        R.held(as64(dw), sums, bw, f"dw, {rows} rows")
