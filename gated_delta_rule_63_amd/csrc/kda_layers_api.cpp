@@ -89,7 +89,7 @@ size_t scan_bytes(const kda_scan_desc_t* d, bool back, bool with_states) {
     const size_t row = up16(4 * (size_t)most_slots(d) * d->C);
     size_t n = back && !with_states ? row : 0;
     for (const bool packed : {false, true})
-        if (kda::scan_width(form(d, packed, back, with_states), compute_units()) == 0) return n + 3 * row;
+        if (kda::scan_width(form(d, packed, back, with_states), compute_units()) == 0) return n + 4 * row;
     return n;
 }
 
@@ -105,6 +105,7 @@ void cut_scan(kda::ScanArgs* a, const kda_scan_desc_t* d, bool back) {
         a->decays = reinterpret_cast<float*>(w);
         a->adds = reinterpret_cast<float*>(w + row);
         a->grads = reinterpret_cast<float*>(w + 2 * row);
+        a->bigs = reinterpret_cast<float*>(w + 3 * row);
         if (!back && !a->states && !a->fold) a->states = a->grads;   // which the forward does not have
     }
 }

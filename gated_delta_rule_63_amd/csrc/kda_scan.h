@@ -23,11 +23,12 @@ struct ScanArgs {
     void* dx;
     float* dg;
     float* dh0;                   // [N, C], nullptr: not written
-    // workspace of the split form, [scan_slots(), C] each: a chunk's decay, what it adds to the state, and
-    // what it adds to the gradient, in whose place the gradient that leaves it is put
+    // workspace of the split form, [scan_slots(), C] each: a chunk's decay, what it adds to the state,
+    // what it adds to the gradient, in whose place the gradient that leaves it is put, and decays past fp32's range
     float* decays;
     float* adds;
     float* grads;
+    float* bigs;
     int T, C, N;
     long long slots;
     bool f32, leaky;

@@ -184,6 +184,13 @@ __device__ __forceinline__ int in_runs(int i, int n) {
     return i < per * 8 ? (i % 8) * per + i / 8 : i;
 }
 
+constexpr float kMost = 3.4028234663852886e38f;
+// Where gates grow, a product of decays may pass fp32's range though no state does (zero, or tiny
+// ones), and infinity times zero is no number. Over a thread's 16 tokens it is held at the largest
+// finite number: a zero state stays zero whatever the gates, one that is not is right while they sum to 88 at
+// most; and a product that is no number is that of a reset, behind growth past all numbers.
+__device__ __forceinline__ float held(float A) { return fminf(fmaxf(A, 0.f), kMost); }
+
 // One tile forwards, from the state h that enters it to the one that leaves it.
 template <bool ALL, bool F32, bool LEAKY, int SW, int LD, int ST>
 struct Tile {
@@ -211,7 +218,7 @@ struct Tile {
             A *= d[i];
             B = fmaf(d[i], B, b[i]);
         }
-        s[p.sub][p.l] = make_float2(A, B);
+        s[p.sub][p.l] = make_float2(held(A), B);
         lds_barrier();
         float in = h;
 #pragma unroll
@@ -296,7 +303,7 @@ struct TileBwd {
         }
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) E = d[i] * (u[i] + E);
-        s[p.sub][p.l] = make_float2(A, B);
+        s[p.sub][p.l] = make_float2(held(A), B);
         sd[p.sub][p.l] = E;
         lds_barrier();
         float into = D;
@@ -374,6 +381,40 @@ __global__ __launch_bounds__(64 * W) void kda_scan_walk_bwd(ScanArgs a) {
 // ------------------------------------------------------------- chunks side by side
 static_assert(W * L == kScanChunk, "a tile of 64 channels is a chunk");
 
+// Decays of a chunk and of runs of chunks pass fp32's range with moderate growth already. Neither
+// infinity nor NaN becomes finite again in a product, or in a state that runs on, so one look at its end
+// tells, and the lanes that need it form it again: a decay A past fp32 is infinity, with A / 2^127 in a place
+// beside it, and a state passes it as (A / 2^127) (h 2^127) + B, where h 2^127 is exact. (A goes up to 2^255, beyond
+// which only a state of zero or below 2^-126 stays in range.)
+template <int NS, int SW>
+struct Runs {
+    float2 m[NS][SW];             // A, B
+    float big[NS][SW];            // where A is infinity
+};
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
+__device__ __forceinline__ float narrow(double A, float& big) {
+    if (A <= kMost) return (float)A;
+    big = (float)fmin(A * 0x1p-127, (double)kMost);
+    return INFINITY;
+}
+// One decay more. (It stays finite: a reset after any growth gives zero.)
+__device__ __forceinline__ double times(double A, double d) { return fmin(A * d, 0x1p400); }
+__device__ __forceinline__ double decay_at(const ScanArgs& a, long long at) {
+    const float d = a.decays[at];
+    return finite(d) ? (double)d : (double)a.bigs[at] * 0x1p127;
+}
+// The state behind all runs of a channel, from h, and on the way the one before run `sub`.
+template <int NS, int SW>
+__device__ __forceinline__ float through(const Runs<NS, SW>& s, int l, float h, int sub, float& in) {
+#pragma unroll 1
+    for (int j = 0; j < NS; ++j) {
+        const float2 m = s.m[j][l];
+        if (j == sub) in = h;
+        h = finite(m.x) ? fmaf(m.x, h, m.y) : fmaf(s.big[j][l], h * 0x1p127f, m.y);
+    }
+    return h;
+}
+
 // A chunk's decay and what it adds to the state (FWD) and to the gradient (BWD).
 template <bool F32, bool LEAKY, bool FWD, bool BWD>
 __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
@@ -410,7 +451,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
     if constexpr (BWD)
 #pragma unroll
         for (int i = L - 1; i >= 0; --i) E = d[i] * (up(dy[i]) + E);
-    sh[p.sub][p.l] = make_float2(A, B);
+    sh[p.sub][p.l] = make_float2(held(A), B);
     sd[p.sub][p.l] = E;
     lds_barrier();
     if (p.sub > 0 || !p.on) return;
@@ -424,6 +465,12 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
 #pragma unroll
     for (int j = W - 1; j >= 0; --j) E = fmaf(sh[j][p.l].x, E, sd[j][p.l]);
     const long long at = slot * a.C + p.c;
+    if (!finite(A)) {
+        double w = 1.0;
+#pragma unroll 1
+        for (int j = 0; j < W; ++j) w = times(w, sh[j][p.l].x);
+        A = narrow(w, a.bigs[at]);
+    }
     a.decays[at] = A;
     if constexpr (FWD) a.adds[at] = B;
     if constexpr (BWD) a.grads[at] = E;
@@ -433,7 +480,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_sums(ScanArgs a) {
 // gradients that leave them: the same fold, of chunks instead of tokens.
 // Workgroups of SC channels by NC runs of L chunks: 16 by 64 for long sequences, else 64 by 4.
 template <bool BACK, int SC, int NC>
-__device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, float2 (*sh)[NC][SC]) {
+__device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, Runs<NC, SC>* sh) {
     const int l = threadIdx.x % SC, sub = threadIdx.x / SC, c = strip * SC + l, cc = min(c, a.C - 1);
     const Run run = sequence(a, n);
     const int chunks = (run.len + kScanChunk - 1) / kScanChunk;
@@ -456,29 +503,54 @@ __device__ __forceinline__ void combine(const ScanArgs& a, int n, int strip, flo
             A *= d[i];
             B = fmaf(d[i], B, b[i]);
         }
-        sh[k & 1][sub][l] = make_float2(A, B);
+        Runs<NC, SC>& s = sh[k & 1];
+        const bool fits = finite(A);               // and so does each of its factors
+        if (!fits) {
+            double w = 1.0, add = 0.0;
+#pragma unroll 1
+            for (int i = row; i < min(row + L, chunks); ++i) {
+                const long long at = place(i);
+                const double x = decay_at(a, at);
+                w = times(w, x);
+                add = fma(x, add, (double)from[at]);
+            }
+            A = narrow(w, s.big[sub][l]), B = (float)add;
+        }
+        s.m[sub][l] = make_float2(A, B);
         lds_barrier();
+        const float before = h;
         float in = h;
 #pragma unroll NC < 16 ? NC : 16
         for (int j = 0; j < NC; ++j) {
-            const float2 m = sh[k & 1][j][l];
+            const float2 m = s.m[j][l];
             if (j == sub) in = h;
             h = fmaf(m.x, h, m.y);
         }
-        if (c < a.C)
+        if (!finite(h)) h = through(s, l, before, sub, in);
+        if (c < a.C && fits) {
 #pragma unroll
             for (int i = 0; i < L; ++i)
                 if (row + i < chunks) {
                     to[place(row + i)] = in;
                     in = fmaf(d[i], in, b[i]);
                 }
+        } else if (c < a.C) {
+            double w = in;
+#pragma unroll 1
+            for (int i = row; i < min(row + L, chunks); ++i) {
+                const long long at = place(i);
+                const double add = from[at];       // (which may lie where the state goes)
+                to[at] = (float)w;
+                w = fma(decay_at(a, at), w, add);
+            }
+        }
     }
     if (end && sub == 0 && c < a.C) end[(long long)n * a.C + c] = h;
 }
 
 template <bool FWD, bool BWD, int SC, int NC>
 __global__ __launch_bounds__(SC * NC) void kda_scan_combine(ScanArgs a) {
-    __shared__ float2 sh[2][NC][SC];
+    __shared__ Runs<NC, SC> sh[2];
     const int strips = (a.C + SC - 1) / SC, both = a.N * strips;
     const int i = blockIdx.x < both ? blockIdx.x : blockIdx.x - both;
     if (FWD && (!BWD || blockIdx.x < both)) combine<false, SC, NC>(a, i / strips, i % strips, sh);
@@ -488,7 +560,7 @@ __global__ __launch_bounds__(SC * NC) void kda_scan_combine(ScanArgs a) {
 // The fold of a sequence's first `count` chunks (BACK: its last), by the workgroup that
 // works on the next one: each wave one run of them, then the runs.
 template <bool BACK>
-__device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chunks, int count, float h, int cc, const Lane<S>& p, float2 (*s)[S]) {
+__device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chunks, int count, float h, int cc, const Lane<S>& p, Runs<W, S>& s) {
     const float* const from = BACK ? a.grads : a.adds;
     const int per = (count + W - 1) / W, first = p.sub * per;
     float A = 1.f, B = 0.f;
@@ -508,11 +580,23 @@ __device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chu
             B = fmaf(d[u], B, b[u]);
         }
     }
-    s[p.sub][p.l] = make_float2(A, B);
+    if (!finite(A)) {
+        double w = 1.0, add = 0.0;
+#pragma unroll 1
+        for (int j = first; j < min(first + per, count); ++j) {
+            const long long at = (run.slot + (BACK ? chunks - 1 - j : j)) * a.C + cc;
+            const double x = decay_at(a, at);
+            w = times(w, x);
+            add = fma(x, add, (double)from[at]);
+        }
+        A = narrow(w, s.big[p.sub][p.l]), B = (float)add;
+    }
+    s.m[p.sub][p.l] = make_float2(A, B);
     lds_barrier();
+    const float start = h;
 #pragma unroll
-    for (int j = 0; j < W; ++j) h = fmaf(s[j][p.l].x, h, s[j][p.l].y);
-    return h;
+    for (int j = 0; j < W; ++j) h = fmaf(s.m[j][p.l].x, h, s.m[j][p.l].y);
+    return finite(h) ? h : through(s, p.l, start, -1, h);
 }
 
 // A chunk from the state that enters it (FOLD: which it forms itself); the last ones
@@ -521,7 +605,8 @@ __device__ __forceinline__ float fold(const ScanArgs& a, const Run& run, int chu
 template <bool F32, bool LEAKY, bool FOLD, bool STREAM>
 __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
     constexpr int ST = STREAM ? kPast : 0;
-    __shared__ float2 sh[2][W][S];
+    __shared__ float2 sh[W][S];
+    __shared__ Runs<W, S> sf;
     const int strips = (a.C + S - 1) / S;
     const int i = a.C % S ? in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     const long long slot = a.slots - 1 - i / strips;
@@ -532,7 +617,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
     if (slot < run.slot || t >= run.len) return;
     float h;
     if constexpr (FOLD) {
-        h = fold<false>(a, run, 0, t / kScanChunk, a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f, cc, p, sh[1]);
+        h = fold<false>(a, run, 0, t / kScanChunk, a.h0 ? a.h0[(long long)n * a.C + cc] : 0.f, cc, p, sf);
     } else {
         h = a.states[slot * a.C + cc];
         a.states = nullptr;                        // they are there
@@ -540,11 +625,11 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
     if (t + kScanChunk <= run.len) {
         Tile<true, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
-        h = tile.run(a, run, p, t, h, sh[0], [] {});
+        h = tile.run(a, run, p, t, h, sh, [] {});
     } else {
         Tile<false, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
-        h = tile.run(a, run, p, t, h, sh[0], [] {});
+        h = tile.run(a, run, p, t, h, sh, [] {});
     }
     if (FOLD && a.hT && t + kScanChunk >= run.len && p.sub == 0 && p.on) a.hT[(long long)n * a.C + p.c] = h;
 }
@@ -554,8 +639,9 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
 template <bool F32, bool LEAKY, bool FOLD, bool STREAM>
 __global__ __launch_bounds__(64 * W, 4) void kda_scan_chunks_bwd(ScanArgs a, bool known) {
     constexpr int ST = STREAM ? kPast : 0;
-    __shared__ float2 sh[3][W][S];
+    __shared__ float2 sh[W][S];
     __shared__ float sd[W][S];
+    __shared__ Runs<W, S> sf[2];
     const int strips = (a.C + S - 1) / S;
     const int i = a.C % S ? in_runs(blockIdx.x, gridDim.x) : blockIdx.x;
     const long long slot = a.slots - 1 - i / strips;
@@ -568,9 +654,9 @@ __global__ __launch_bounds__(64 * W, 4) void kda_scan_chunks_bwd(ScanArgs a, boo
     if constexpr (FOLD) {
         const int chunks = (run.len + kScanChunk - 1) / kScanChunk, j = t / kScanChunk;
         const long long at = (long long)n * a.C + cc;
-        D = fold<true>(a, run, chunks, chunks - 1 - j, a.dhT ? a.dhT[at] : 0.f, cc, p, sh[1]);
+        D = fold<true>(a, run, chunks, chunks - 1 - j, a.dhT ? a.dhT[at] : 0.f, cc, p, sf[0]);
         if (known) h = a.states[slot * a.C + cc];
-        else h = fold<false>(a, run, chunks, j, a.h0 ? a.h0[at] : 0.f, cc, p, sh[2]);
+        else h = fold<false>(a, run, chunks, j, a.h0 ? a.h0[at] : 0.f, cc, p, sf[1]);
     } else {
         h = a.states[slot * a.C + cc];
         D = a.grads[slot * a.C + cc];
@@ -578,11 +664,11 @@ __global__ __launch_bounds__(64 * W, 4) void kda_scan_chunks_bwd(ScanArgs a, boo
     if (t + kScanChunk <= run.len) {
         TileBwd<true, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
-        D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
+        D = tile.run(a, run, p, t, h, D, sh, sd, [] {});
     } else {
         TileBwd<false, F32, LEAKY, S, 0, ST> tile;
         tile.get(a, run, p, t);
-        D = tile.run(a, run, p, t, h, D, sh[0], sd, [] {});
+        D = tile.run(a, run, p, t, h, D, sh, sd, [] {});
     }
     if (FOLD && a.dh0 && t == 0 && p.sub == 0 && p.on) a.dh0[(long long)n * a.C + p.c] = D;
 }

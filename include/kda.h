@@ -487,8 +487,12 @@ size_t kda_block_out_bwd_workspace_size(const kda_desc_t* desc);
  *             holds chunk j of sequence n; packed, row cu[n] / 128 + n + j. Rows
  *             without a chunk are left as they were.
  * C is any number of channels (heads times head size, say); nothing needs more
- * alignment than its type. g is usually <= 0; -inf is a reset (nothing of the
- * state before it remains), and g > 0 a growing state (above 88 its decay is not a number).
+ * alignment than its type. g is usually <= 0; -inf is a reset (nothing of a finite
+ * state before it remains), and g > 0 a growing state: gates of 16 tokens in a row, or of
+ * fewer, sum to 88 at most, unless the state that they meet is zero (of one token: 88 in any
+ * case), and over longer runs to anything that leaves every state finite. Decays of up
+ * to 4096 tokens are multiplied in fp32: behind gates that sum to less than -87 a
+ * state counts as zero, though gates above zero follow. The same holds of the gradient.
  * The state is fp32. y == x and hT == h0 are allowed; rows of tokens outside [cu[0], cu[N]) are left as they were;
  * a zero-length sequence has hT = h0. T is at most 2^30, B T C 2^40, C 2^20 and
  * N ceil(C / 64) 2^22 (KDA_ERR_SHAPE). Needs desc->workspace of

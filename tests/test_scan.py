@@ -443,3 +443,91 @@ def test_streams_and_graphs(kda):
         other = both()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, want)) and all(torch.equal(a, b) for a, b in zip(other, want))
+
+
+def growing(B, T, C, dtype, lens, leaky, seed):
+    """Gates above zero, in nine kinds of channels whose states, and gradients, stay finite
+    throughout: growth over zeros (slow, fast and within a few tokens) until inputs come, a tiny state that grows, growth
+    and decay in turn, a reset after growth, a large state that decays and grows back, ordinary
+    decays, and differences of bounded values."""
+    gen = torch.Generator().manual_seed(seed)
+    n = lambda *s: torch.randn(*s, generator=gen)
+    u = lambda *s: torch.rand(*s, generator=gen)
+    bounds = R.bounds_of(lens, B, T)
+    x, dy, g = n(B, T, C), n(B, T, C), torch.zeros(B, T, C)
+    h0, dhT = torch.zeros(len(bounds), C), torch.zeros(len(bounds), C)
+    for s, (r, t0, t1) in enumerate(bounds):
+        k, at, half = t1 - t0, slice(t0, t1), (t1 - t0) // 2
+        if k == 0:
+            continue
+        for kind, gate, window in ((0, 0.05, 400), (1, 0.7, 60), (8, 12.0, 4)):
+            g[r, at, kind::9] = gate
+            x[r, t0:max(t1 - window, t0), kind::9] = 0.0
+            dy[r, min(t0 + window, t1):t1, kind::9] = 0.0
+        g[r, at, 2::9] = min(5.0, 100.0 / k)
+        x[r, at, 2::9] = dy[r, at, 2::9] = 0.0
+        h0[s, 2::9] = dhT[s, 2::9] = 1e-30
+        g[r, at, 3::9] = (60.0 - 120.0 * (torch.arange(k) % 2))[:, None]
+        g[r, at, 4::9] = 0.7
+        g[r, t0 + half:t1, 4::9] = -0.5
+        g[r, t0 + half, 4::9] = -float("inf")
+        x[r, t0:t0 + half, 4::9] = 0.0
+        dy[r, min(t0 + 60, t0 + half):t0 + half, 4::9] = 0.0
+        if half:
+            step = min(80.0, 40.0 * half) / half
+            g[r, t0:t0 + half, 5::9] = -step
+            g[r, t0 + half:t0 + 2 * half, 5::9] = step
+        x[r, at, 5::9] = dy[r, at, 5::9] = 0.0
+        h0[s, 5::9], dhT[s, 5::9] = 1e20, 1e-10
+        g[r, at, 6::9] = -2 * u(k, C)[:, 6::9]
+        w = 20 * u(k + 1, C)[:, 7::9] - 10
+        g[r, at, 7::9] = w[1:] - w[:-1]
+    dt = getattr(torch, dtype)
+    return dict(x=x.to(dt), g=g, dy=dy.to(dt), h0=h0, dhT=dhT, bounds=bounds,
+                cu=torch.tensor(np.cumsum([0] + list(lens)), dtype=torch.int32) if lens else None)
+
+
+GROWING = [  # lengths (None: rows of T), B, T, C, type
+    (None, 2, 1, 16, "float32"),
+    (None, 1, 128, 64, "float32"),                      # a workgroup a strip: 16, 32 and 64 channels
+    (None, 2, 257, 100, "bfloat16"),
+    (None, 40, 150, 260, "float32"),
+    (None, 40, 300, 130, "bfloat16"),
+    ((130, 5, 300, 0, 64), 1, 499, 64, "float32"),
+    (None, 1, 4300, 67, "bfloat16"),                    # chunks side by side, each folding those before it
+    (None, 1, 9000, 40, "float32"),
+    ((900, 0, 70, 1500, 129), 1, 2599, 1000, "float32"),
+    (None, 1, 33000, 24, "bfloat16"),                   # with the fold in a launch of its own
+    (None, 1, 12800, 1300, "float32"),
+    ((20000, 0, 13001), 1, 33001, 33, "float32"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("leaky", [False, True])
+@pytest.mark.parametrize("lens,B,T,C,dtype", GROWING)
+def test_growing_gates(kda, lens, B, T, C, dtype, leaky):
+    """Where no state overflows none of the composed decays does, in any form, forwards and back."""
+    s = growing(B, T, C, dtype, lens, leaky, 14)
+    x, g, dy, cu, h0, dhT = (on(s[n]) for n in ("x", "g", "dy", "cu", "h0", "dhT"))
+    y, hT, kept = kda.scan(x, g, cu_seqlens=cu, initial_state=h0, leaky=leaky, output_chunk_states=True)
+    grads = [kda.scan_bwd(x, g, dy, cu_seqlens=cu, initial_state=h0, d_final_state=dhT, chunk_states=states, leaky=leaky)
+             for states in (kept, None)]
+    torch.cuda.synchronize()
+    args = [as64(s[n]) for n in ("x", "g")]
+    back = lambda leaky: R.scan_bwd(*args, as64(s["dy"]), s["bounds"], as64(s["h0"]), as64(s["dhT"]), leaky)
+    h, rT, e, eT = R.scan(*args, s["bounds"], as64(s["h0"]), leaky)
+    ref, off = back(leaky)
+    if leaky:
+        # the factor 1 - e^g of an input is off by 2 e^g / (e^g - 1) + 1 half steps, 6.1 at most (g = 1/2), and its product
+        # by one more: 8 where the references have 6. dx is off by |1 - e^g| times D's error (D is dx without the
+        # factor), and by 8 half steps of its own
+        (D, _, _), (eD, _, _) = back(False)
+        f = np.abs(np.expm1(args[1]))
+        off = (f * (eD - 5 * R.U * np.abs(D)) + 8 * R.U * f * np.abs(D), off[1] * 8 / 6, off[2])
+        e, eT = e * 8 / 6, eT * 8 / 6
+    R.held(as64(y), h, e, "y", dtype)
+    R.held(as64(hT), rT, eT, "hT")
+    for got, states in zip(grads, ("kept", "formed again")):
+        for v, want, bound, what, t in zip(got, ref, off, ("dx", "dg", "dh0"), (dtype, "float32", "float32")):
+            R.held(as64(v), want, bound, f"{what}, states {states}", t)
