@@ -21,6 +21,24 @@ def _plain(name, t, shape, dtype, device, _device=True):
         _rows(name, t, shape, dtype, device, _device)
 
 
+def _span(t):
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
+
+
+def _place(name, out, inputs=(), others=()):
+    """An output may lie exactly where one of `inputs` does; otherwise it overlaps none of them, nor of `others`."""
+    if out is None:
+        return
+    a0, a1 = _span(out)
+    for other, same in [(t, True) for t in inputs] + [(t, False) for t in others]:
+        if other is None or other is out and same:
+            continue
+        b0, b1 = _span(other)
+        if a0 < b1 and b0 < a1 and not (same and (a0, a1) == (b0, b1)):
+            raise ValueError(f"{name} may not overlap another argument of the call")
+
+
 def _bytes(n: int, like: torch.Tensor) -> _Tensor:
     return like.new_empty(n, dtype=torch.uint8) if n else None
 
@@ -194,26 +212,35 @@ def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: floa
     """r = x + residual, and the RMS norm of r over the last dimension, r / sqrt(mean(r^2) + eps) *
     weight. x [..., C] bf16 or fp32; residual of the same shape, in x's dtype or fp32, or None
     (r is x then); weight fp32 [C]. Returns (y in x's dtype, r in residual's). out may be x,
-    residual_out may be residual (the stream updated in place)."""
+    residual_out may be residual (the stream updated in place). With out in x's place and no
+    residual r is overwritten, and returned as None: add_norm_bwd() needs a copy of x then."""
     d = _check_norm(x, residual, weight)
-    _plain("out", out, x.shape, x.dtype, x.device)
+    _check_norm_out(x, residual, weight, out, residual_out)
     with _on(x.device, stream) as s:
         y = torch.empty_like(x) if out is None else out
         r = _sum_out(x, residual, residual_out)
+        if residual is None and out is not None and out.data_ptr() == x.data_ptr():
+            r = None
         _call("kda_add_norm", _ptr(x), _ptr(residual), _ptr(weight), eps, _ptr(y), _ptr(r) if residual is not None else None,
               ctypes.byref(d), s)
     return y, r
 
 
+def _check_norm_out(x, residual, weight, out, residual_out, _device=True):
+    if out is not None:
+        _rows("out", out, x.shape, x.dtype, x.device, _device)
+        _place("out", out, (x, residual), (weight, residual_out))
+    if residual_out is not None:
+        if residual is None:
+            raise ValueError("residual_out needs a residual")
+        _rows("residual_out", residual_out, residual.shape, residual.dtype, residual.device, _device)
+        _place("residual_out", residual_out, (x, residual), (weight,))
+
+
 def _sum_out(x, residual, residual_out):
     if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out needs a residual")
         return x
-    if residual_out is None:
-        return torch.empty_like(residual)
-    _rows("residual_out", residual_out, residual.shape, residual.dtype, residual.device, False)
-    return residual_out
+    return torch.empty_like(residual) if residual_out is None else residual_out
 
 
 def add_norm_q8(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, group: int = 0, eps: float = 1e-5,
@@ -224,6 +251,7 @@ def add_norm_q8(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, group:
     d = _check_norm(x, residual, weight)
     if group not in (0, 128) or (group and d.C % group):
         raise ValueError("group must be 0 (a row) or 128, with a multiple of 128 channels")
+    _check_norm_out(x, residual, weight, None, residual_out)
     with _on(x.device, stream) as s:
         q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
         scales = weight.new_empty((*x.shape[:-1], d.C // group) if group else x.shape[:-1])
@@ -251,6 +279,8 @@ def add_norm_bwd(r: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dr: _T
 
 
 def _check_norm_bwd(r, weight, dy, dr, _device=True) -> NormDesc:
+    if r is None:
+        raise ValueError("r must be the sum that add_norm() normed")
     d = _check_norm(dy, r, weight, _device)
     _plain("dr", dr, r.shape, r.dtype, r.device, _device)
     return d

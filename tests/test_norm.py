@@ -114,6 +114,30 @@ def test_binding_refusals():
         ok(x=x, w=w) and M._check_norm(x, x, w)         # not on a GPU
 
 
+def test_outputs_in_the_place_of_inputs():
+    """An output exactly where an input lies, or apart from all of them and from the other one."""
+    from gated_delta_rule_63_amd import _layers as M
+    x, res, w = torch.zeros(4, 64), torch.zeros(4, 64), torch.zeros(64)
+    ok = lambda x=x, res=res, w=w, out=None, rout=None: M._check_norm_out(x, res, w, out, rout, _device=False)
+    ok()
+    ok(out=x, rout=res)
+    ok(out=res)
+    ok(rout=x)
+    ok(out=torch.zeros(4, 64), rout=torch.zeros(4, 64))
+    ok(res=None, out=x)
+    five = torch.zeros(5, 64)
+    half, wide = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64)
+    for kw in (dict(out=res, rout=res), dict(out=x, rout=x), dict(x=five[:4], out=five[1:]), dict(res=five[:4], rout=five[1:]),
+               dict(res=five[1:], out=five[:4]), dict(w=five[0], out=five[:4]), dict(w=five[3], rout=five[:4]),
+               dict(x=half, res=wide, out=wide.view(torch.bfloat16).flatten()[:256].view(4, 64)), dict(res=None, rout=torch.zeros(4, 64))):
+        with pytest.raises(ValueError):
+            ok(**kw)
+    none = torch.zeros(0, 64)
+    ok(x=none, res=none, out=none, rout=none)
+    with pytest.raises(ValueError):
+        M._check_norm_bwd(None, w, x, None, _device=False)
+
+
 # ------------------------------------------------------------------------- GPU
 
 @pytest.fixture
@@ -341,3 +365,18 @@ def test_eps_of_zero(kda, C, dtype, res, monkeypatch):
         R.held(as64(dx), d, bd, "dx", dtype)
         R.held(as64(dres), d, bd, "dres", res)
         R.held(as64(dw), sums, bw, f"dw, {rows} rows")
+
+
+@pytest.mark.gpu
+def test_in_place_without_a_residual(kda):
+    """The norm in x's place leaves no sum to return; elsewhere x is the sum."""
+    x, _, w, dy, _ = (t.cuda() for t in make(5, 200, "float32", "float32", 9))
+    y, r = kda.add_norm(x, None, w)
+    assert r is x and kda.add_norm(x[:0], None, w)[1].shape == (0, 200)
+    xi = x.clone()
+    got, lost = kda.add_norm(xi, None, w, out=xi)
+    assert got is xi and lost is None and torch.equal(got, y)
+    with pytest.raises(ValueError):
+        kda.add_norm_bwd(lost, w, dy)
+    with pytest.raises(ValueError):
+        kda.add_norm(x, x, w, out=xi, residual_out=xi)
