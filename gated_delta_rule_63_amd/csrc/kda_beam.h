@@ -9,7 +9,7 @@ namespace kda {
 
 constexpr int kBeamMax = 64;           // beams of a batch entry, and places selected
 
-// A part of a row: its largest logit, sum of exp(logit - max), and its best
+// A part of a row: its largest logit, or one at most one below it, sum of exp(logit - max), and its best
 // candidates as keys (see kda_beam.hip), descending, zeros behind the last.
 struct BeamPart {
     float max;

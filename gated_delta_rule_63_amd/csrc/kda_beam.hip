@@ -246,7 +246,8 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     const int t0 = (int)((long long)tiles * part / a.splits), t1 = (int)((long long)tiles * (part + 1) / a.splits);
     const int tid = threadIdx.x;
     if (tid == 0) held = rows[0] = rows[1] = 0;
-    float m = -kHuge, sum = 0.f;
+    float m = -kHuge;
+    double sum = 0.0;
     uint32_t floor = 0;
     int turn = 0;
     Piece<F32> next[NV];
@@ -264,9 +265,12 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
             for (int e = 1; e < VE; ++e) top[i] = fmaxf(top[i], x[i][e]);
             tm = fmaxf(tm, top[i]);
         }
-        // sum of exp(x - m), m the thread's largest so far
+        // Sum of exp(x - m), m within one of the thread's largest so far: it follows by steps of more
+        // than one, since each step rounds what is there. A tile's 16 or 32 are added in fp32, the
+        // tiles in fp64: over many of them roundings may go one way (2^23 equal logits below the
+        // largest: 7e-6 off in fp32, in the same time).
         constexpr float kLog2e = 1.44269504f;
-        const float m1 = fminf(fmaxf(m, tm), kHuge);
+        const float tm1 = fminf(tm, kHuge), m1 = tm1 > m + 1.f ? tm1 : m;
         float add = 0.f;
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -280,7 +284,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
                 for (int e = 0; e < VE; ++e)
                     if (x[i][e] > -INFINITY) add += __builtin_amdgcn_exp2f((fminf(x[i][e], kHuge) - m1) * kLog2e);
         }
-        sum = sum * __builtin_amdgcn_exp2f((m - m1) * kLog2e) + add;
+        sum = fma(sum, (double)__builtin_amdgcn_exp2f((m - m1) * kLog2e), (double)add);
         m = m1;
         const uint32_t mine = order_of(tm);
         uint32_t* const bests = best[(t - t0) & 1];
@@ -347,7 +351,7 @@ __global__ __launch_bounds__(TH, 4) void kda_beam_rows(BeamArgs a) {
     float all = sm[0];
 #pragma unroll
     for (int i = 1; i < Q; ++i) all = fmaxf(all, sm[i]);
-    const double d = wave_all((double)(sum * expf(m - all)), [](double x, double y) { return x + y; });
+    const double d = wave_all(sum * (double)expf(m - all), [](double x, double y) { return x + y; });
     if ((tid & 63) == 0) ss[tid >> 6] = d;
     __syncthreads();
     double sums = ss[0];

@@ -588,8 +588,12 @@ size_t kda_add_norm_bwd_workspace_size(const kda_norm_desc_t* desc);
  *     out_scores fp32, parents int32 (the beam), tokens int32, each [B, K]
  * A logit of -inf or NaN is no candidate and adds nothing to the sum; +inf counts
  * as the largest finite value. Places beyond the last candidate hold -inf, -1, -1.
- * Totals are compared in fp64, formed from sums of fp32 exponentials (an error of
- * the order of 1e-7, the same for beams with the same logits). W and K are 1 to 64, V 1 to 2^25, B W at most 2^20 (KDA_ERR_SHAPE);
+ * Totals are compared in fp64, formed from fp32 exponentials that are added in fp32
+ * by 32 and in fp64 from there on, for any V: the total is off by at most
+ * (2 d + 23) 2^-24, d the distance below the largest logit of those that make up the
+ * sum, usually by some 1e-7, and by the same for beams with the same logits. Only a
+ * beam's K largest logits are looked at: where its score is so large (beyond 2^30, say) that
+ * totals of different logits are equal, those of the K largest tie. W and K are 1 to 64, V 1 to 2^25, B W at most 2^20 (KDA_ERR_SHAPE);
  * with done, eos lies in [0, V) (KDA_ERR_SHAPE). Needs desc->workspace of
  * kda_beam_workspace_size(desc) bytes, 16-byte aligned, used by one call at a time. */
 typedef struct kda_beam_desc {

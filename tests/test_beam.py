@@ -298,3 +298,38 @@ def test_streams_and_graphs(kda):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, eager)) and torch.equal(pool, after)
         assert all(torch.equal(a, b) for a, b in zip(other, want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["gap", "ramp"])
+def test_sums_of_long_rows(kda, kind):
+    """Totals of rows that one workgroup adds up (there are 1024 of them), against fp64: a largest
+    logit and all others at one distance below it, where roundings of a sum go one way; and
+    ascending or descending ones, where the largest so far changes with every tile."""
+    if kind == "gap":
+        V, first, d, at = 1 << 23, 8192, [3.0, 5.5, 8.0, 9.3125], [0] * 4
+        x = torch.empty(256, 4, V, dtype=torch.bfloat16, device="cuda")
+        for w in range(4):
+            x[:, w] = -d[w]
+            x[:, w, :first] = 0.0                       # every thread sees the largest first
+        logs = [np.log(first + (V - first) * np.exp(-d[w])) for w in range(4)]
+    else:
+        V, d = 1 << 20, [1.0, 0.37, 2.5, -1.0]
+        rows = [(torch.arange(V, dtype=torch.float64) * (s / V)).float() for s in d]
+        x = torch.stack(rows).cuda().expand(256, 4, V).contiguous()
+        at = [int(r.argmax()) for r in rows]
+        logs = [float(np.log(np.exp(R.f64(r) - float(r.max())).sum())) for r in rows]
+    # one candidate a beam: the others are masked by the scores of a call for each beam
+    for w in range(4):
+        scores = torch.full((256, 4), -float("inf"), device="cuda")
+        scores[:, w] = 0.0
+        best, parents, tokens = kda.beam_select(x, scores, k=1)
+        assert bool((parents == w).all()) and bool((tokens == at[w]).all()) and bool((best == best[0]).all())
+        want = -logs[w]                             # (the best one's logit is the largest)
+        off = abs(float(best[0, 0]) - want)
+        # relative to the sum: an exponential's argument 2 U a unit of distance, its value 2 U, 32 like ones added in turn
+        # sum of k / 32 U = 16.5 U, the exponential that brings two threads' sums together 4 U, and 4 U for each unit by
+        # which the largest moved; then the score's rounding
+        bound = (2 * abs(d[w]) + 22.5 + (4 * (abs(d[w]) + 1) if kind == "ramp" else 0)) * R.U + R.U * abs(want)
+        print(f"{kind} {d[w]}: off by {off / bound:.2f} of its bound", flush=True)
+        assert off <= bound, (kind, d[w], off, bound)
