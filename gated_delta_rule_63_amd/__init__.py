@@ -20,7 +20,8 @@ __all__ = ["fwd", "gdn_fwd", "fwd_noalloc", "noalloc_max_workspace", "fwd_worksp
            "bwd", "gdn_bwd", "bwd_workspace_size", "recurrent", "gdn_recurrent", "block_in", "gdn_block_in",
            "block_in_bwd", "gdn_block_in_bwd", "block_out", "block_out_bwd",
            "scan", "scan_workspace_size", "scan_bwd", "scan_bwd_workspace_size", "scan_recurrent",
-           "add_norm", "add_norm_q8", "add_norm_bwd", "beam_select", "beam_reorder"]
+           "add_norm", "add_norm_q8", "add_norm_bwd", "add_norm_bwd_workspace_size", "beam_select", "beam_workspace_size",
+           "beam_reorder"]
 
 D = 128
 
@@ -293,5 +294,6 @@ def fwd_staged(q, k, v, g, beta, cu_seqlens=None, initial_state=None, output_fin
 
 from ._ops import (block_in, block_in_bwd, block_out, block_out_bwd, bwd, bwd_workspace_size,  # noqa: E402
                    gdn_block_in, gdn_block_in_bwd, gdn_bwd, gdn_recurrent, recurrent)
-from ._layers import (add_norm, add_norm_bwd, add_norm_q8, beam_reorder, beam_select, scan, scan_bwd,  # noqa: E402
-                      scan_bwd_workspace_size, scan_recurrent, scan_workspace_size)
+from ._layers import (add_norm, add_norm_bwd, add_norm_bwd_workspace_size, add_norm_q8, beam_reorder,  # noqa: E402
+                      beam_select, beam_workspace_size, scan, scan_bwd, scan_bwd_workspace_size, scan_recurrent,
+                      scan_workspace_size)

@@ -9,7 +9,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._lib import BeamDesc, NormDesc, ScanDesc, lib
+from ._lib import KDA_F32, BeamDesc, NormDesc, ScanDesc, lib
 from ._ops import _DTYPES, _Tensor, _call, _on, _ptr, _rows
 
 SCAN_CHUNK = 128
@@ -267,7 +267,9 @@ def add_norm_bwd(r: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dr: _T
     gradient with respect to y (bf16 or fp32; r in dy's dtype or fp32), dr (r's dtype, None:
     zero) that with respect to r from where else it is used. Returns (dx in dy's dtype,
     d_residual in r's, dweight fp32): the gradients of x and of residual are the same sum, and
-    one tensor where the dtypes are. dweight takes every row."""
+    one tensor where the dtypes are. dweight takes every row. workspace: an optional device
+    tensor of add_norm_bwd_workspace_size() bytes, used by one call at a time; allocated
+    otherwise."""
     d = _check_norm_bwd(r, weight, dy, dr)
     with _on(r.device, stream) as s:
         dx, dw = torch.empty_like(dy), torch.empty_like(weight)
@@ -276,6 +278,14 @@ def add_norm_bwd(r: torch.Tensor, weight: torch.Tensor, dy: torch.Tensor, dr: _T
         _call("kda_add_norm_bwd", _ptr(r), _ptr(weight), eps, _ptr(dy), _ptr(dr), _ptr(dx), None if dres is dx else _ptr(dres),
               _ptr(dw), _with(d, ws), s)
     return dx, dres, dw
+
+
+def add_norm_bwd_workspace_size(dy: torch.Tensor) -> int:
+    """Bytes of device workspace add_norm_bwd() uses for a gradient shaped like dy, on the current device."""
+    if dy.dim() < 1 or dy.shape[-1] < 1:
+        raise ValueError("dy must be a [..., C] tensor")
+    C = dy.shape[-1]
+    return int(lib().kda_add_norm_bwd_workspace_size(ctypes.byref(NormDesc(dy.numel() // C, C, KDA_F32, KDA_F32, None, 0))))
 
 
 def _check_norm_bwd(r, weight, dy, dr, _device=True) -> NormDesc:
@@ -314,7 +324,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
     lowest beam, then token. logits [B, W, V] bf16 or fp32, scores fp32 [B, W] (-inf: a dead
     beam). done: bool [B, W], beams that have ended: each has one candidate, eos with its score
     unchanged, and its logits are not read. Returns (scores fp32, parents int32, tokens int32),
-    each [B, k]; places beyond the last candidate hold -inf, -1, -1."""
+    each [B, k]; places beyond the last candidate hold -inf, -1, -1. workspace: an optional device
+    tensor of beam_workspace_size() bytes, used by one call at a time; allocated otherwise."""
     d = _check_beam(logits, scores, k, done, eos)
     with _on(logits.device, stream) as s:
         ws = _workspace(workspace, int(lib().kda_beam_workspace_size(ctypes.byref(d))), logits)
@@ -323,6 +334,15 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = N
         tokens = torch.empty_like(parents)
         _call("kda_beam_select", _ptr(logits), _ptr(scores), _ptr(done), _ptr(best), _ptr(parents), _ptr(tokens), _with(d, ws), s)
     return best, parents, tokens
+
+
+def beam_workspace_size(logits: torch.Tensor, k: Optional[int] = None) -> int:
+    """Bytes of device workspace beam_select() uses for logits shaped like these, on the current device."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, W, V]")
+    B, W, V = logits.shape
+    d = BeamDesc(B, W, V, W if k is None else k, _DTYPES.get(logits.dtype, -1), -1, None, 0)
+    return int(lib().kda_beam_workspace_size(ctypes.byref(d)))
 
 
 def _check_reorder(pool, slots, parents, out, _device=True):

@@ -572,7 +572,7 @@ kda_status_t kda_add_norm_q8(const void* x, const void* residual, const float* w
  * (NULL: not written). dweight [C] fp32, over every row, in a fixed order (0 rows:
  * zero). dx == dy and d_residual == dr are allowed. Needs desc->workspace of
  * kda_add_norm_bwd_workspace_size(desc) bytes, 16-byte aligned, used by one call
- * at a time. */
+ * at a time (sizes of workspaces hold for the current device, here and below). */
 kda_status_t kda_add_norm_bwd(const void* r, const float* weight, float eps, const void* dy, const void* dr,
                               void* dx, void* d_residual, float* dweight, const kda_norm_desc_t* desc, void* stream);
 size_t kda_add_norm_bwd_workspace_size(const kda_norm_desc_t* desc);

@@ -114,6 +114,18 @@ def test_binding_refusals():
         ok(x=x, w=w) and M._check_norm(x, x, w)         # not on a GPU
 
 
+def test_workspace_size():
+    import gated_delta_rule_63_amd as kda
+    for shape, dtype in (((3, 256), torch.float32), ((2, 5, 7), torch.bfloat16), ((4000, 4096), torch.bfloat16), ((0, 64), torch.float32), ((9,), torch.float32)):
+        dy = torch.empty(shape, dtype=dtype)
+        d = kda._lib.NormDesc(dy.numel() // shape[-1], shape[-1], 0, 0, None, 0)
+        need = kda.add_norm_bwd_workspace_size(dy)
+        assert need == kda.lib().kda_add_norm_bwd_workspace_size(ctypes.byref(d)) and (need > 0) == (dy.numel() > 0)
+    for bad in (torch.tensor(1.0), torch.empty(3, 0)):
+        with pytest.raises(ValueError):
+            kda.add_norm_bwd_workspace_size(bad)
+
+
 def test_outputs_in_the_place_of_inputs():
     """An output exactly where an input lies, or apart from all of them and from the other one."""
     from gated_delta_rule_63_amd import _layers as M
@@ -380,3 +392,17 @@ def test_in_place_without_a_residual(kda):
         kda.add_norm_bwd(lost, w, dy)
     with pytest.raises(ValueError):
         kda.add_norm(x, x, w, out=xi, residual_out=xi)
+
+
+@pytest.mark.gpu
+def test_given_workspace(kda):
+    """Of the size that is asked for; a byte less is refused."""
+    x, r0, w, dy, dr = (t.cuda() for t in make(70, 640, "bfloat16", "float32", 10))
+    want = kda.add_norm_bwd(r0, w, dy, dr=dr)
+    need = kda.add_norm_bwd_workspace_size(dy)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert all(torch.equal(a, b) for a, b in zip(kda.add_norm_bwd(r0, w, dy, dr=dr, workspace=ws), want))
+    with pytest.raises(kda.KDAError):
+        kda.add_norm_bwd(r0, w, dy, dr=dr, workspace=ws[:need - 1])
+    with pytest.raises(ValueError):
+        kda.add_norm_bwd(r0, w, dy, dr=dr, workspace=ws.cpu())
