@@ -21,6 +21,13 @@ def _plain(name, t, shape, dtype, device, _device=True):
         _rows(name, t, shape, dtype, device, _device)
 
 
+def _sizes(*n):
+    """Sizes as the descriptors' 32-bit fields hold them (ctypes would cut them off silently)."""
+    if max(n) > 0x7fffffff:
+        raise ValueError("a dimension is beyond 32 bits")
+    return n
+
+
 def _span(t):
     at = t.data_ptr()
     return at, at + t.numel() * t.element_size()
@@ -54,7 +61,8 @@ def _with(desc, ws: _Tensor):
 def _scan_desc(x, cu_seqlens, leaky=False) -> ScanDesc:
     shape = x.shape
     N = shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    return ScanDesc(shape[0], shape[1], shape[2] if len(shape) == 3 else shape[2:].numel(), N, _DTYPES[x.dtype], leaky, None, 0)
+    sizes = _sizes(shape[0], shape[1], shape[2] if len(shape) == 3 else shape[2:].numel(), N)
+    return ScanDesc(*sizes, _DTYPES[x.dtype], leaky, None, 0)
 
 
 def _scan_state(d: ScanDesc, x) -> torch.Size:
@@ -181,6 +189,7 @@ def _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, leaky=F
     device = x.device
     if pool.shape[1:] != x.shape[2:] or not pool.is_contiguous() or pool.dtype not in _DTYPES or pool.device != device:
         raise ValueError(f"pool must be a contiguous float32 or bfloat16 [P, {', '.join(map(str, x.shape[2:]))}] tensor on x's device")
+    _sizes(pool.shape[0])
     if slots is None and pool.shape[0] < d.num_seqs:
         raise ValueError("pool has fewer slots than there are sequences")
     for name, t, n in (("slots", slots, d.num_seqs), ("out_slots", out_slots, d.B * d.T)):
@@ -204,7 +213,7 @@ def _check_norm(x, residual, weight, _device=True) -> NormDesc:
         if res != dtype and res != torch.float32:
             raise ValueError("residual must have x's dtype or be float32")
         _rows("residual", residual, shape, res, device, False)
-    return NormDesc(x.numel() // C, C, _DTYPES[dtype], _DTYPES[res], None, 0)
+    return NormDesc(x.numel() // C, *_sizes(C), _DTYPES[dtype], _DTYPES[res], None, 0)
 
 
 def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: float = 1e-5, out: _Tensor = None,
@@ -285,7 +294,7 @@ def add_norm_bwd_workspace_size(dy: torch.Tensor) -> int:
     if dy.dim() < 1 or dy.shape[-1] < 1:
         raise ValueError("dy must be a [..., C] tensor")
     C = dy.shape[-1]
-    return int(lib().kda_add_norm_bwd_workspace_size(ctypes.byref(NormDesc(dy.numel() // C, C, KDA_F32, KDA_F32, None, 0))))
+    return int(lib().kda_add_norm_bwd_workspace_size(ctypes.byref(NormDesc(dy.numel() // C, *_sizes(C), KDA_F32, KDA_F32, None, 0))))
 
 
 def _check_norm_bwd(r, weight, dy, dr, _device=True) -> NormDesc:
@@ -314,7 +323,7 @@ def _check_beam(logits, scores, k, done, eos, _device=True) -> BeamDesc:
     k = W if k is None else k
     if not (1 <= W <= 64 and 1 <= k <= 64):
         raise ValueError("beams and k must be 1 to 64")
-    return BeamDesc(B, W, V, k, _DTYPES[logits.dtype], eos, None, 0)
+    return BeamDesc(*_sizes(B, W, V), k, _DTYPES[logits.dtype], eos, None, 0)
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = None, done: _Tensor = None, eos: int = -1,
@@ -341,7 +350,7 @@ def beam_workspace_size(logits: torch.Tensor, k: Optional[int] = None) -> int:
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
     B, W, V = logits.shape
-    d = BeamDesc(B, W, V, W if k is None else k, _DTYPES.get(logits.dtype, -1), -1, None, 0)
+    d = BeamDesc(*_sizes(B, W, V, W if k is None else k), _DTYPES.get(logits.dtype, -1), -1, None, 0)
     return int(lib().kda_beam_workspace_size(ctypes.byref(d)))
 
 
@@ -350,6 +359,7 @@ def _check_reorder(pool, slots, parents, out, _device=True):
         raise ValueError("pool must be a contiguous device tensor [P, ...]")
     if slots.dim() != 2 or not 1 <= slots.shape[1] <= 64:
         raise ValueError("slots must be [B, W] with 1 to 64 beams")
+    _sizes(pool.shape[0], slots.shape[0])
     for name, t in (("slots", slots), ("parents", parents), ("out", out)):
         _plain(name, t, slots.shape, torch.int32, pool.device, _device)
     if out is not None and out.data_ptr() in (slots.data_ptr(), parents.data_ptr()) and out.numel():

@@ -80,6 +80,22 @@ def test_workspace_size():
         kda.beam_workspace_size(torch.empty(6, 50))
 
 
+def test_sizes_beyond_32_bits():
+    """2^32 + 3 of anything is refused, not taken for 3. (Tensors without storage.)"""
+    from gated_delta_rule_63_amd import _layers as M
+    n = (1 << 32) + 3
+    e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")
+    for B, W, V in ((1, 1, n), (n, 1, 1)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M._check_beam(e(B, W, V), e(B, W), 1, None, -1, _device=False)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.beam_workspace_size(e(B, W, V))
+    i = lambda *s: e(*s, dtype=torch.int32)
+    for pool, slots in ((e(n, 1), i(2, 3)), (e(9, 1), i(n, 1))):
+        with pytest.raises(ValueError, match="32 bits"):
+            M._check_reorder(pool, slots, slots, None, _device=False)
+
+
 # ------------------------------------------------------------------------- GPU
 
 @pytest.fixture

@@ -150,6 +150,17 @@ def test_outputs_in_the_place_of_inputs():
         M._check_norm_bwd(None, w, x, None, _device=False)
 
 
+def test_sizes_beyond_32_bits():
+    """Rows of 2^32 + 8 channels are refused, not taken for 8. (Tensors without storage.)"""
+    from gated_delta_rule_63_amd import _layers as M
+    e = lambda *s: torch.empty(*s, device="meta")
+    n = (1 << 32) + 8
+    with pytest.raises(ValueError, match="32 bits"):
+        M._check_norm(e(1, n), None, e(n), _device=False)
+    with pytest.raises(ValueError, match="32 bits"):
+        M.add_norm_bwd_workspace_size(e(1, n))
+
+
 # ------------------------------------------------------------------------- GPU
 
 @pytest.fixture

@@ -91,6 +91,22 @@ def test_binding_refusals():
             rec(**kw)
 
 
+def test_sizes_beyond_32_bits():
+    """2^32 + 3 of anything is refused, not taken for 3. (Tensors without storage: only shapes are looked at.)"""
+    from gated_delta_rule_63_amd import _layers as M
+    n = (1 << 32) + 3
+    e = lambda *s, dtype=torch.float32: torch.empty(*s, dtype=dtype, device="meta")
+    for shape in ((1, n, 1), (n, 1, 1), (1, 1, n), (1, 1, 1 << 20, 1 << 13)):
+        with pytest.raises(ValueError, match="32 bits"):
+            M._check_scan(e(*shape), e(*shape), None, _device=False)
+        with pytest.raises(ValueError, match="32 bits"):
+            M.scan_workspace_size(e(*shape))
+    with pytest.raises(ValueError, match="32 bits"):
+        M._check_scan(e(1, 3, 1), e(1, 3, 1), e(n, dtype=torch.int32), _device=False)
+    with pytest.raises(ValueError, match="32 bits"):
+        M._check_scan_recurrent(e(2, 1, 1), e(2, 1, 1), e(n, 1), e(2, dtype=torch.int32), None, None, None, _device=False)
+
+
 # ------------------------------------------------------------------------- GPU
 
 @pytest.fixture
