@@ -362,8 +362,7 @@ def _check_reorder(pool, slots, parents, out, _device=True):
     _sizes(pool.shape[0], slots.shape[0])
     for name, t in (("slots", slots), ("parents", parents), ("out", out)):
         _plain(name, t, slots.shape, torch.int32, pool.device, _device)
-    if out is not None and out.data_ptr() in (slots.data_ptr(), parents.data_ptr()) and out.numel():
-        raise ValueError("out may not be slots or parents")
+    _place("out", out, (), (slots, parents))
 
 
 def beam_reorder(pool: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor, out: _Tensor = None,
@@ -374,7 +373,7 @@ def beam_reorder(pool: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor,
     first child keeps its slot, further ones get copies in the slots of beams without children
     (the same slots in each entry, and the same result for every pool of a model). A parent
     outside [0, W) is an empty place: it gets a free slot, whose state is left as it is. out may
-    not be slots or parents."""
+    not overlap slots or parents."""
     _check_reorder(pool, slots, parents, out)
     with _on(pool.device, stream) as s:
         new = torch.empty_like(slots) if out is None else out

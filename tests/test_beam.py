@@ -80,6 +80,23 @@ def test_workspace_size():
         kda.beam_workspace_size(torch.empty(6, 50))
 
 
+def test_new_slots_apart_from_the_inputs():
+    """Slots of new beams that overlap an input, in part or as a whole, are refused: other workgroups still read it."""
+    from gated_delta_rule_63_amd import _layers as M
+    flat, other, pool = torch.zeros(12, dtype=torch.int32), torch.zeros(2, 3, dtype=torch.int32), torch.zeros(9, 4)
+    part = lambda i: flat[i:i + 6].view(2, 3)
+    re = lambda s, p, out: M._check_reorder(pool, s, p, out, _device=False)
+    re(part(0), other, part(6))
+    re(other, part(6), part(0))
+    for at in (0, 1, 5):
+        with pytest.raises(ValueError):
+            re(part(at), other, part(0))
+        with pytest.raises(ValueError):
+            re(other, part(0), part(at))
+    empty = torch.zeros(0, 3, dtype=torch.int32)
+    re(empty, empty, empty)
+
+
 def test_sizes_beyond_32_bits():
     """2^32 + 3 of anything is refused, not taken for 3. (Tensors without storage.)"""
     from gated_delta_rule_63_amd import _layers as M
