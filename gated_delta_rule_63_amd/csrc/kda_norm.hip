@@ -55,7 +55,7 @@ struct Place {
     __device__ __forceinline__ int col(int u) const { return (u * lanes + lane) * V; }
     __device__ __forceinline__ int off(int u, int size) const {
         if constexpr (R == 1) return col(u) * size;
-        else return col(u) < C ? (sub * C + col(u)) * size : INT32_MAX;
+        else return col(u) < C ? (sub * C + col(u)) * size : 1 << 30;   // (pieces of it are added)
     }
     __device__ __forceinline__ __amdgpu_buffer_rsrc_t row(const void* p, int size) const {
         return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(static_cast<const char*>(p)) + at * size, (short)0, rows * C * size, 0x00020000);
