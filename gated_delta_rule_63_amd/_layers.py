@@ -28,22 +28,9 @@ def _sizes(*n):
     return n
 
 
-def _span(t):
-    at = t.data_ptr()
-    return at, at + t.numel() * t.element_size()
-
-
-def _place(name, out, inputs=(), others=()):
-    """An output may lie exactly where one of `inputs` does; otherwise it overlaps none of them, nor of `others`."""
-    if out is None:
-        return
-    a0, a1 = _span(out)
-    for other, same in [(t, True) for t in inputs] + [(t, False) for t in others]:
-        if other is None or other is out and same:
-            continue
-        b0, b1 = _span(other)
-        if a0 < b1 and b0 < a1 and not (same and (a0, a1) == (b0, b1)):
-            raise ValueError(f"{name} may not overlap another argument of the call")
+def _meets(p, n, q, m):
+    """Whether n bytes from p on and m bytes from q on overlap."""
+    return p < q + m and q < p + n
 
 
 def _bytes(n: int, like: torch.Tensor) -> _Tensor:
@@ -117,8 +104,11 @@ def scan(x: torch.Tensor, g: torch.Tensor, cu_seqlens: _Tensor = None, initial_s
     in fp32, and with output_chunk_states the states that enter each chunk of 128 tokens,
     which scan_bwd() takes ([B, ceil(T / 128), ...]; packed [1, T // 128 + N, ...], where
     sequence n's begin at row cu[n] // 128 + n and rows without a chunk are unset), else
-    None. out may be x, final_state initial_state. workspace: an optional device tensor of scan_workspace_size() bytes,
-    used by one call at a time; allocated otherwise."""
+    None. Rows of y of tokens that belong to no sequence are left as they were: unset without
+    out. Gates above 0 make a state grow: gates of 16 tokens in a row, or fewer, sum to 88 at
+    most where the state is not zero, and longer runs to anything that leaves every state
+    finite. out may be x, final_state initial_state. workspace: an optional device tensor of
+    scan_workspace_size() bytes, used by one call at a time; allocated otherwise."""
     d = _check_scan(x, g, cu_seqlens, leaky)
     state = _scan_state(d, x)
     _plain("initial_state", initial_state, state, torch.float32, x.device)
@@ -236,14 +226,32 @@ def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: floa
 
 
 def _check_norm_out(x, residual, weight, out, residual_out, _device=True):
+    """Outputs may lie exactly where x or residual does, and are apart from all else. (Straight on, since a
+    small call's time is the host's: 1.6 us in place, 4.1 with tensors of their own.)"""
+    if out is None and residual_out is None:
+        return
+    n, px, pw, m = x.nbytes, x.data_ptr(), weight.data_ptr(), 4 * x.shape[-1]
+    pr = nr = po = 0
+    if residual is not None:
+        pr, nr = residual.data_ptr(), n if residual.dtype == x.dtype else 2 * n
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
     if out is not None:
-        _rows("out", out, x.shape, x.dtype, x.device, _device)
-        _place("out", out, (x, residual), (weight, residual_out))
+        po = px
+        if out is not x:
+            _rows("out", out, x.shape, x.dtype, x.device, _device)
+            po = out.data_ptr()
+        if -n < po - px < n and po != px or -n < po - pr < nr and (po != pr or n != nr) or -n < po - pw < m:
+            raise ValueError("out overlaps an input and does not lie exactly in its place")
     if residual_out is not None:
-        if residual is None:
-            raise ValueError("residual_out needs a residual")
-        _rows("residual_out", residual_out, residual.shape, residual.dtype, residual.device, _device)
-        _place("residual_out", residual_out, (x, residual), (weight,))
+        ps = pr
+        if residual_out is not residual:
+            _rows("residual_out", residual_out, residual.shape, residual.dtype, residual.device, _device)
+            ps = residual_out.data_ptr()
+        if -nr < ps - px < n and (ps != px or n != nr) or -nr < ps - pr < nr and ps != pr or -nr < ps - pw < m:
+            raise ValueError("residual_out overlaps an input and does not lie exactly in its place")
+        if out is not None and -n < po - ps < nr:
+            raise ValueError("out and residual_out overlap")
 
 
 def _sum_out(x, residual, residual_out):
@@ -362,7 +370,8 @@ def _check_reorder(pool, slots, parents, out, _device=True):
     _sizes(pool.shape[0], slots.shape[0])
     for name, t in (("slots", slots), ("parents", parents), ("out", out)):
         _plain(name, t, slots.shape, torch.int32, pool.device, _device)
-    _place("out", out, (), (slots, parents))
+    if out is not None and any(_meets(out.data_ptr(), out.nbytes, t.data_ptr(), t.nbytes) for t in (slots, parents)):
+        raise ValueError("out may not overlap slots or parents")
 
 
 def beam_reorder(pool: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor, out: _Tensor = None,

@@ -587,7 +587,7 @@ size_t kda_add_norm_bwd_workspace_size(const kda_norm_desc_t* desc);
  *            token `eos` with its score as it is; its logits are not read.
  *     out_scores fp32, parents int32 (the beam), tokens int32, each [B, K]
  * A logit of -inf or NaN is no candidate and adds nothing to the sum; +inf counts
- * as the largest finite value. Places beyond the last candidate hold -inf, -1, -1.
+ * as fp32's largest finite value. Places beyond the last candidate hold -inf, -1, -1.
  * Totals are compared in fp64, formed from fp32 exponentials that are added in fp32
  * by 32 and in fp64 from there on, for any V: the total is off by at most
  * (2 d + 23) 2^-24, d the distance below the largest logit of those that make up the
