@@ -11,8 +11,8 @@
 // NaN and -inf give no key; +inf counts as the largest finite value.
 //
 // 64 x 8 beams, 131072 tokens in bf16 (134 MB), K = 16: 32 us for the rows, 4.1 TB/s read (a sum
-// by the library reads 4.0), 5 for the merge; 1 x 4 beams, 32000 tokens: 5.4 + 4.0 us,
-// launches and trips to memory. Reordering 16 x 4 beams of 2 MiB, 13 us, moves 5 TB/s.
+// by the library reads 4.0), 5.6 for the merge; 1 x 4 beams, 32000 tokens: 5.3 + 4.0 us,
+// launches and trips to memory. Reordering 16 x 4 beams of 2 MiB, 13 to 15 us, moves 5 TB/s.
 #include "kda_beam.h"
 #include "kda_device.h"
 
@@ -480,7 +480,7 @@ __global__ __launch_bounds__(TH) void kda_beam_merge(BeamArgs a) {
     int c = held;
     if (c > TH && c > 4 * a.K) {
         // Ranking takes c^2 reads: only those that a second bound leaves, of each thread's best, found
-        // as above (53 x 32 beams, K = 64: 55 -> 15 us; 3 x 16, 198533 tokens in bf16, many equal, K = 32: 201 -> 22)
+        // as above (the merge of 53 x 32 beams, K = 64: 55 -> 16 us; of 3 x 16, 198533 tokens in bf16, many equal, K = 32: 201 -> 22)
         Total top{0, kNone};
         for (int i = tid; i < c; i += TH) {
             const Total x{values[i], ats[i]};
@@ -591,7 +591,7 @@ hipError_t launch_beam_select(const BeamArgs& a, hipStream_t s) {
     const unsigned n = (unsigned)(a.B * a.W * a.splits);
     // A row that fits a wave's tile is one wave's work, and so is an entry with few keys (15386 x 8 x
     // 156 in fp32, K = 1: 560 -> 119 us; 540 x 16 x 423, K = 16: 49 -> 28), but many keys are ranked by
-    // more threads (53 x 32 x 1882, K = 64: 42 us, on a wave each 1.4 ms; 64 x 8 x 131072, K = 16, the
+    // more threads (53 x 32 x 1882, K = 64: a call 42 us, on a wave each 1.4 ms; 64 x 8 x 131072, K = 16, the
     // merge of 256 on a wave: 5 us more).
     const bool wave = a.K <= 16 && a.V <= (a.f32 ? kTile<true, 64> : kTile<false, 64>);
     const int most = shown_threads(a.K, wave ? 64 : kThreads);

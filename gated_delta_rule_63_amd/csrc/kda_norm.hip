@@ -9,10 +9,10 @@
 // Sums, norms and scales are fp32; a value is rounded where it is stored.
 //
 // Bound by memory: every tensor passes once, a row held in registers between its sum and
-// its result. 8192 x 4096, bf16 (268 MB): 42 us, 6.3 TB/s, part of it from the last-level cache;
-// 16384 x 4096 (537 MB): 82 us, in 8 bits 83, its gradient with dr 95; with an fp32 residual
-// (805 MB) 138 us, 5.8 TB/s; the gradient of 4004 x 8192 so (525 MB) 93 us, 5.7 TB/s, of which
-// the column sums take 6. A copy reaches 4.9 to 5.1 TB/s. 32 x 4096 in 8 bits is one trip to
+// its result. 8192 x 4096, bf16 (268 MB): 51 us, 5.3 TB/s, on other inputs each time, 43 where the last-level
+// cache holds part of them; 16384 x 4096 (537 MB): 83 us, in 8 bits 83, its gradient with dr 97; with an
+// fp32 residual (805 MB) 139 us, 5.8 TB/s; the gradient of 4004 x 8192 so (525 MB) 102 us, 5.2 TB/s, or 93, of
+// which the column sums take 5. A copy reaches 4.9 to 5.1 TB/s. 32 x 4096 in 8 bits is one trip to
 // memory and a launch: 4 us.
 //
 // Fetching a workgroup's next row ahead costs registers, so waves, and gave nothing (8192 x
@@ -283,7 +283,8 @@ __global__ __launch_bounds__(1024) void kda_add_norm_kernel(NormArgs a, int wpr)
 }
 
 // dweight's sum over a workgroup's rows stays in registers, and goes to its row of the
-// workspace.
+// workspace. (In bf16 beyond 8192 channels, pieces of one or two spill 13 or 3 registers under the bound
+// of 128 that a workgroup of 16 waves sets.)
 template <bool F32, bool RF32, int LANES, int E, int V, int PAST>
 __global__ __launch_bounds__(1024) void kda_add_norm_bwd_kernel(NormArgs a, int wpr) {
     constexpr int LD = PAST > 0 ? kPast : 0, ST = PAST > 1 ? kPast : 0;

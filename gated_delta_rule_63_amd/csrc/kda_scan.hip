@@ -16,7 +16,7 @@
 // Few chains leave most of the chip idle, so their chunks run side by side and the inputs
 // pass twice, the second time in part from the last-level cache (131072 x 512, 0.54 GB:
 // 165 us; packed lengths of 271 to 3063, 8192 x 1000, leaky, fp32, the gradient without states,
-// 164 MB: 55 us, 22 + 33 in its two kernels).
+// 164 MB: 62 us on other inputs each time, 52 on the same; 21 + 34 in its two kernels).
 #include "kda_device.h"
 #include "kda_scan.h"
 
@@ -635,7 +635,7 @@ __global__ __launch_bounds__(64 * W) void kda_scan_chunks(ScanArgs a) {
 }
 
 // (4 waves a SIMD: the leaky form in bf16 would keep one workgroup a compute unit; 131072 x 512: 239
-// -> 219 us, 8192 x 1024: 37 -> 31)
+// -> 219 us, 8192 x 1024: 37 -> 31, though it spills six registers with the fold, two without)
 template <bool F32, bool LEAKY, bool FOLD, bool STREAM>
 __global__ __launch_bounds__(64 * W, 4) void kda_scan_chunks_bwd(ScanArgs a, bool known) {
     constexpr int ST = STREAM ? kPast : 0;
