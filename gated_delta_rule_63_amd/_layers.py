@@ -21,16 +21,12 @@ def _plain(name, t, shape, dtype, device, _device=True):
         _rows(name, t, shape, dtype, device, _device)
 
 
-def _sizes(*n):
-    """Sizes as the descriptors' 32-bit fields hold them (ctypes would cut them off silently)."""
-    if max(n) > 0x7fffffff:
+_MOST = 0x7fffffff                    # of the descriptors' 32-bit fields: ctypes would cut off silently
+
+
+def _fits(*n):
+    if max(n) > _MOST:
         raise ValueError("a dimension is beyond 32 bits")
-    return n
-
-
-def _meets(p, n, q, m):
-    """Whether n bytes from p on and m bytes from q on overlap."""
-    return p < q + m and q < p + n
 
 
 def _bytes(n: int, like: torch.Tensor) -> _Tensor:
@@ -48,8 +44,10 @@ def _with(desc, ws: _Tensor):
 def _scan_desc(x, cu_seqlens, leaky=False) -> ScanDesc:
     shape = x.shape
     N = shape[0] if cu_seqlens is None else cu_seqlens.numel() - 1
-    sizes = _sizes(shape[0], shape[1], shape[2] if len(shape) == 3 else shape[2:].numel(), N)
-    return ScanDesc(*sizes, _DTYPES[x.dtype], leaky, None, 0)
+    C = shape[2] if len(shape) == 3 else shape[2:].numel()
+    if not 0 < x.numel() <= _MOST or N > _MOST:       # (no dimension is larger than all elements, if there are any)
+        _fits(shape[0], shape[1], C, N)
+    return ScanDesc(shape[0], shape[1], C, N, _DTYPES[x.dtype], leaky, None, 0)
 
 
 def _scan_state(d: ScanDesc, x) -> torch.Size:
@@ -176,11 +174,12 @@ def scan_recurrent(x: torch.Tensor, g: torch.Tensor, pool: torch.Tensor, slots: 
 
 def _check_scan_recurrent(x, g, pool, slots, out_slots, cu_seqlens, out, leaky=False, _device=True) -> ScanDesc:
     d = _check_scan(x, g, cu_seqlens, leaky, _device)
-    device = x.device
-    if pool.shape[1:] != x.shape[2:] or not pool.is_contiguous() or pool.dtype not in _DTYPES or pool.device != device:
+    device, shape = x.device, pool.shape
+    if shape[1:] != x.shape[2:] or not pool.is_contiguous() or pool.dtype not in _DTYPES or pool.device != device:
         raise ValueError(f"pool must be a contiguous float32 or bfloat16 [P, {', '.join(map(str, x.shape[2:]))}] tensor on x's device")
-    _sizes(pool.shape[0])
-    if slots is None and pool.shape[0] < d.num_seqs:
+    if shape[0] > _MOST:
+        _fits(shape[0])
+    if slots is None and shape[0] < d.num_seqs:
         raise ValueError("pool has fewer slots than there are sequences")
     for name, t, n in (("slots", slots, d.num_seqs), ("out_slots", out_slots, d.B * d.T)):
         if t is not None and (t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != device):
@@ -203,7 +202,9 @@ def _check_norm(x, residual, weight, _device=True) -> NormDesc:
         if res != dtype and res != torch.float32:
             raise ValueError("residual must have x's dtype or be float32")
         _rows("residual", residual, shape, res, device, False)
-    return NormDesc(x.numel() // C, *_sizes(C), _DTYPES[dtype], _DTYPES[res], None, 0)
+    if C > _MOST:
+        _fits(C)
+    return NormDesc(x.numel() // C, C, _DTYPES[dtype], _DTYPES[res], None, 0)
 
 
 def add_norm(x: torch.Tensor, residual: _Tensor, weight: torch.Tensor, eps: float = 1e-5, out: _Tensor = None,
@@ -302,7 +303,8 @@ def add_norm_bwd_workspace_size(dy: torch.Tensor) -> int:
     if dy.dim() < 1 or dy.shape[-1] < 1:
         raise ValueError("dy must be a [..., C] tensor")
     C = dy.shape[-1]
-    return int(lib().kda_add_norm_bwd_workspace_size(ctypes.byref(NormDesc(dy.numel() // C, *_sizes(C), KDA_F32, KDA_F32, None, 0))))
+    _fits(C)
+    return int(lib().kda_add_norm_bwd_workspace_size(ctypes.byref(NormDesc(dy.numel() // C, C, KDA_F32, KDA_F32, None, 0))))
 
 
 def _check_norm_bwd(r, weight, dy, dr, _device=True) -> NormDesc:
@@ -331,7 +333,9 @@ def _check_beam(logits, scores, k, done, eos, _device=True) -> BeamDesc:
     k = W if k is None else k
     if not (1 <= W <= 64 and 1 <= k <= 64):
         raise ValueError("beams and k must be 1 to 64")
-    return BeamDesc(*_sizes(B, W, V), k, _DTYPES[logits.dtype], eos, None, 0)
+    if not 0 < logits.numel() <= _MOST:
+        _fits(B, V)
+    return BeamDesc(B, W, V, k, _DTYPES[logits.dtype], eos, None, 0)
 
 
 def beam_select(logits: torch.Tensor, scores: torch.Tensor, k: Optional[int] = None, done: _Tensor = None, eos: int = -1,
@@ -358,7 +362,9 @@ def beam_workspace_size(logits: torch.Tensor, k: Optional[int] = None) -> int:
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
     B, W, V = logits.shape
-    d = BeamDesc(*_sizes(B, W, V, W if k is None else k), _DTYPES.get(logits.dtype, -1), -1, None, 0)
+    k = W if k is None else k
+    _fits(B, W, V, k)
+    d = BeamDesc(B, W, V, k, _DTYPES.get(logits.dtype, -1), -1, None, 0)
     return int(lib().kda_beam_workspace_size(ctypes.byref(d)))
 
 
@@ -367,11 +373,14 @@ def _check_reorder(pool, slots, parents, out, _device=True):
         raise ValueError("pool must be a contiguous device tensor [P, ...]")
     if slots.dim() != 2 or not 1 <= slots.shape[1] <= 64:
         raise ValueError("slots must be [B, W] with 1 to 64 beams")
-    _sizes(pool.shape[0], slots.shape[0])
+    if pool.shape[0] > _MOST or slots.shape[0] > _MOST:
+        _fits(pool.shape[0], slots.shape[0])
     for name, t in (("slots", slots), ("parents", parents), ("out", out)):
         _plain(name, t, slots.shape, torch.int32, pool.device, _device)
-    if out is not None and any(_meets(out.data_ptr(), out.nbytes, t.data_ptr(), t.nbytes) for t in (slots, parents)):
-        raise ValueError("out may not overlap slots or parents")
+    if out is not None:
+        n, at = out.nbytes, out.data_ptr()                # three tensors of one size
+        if -n < at - slots.data_ptr() < n or -n < at - parents.data_ptr() < n:
+            raise ValueError("out may not overlap slots or parents")
 
 
 def beam_reorder(pool: torch.Tensor, slots: torch.Tensor, parents: torch.Tensor, out: _Tensor = None,
